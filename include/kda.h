@@ -409,6 +409,164 @@ int kda_commit_snapshot(const int32_t *accepted_len, const int32_t *state_slots,
                         const float *snapshots, int32_t max_T,
                         kda_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Selective state space layers: the other recurrent layers that hybrid models
+ * keep in the same slots.  A layer is a short causal convolution over its
+ * channels and a selective scan; both carry a state per sequence, both have a
+ * form for prompts (packed ragged segments, checkpoints at cache-block
+ * boundaries) and one for steps of one or a few tokens.  (No counterpart on
+ * the pages; the conventions above hold, with these differences.)
+ *   - Token tensors are rows of one token each with a row stride in elements
+ *     (views into a wider projection are taken as they are); the channels of
+ *     a row are contiguous.  They need the alignment of their element only,
+ *     but rows that all start on 16 bytes, with channels (and channels /
+ *     groups) a multiple of 16 bytes, run a faster variant.  Per-channel
+ *     parameters and pools are contiguous and 16-byte aligned.
+ *   - Outputs have the inputs' dtype, rounded once from fp32, and must not
+ *     overlap any input.
+ *   - The slots of one call must be distinct, checkpoint slots included.
+ */
+
+/* One packed batch of the convolution. */
+typedef struct {
+  kda_dtype dtype;           /* dtype of x, y, weight, bias                  */
+  const void *x;             /* [N] rows of D channels                       */
+  void *y;                   /* [N] rows of D channels                       */
+  int64_t x_stride, y_stride; /* elements between rows, >= D                 */
+  const void *weight;        /* [D][W], tap W - 1 on the current token       */
+  const void *bias;          /* [D] or NULL                                  */
+  const int32_t *cu_seqlens; /* [B + 1] device; steps: NULL = one token a row */
+  int32_t num_seqs;          /* B                                            */
+  int32_t num_tokens;        /* N                                            */
+  int32_t channels;          /* D                                            */
+  int32_t width;             /* W in {2, 3, 4}                               */
+  int32_t silu;              /* != 0: y = u * sigmoid(u), else y = u         */
+} kda_conv_tokens;
+
+/* Convolution states [num_slots][W - 1][D]: a slot's last W - 1 inputs, the
+ * oldest first, in the tokens' dtype; zero = no history. */
+typedef struct {
+  void *base;
+  kda_dtype dtype;
+  int32_t num_slots, channels, width;
+} kda_conv_pool;
+
+/* One packed batch of the selective scan. */
+typedef struct {
+  kda_dtype dtype;           /* dtype of x, dt, z, B, C, y                   */
+  const void *x, *dt;        /* [N] rows of D channels                       */
+  const void *z;             /* [N] rows of D channels, or NULL: no gate     */
+  const void *B, *C;         /* [N] rows of [G][S], contiguous in a row      */
+  void *y;                   /* [N] rows of D channels                       */
+  int64_t x_stride, dt_stride, z_stride, b_stride, c_stride, y_stride;
+  const float *A;            /* [D][S] fp32                                  */
+  const float *D;            /* [D] fp32 or NULL: no skip                    */
+  const float *dt_bias;      /* [D] fp32 or NULL                             */
+  const int32_t *cu_seqlens; /* [B + 1] device; steps: NULL = one token a row */
+  int32_t num_seqs;          /* B                                            */
+  int32_t num_tokens;        /* N                                            */
+  int32_t channels;          /* D, a multiple of G                           */
+  int32_t state;             /* S in {16, 32, 64, 128}                       */
+  int32_t groups;            /* G: channel d reads B, C of group d / (D / G) */
+  int32_t dt_softplus;       /* != 0: delta = softplus(dt + dt_bias), else
+                                delta = dt + dt_bias                         */
+} kda_scan_tokens;
+
+/* Scan states fp32 [num_slots][D][S]. */
+typedef struct {
+  float *base;
+  int32_t num_slots, channels, state;
+} kda_scan_pool;
+
+/*
+ * kda_conv_prefill -- causal depthwise convolution of packed prompts.
+ * With u = [the slot's W - 1 inputs; the segment's rows]:
+ *     y[t] = act(bias + sum_j weight[:, j] * u[t + j]),   j = 0 .. W - 1
+ * and the slot then holds the last W - 1 rows of u.  A segment of no tokens
+ * leaves its slot as it is.  Checkpoints as in kda_prefill_chunked: the
+ * state after absolute position (floor(p0 / ckpt_every) + m + 1) * ckpt_every
+ * goes to slot ckpt_slots[i * max_ckpt + m]; entries < 0 are skipped.
+ */
+int kda_conv_prefill(const kda_conv_tokens *tok, kda_conv_pool *pool,
+                     const int32_t *state_slots, const int32_t *ckpt_slots,
+                     int32_t max_ckpt, int32_t ckpt_every,
+                     const int32_t *start_pos, kda_stream_t stream);
+
+/*
+ * kda_conv_step -- the same for steps of one or a few tokens per row.
+ * commit_len (device [B], or NULL = all): y is computed for all T_i tokens of
+ * row i, the slot receives the state after the first commit_len[i] of them
+ * (0: it stays as it is).  So a speculative step passes the tokens accepted
+ * last time and the new drafts in one segment, and the accepted count as
+ * commit_len: a rejection needs no stored state.  commit_len outside
+ * [0, T_i] sets KDA_DERR_ACCEPT and skips the row.
+ */
+int kda_conv_step(const kda_conv_tokens *tok, kda_conv_pool *pool,
+                  const int32_t *state_slots, const int32_t *commit_len,
+                  kda_stream_t stream);
+
+/*
+ * kda_scan_prefill -- selective scan of packed prompts, from the slot's state
+ * h [D][S]; for each token, channel d with group g, and state n:
+ *     delta = softplus(dt[d] + dt_bias[d])
+ *     h[d][n] = exp(delta * A[d][n]) * h[d][n] + delta * x[d] * B[g][n]
+ *     y[d] = (sum_n C[g][n] * h[d][n] + D[d] * x[d]) * z[d] * sigmoid(z[d])
+ * The state, the sum over n and delta are fp32.  The slot receives the last
+ * state.  Checkpoints as above, with ckpt_every a multiple of 16.
+ * workspace: kda_scan_workspace_size(...) bytes, 256-byte aligned, owned by
+ * the caller and not used by another call until this one completes; with it
+ * long segments are split into parts that run at the same time.  NULL: every
+ * segment is walked by itself.  Both meet the same tolerances; they are not
+ * bit-identical to each other.
+ */
+int kda_scan_prefill(const kda_scan_tokens *tok, kda_scan_pool *pool,
+                     const int32_t *state_slots, const int32_t *ckpt_slots,
+                     int32_t max_ckpt, int32_t ckpt_every,
+                     const int32_t *start_pos, void *workspace,
+                     size_t workspace_bytes, kda_stream_t stream);
+
+/* Bytes of workspace with which kda_scan_prefill splits long segments; 0 when
+ * it would not split at these sizes, and on bad arguments (which the prefill
+ * call itself rejects). */
+size_t kda_scan_workspace_size(int32_t num_tokens, int32_t num_seqs,
+                               int32_t channels, int32_t state, int32_t groups);
+
+/* kda_scan_step -- kda_scan_prefill's recurrence for steps of one or a few
+ * tokens per row, commit_len as in kda_conv_step. */
+int kda_scan_step(const kda_scan_tokens *tok, kda_scan_pool *pool,
+                  const int32_t *state_slots, const int32_t *commit_len,
+                  kda_stream_t stream);
+
+/* One array of per-slot data: a state pool, ring part or convolution pool of
+ * one layer; slot s is the slot_bytes bytes at base + s * slot_bytes. */
+typedef struct {
+  void *base;
+  size_t slot_bytes; /* a multiple of 4 */
+} kda_slot_array;
+
+/*
+ * kda_move_slots -- copy, fork, compact and free slots in all arrays of a
+ * model in one call (kda_copy_slots moves one fp32 pool's).
+ * For every i < n (src, dst device arrays) and every array:
+ *     src[i] >= 0:  slot dst[i] receives slot src[i]  (one src may serve many)
+ *     src[i] < 0:   slot dst[i] is zeroed             (freed, or made fresh)
+ *     dst[i] < 0:   nothing
+ * arrays is a HOST array of num_arrays <= 64 entries that all have num_slots
+ * slots.  The dst >= 0 must be distinct.  With a workspace of
+ * kda_move_workspace_size(...) bytes, 256-byte aligned, the moves act as if
+ * all at once: a slot may be the src of one and the dst of another.  With a
+ * NULL workspace src and dst must be disjoint.  An id that is not below
+ * num_slots sets KDA_DERR_SLOT and skips that move.
+ */
+int kda_move_slots(const kda_slot_array *arrays, int32_t num_arrays,
+                   int32_t num_slots, const int32_t *src, const int32_t *dst,
+                   int32_t n, void *workspace, size_t workspace_bytes,
+                   kda_stream_t stream);
+
+/* Bytes of workspace for kda_move_slots with n moves; 0 on bad arguments. */
+size_t kda_move_workspace_size(const kda_slot_array *arrays, int32_t num_arrays,
+                               int32_t n);
+
 /* kda_get_device_error -- synchronize `stream`, read the device error word
  * of the current device into *host_bits (host pointer), clear it, and return
  * KDA_EDEVICE if any bit was set, else KDA_OK. */

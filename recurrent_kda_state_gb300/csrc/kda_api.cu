@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "kda_internal.cuh"
+#include "kda_ssm.cuh"
 
 // Library-wide device error word (one per device that loads the library).
 __device__ unsigned int g_kda_device_error = 0;
@@ -131,6 +132,9 @@ kda::VerifyParams verify_params(const kda_state_pool *pool,
 }  // namespace
 
 namespace kda {
+unsigned int *error_word() { return device_error_word(); }
+bool device_refused() { return device_unsafe(); }
+
 int wait_limit_polls() {
   const int v = g_wait_limit.load();
   return v < 0 ? kDefaultWaitPolls : v;

@@ -1,0 +1,187 @@
+// Internal declarations of the state space layers' translation units: launch
+// parameter blocks, device helpers and the launchers that kda_ssm_api.cu calls
+// after validating the public arguments.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// Device address of the library's error word (nullptr: lookup failed), and
+// whether launches on the current device are refused (kda_api.cu).
+unsigned int *error_word();
+bool device_refused();
+
+// Segments of the packed batch and what becomes of their states.
+struct SegParams {
+  const int32_t *cu;          // [B + 1]; NULL: row i is token i
+  const int32_t *slots;       // [B]
+  const int32_t *commit;      // [B] or NULL (steps)
+  const int32_t *ckpt_slots;  // [B][max_ckpt] or NULL (prompts)
+  const int32_t *start_pos;   // [B] or NULL (prompts)
+  unsigned int *err;
+  int B, N, P, max_ckpt, ckpt_every;
+};
+
+struct ConvParams {
+  SegParams seg;
+  const void *x, *weight, *bias;
+  void *y, *pool;
+  long long xs, ys;  // row strides in elements
+  int D, W, silu;
+  int tile;  // prompts: tokens of a tile
+};
+
+struct ScanParams {
+  SegParams seg;
+  const void *x, *dt, *z, *B, *C;
+  void *y;
+  long long xs, dts, zs, bs, cs, ys;  // row strides in elements
+  const float *A, *D, *dtb;
+  float *pool;
+  float *ws;  // prompts: carried states of split segments, or NULL
+  int C_, S, G, softplus;
+  int part;  // prompts: tokens of a part, 0 = segments are not split
+};
+
+constexpr int kMaxSlotArrays = 64;
+struct MoveParams {
+  unsigned char *base[kMaxSlotArrays];
+  long long bytes[kMaxSlotArrays];   // of a slot
+  long long ws_off[kMaxSlotArrays];  // of the array in a move's staging area
+  int first[kMaxSlotArrays + 1];     // first chunk of the array
+  const int32_t *src, *dst;
+  unsigned char *ws;
+  long long ws_bytes;  // staging area of one move
+  unsigned int *err;
+  int L, n, P;
+};
+
+__host__ __device__ inline long long pad16(long long b) { return (b + 15) & ~15LL; }
+
+// A segment's rows and slot, checked against the batch and the pool; false
+// (and the error bit) if they are not sound.  keep: tokens that the stored
+// state takes in.
+struct SegLoc {
+  int begin, len, slot, keep;
+};
+__device__ __forceinline__ bool locate_segment(const SegParams &p, int i, SegLoc *s) {
+  int b = i, e = i + 1;
+  if (p.cu) {
+    b = p.cu[i];
+    e = p.cu[i + 1];
+  }
+  s->slot = p.slots[i];
+  if (b < 0 || e < b || e > p.N) {
+    set_error(p.err, KDA_DERR_SEGMENT);
+    return false;
+  }
+  if (s->slot < 0 || s->slot >= p.P) {
+    set_error(p.err, KDA_DERR_SLOT);
+    return false;
+  }
+  s->begin = b;
+  s->len = e - b;
+  s->keep = p.commit ? p.commit[i] : s->len;
+  if (s->keep < 0 || s->keep > s->len) {
+    set_error(p.err, KDA_DERR_ACCEPT);
+    return false;
+  }
+  return true;
+}
+
+// Checkpoint slot for the state after `local` tokens of segment i (absolute
+// position start_pos + local), or -1 if none is wanted there.
+__device__ __forceinline__ int checkpoint_slot(const SegParams &p, int i, long long p0,
+                                               long long local) {
+  const long long pos = p0 + local;
+  if (!p.ckpt_slots || local <= 0 || pos % p.ckpt_every != 0) return -1;
+  const long long m = pos / p.ckpt_every - p0 / p.ckpt_every - 1;
+  if (m < 0 || m >= p.max_ckpt) return -1;
+  const int slot = p.ckpt_slots[(long long)i * p.max_ckpt + m];
+  if (slot >= p.P) {
+    set_error(p.err, KDA_DERR_SLOT);
+    return -1;
+  }
+  return slot;
+}
+
+// 2^x and 1/x of the special function unit (2 ulp and 1 ulp).
+__device__ __forceinline__ float ex2f(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcpf(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// v * sigmoid(v).  Below about -88 the reciprocal of 1 + e^-v is 0, as is the
+// value in fp32; -inf gives NaN, as -inf / (1 + inf) does.
+__device__ __forceinline__ float silu_f(float v) { return v * rcpf(1.0f + ex2f(-kLog2e * v)); }
+
+// log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v| in (0, 1], with
+// log1p(u) = 2 artanh(s), s = u / (2 + u) <= 1/3, by its power series through
+// s^13 (the next term is below 2e-8 of the sum).  Relative, not only
+// absolute, accuracy matters: time steps of 1e-3 and less are ordinary.
+__device__ __forceinline__ float softplus_f(float v) {
+  const float u = ex2f(-kLog2e * fabsf(v));
+  const float s = u * rcpf(2.0f + u), q = s * s;
+  float r = 1.0f / 13.0f;
+  r = fmaf(r, q, 1.0f / 11.0f);
+  r = fmaf(r, q, 1.0f / 9.0f);
+  r = fmaf(r, q, 1.0f / 7.0f);
+  r = fmaf(r, q, 1.0f / 5.0f);
+  r = fmaf(r, q, 1.0f / 3.0f);
+  r = fmaf(r, q, 1.0f);
+  return fmaxf(v, 0.0f) + 2.0f * s * r;
+}
+
+template <typename T>
+__device__ __forceinline__ T out_scalar(float v);
+template <>
+__device__ __forceinline__ float out_scalar<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 out_scalar<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// V consecutive elements (V = 1: plain scalars; else one 16-byte vector).
+template <typename T, int V>
+__device__ __forceinline__ void load_elems(const T *p, float *dst) {
+  if constexpr (V == 1) dst[0] = in_scalar<T>(p);
+  else InVec<T>::load(p, dst);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_elems(T *p, const float *v) {
+  if constexpr (V == 1) {
+    *p = out_scalar<T>(v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+cudaError_t launch_conv(const ConvParams &p, kda_dtype dt, bool step, cudaStream_t s);
+cudaError_t launch_scan_prefill(const ScanParams &p, kda_dtype dt, cudaStream_t s);
+cudaError_t launch_scan_step(const ScanParams &p, kda_dtype dt, cudaStream_t s);
+cudaError_t launch_moves(const MoveParams &p, cudaStream_t s);
+
+// Chunks of kMoveChunk bytes that a slot of `bytes` is copied in.
+constexpr int kMoveChunk = 16384;
+inline long long move_chunks(long long bytes) { return (bytes + kMoveChunk - 1) / kMoveChunk; }
+
+// Workspace floats of the split scan (0: segments are not split).
+size_t scan_workspace_floats(int N, int B, int C, int S, int G);
+
+}  // namespace kda

@@ -22,6 +22,7 @@ KDA_F32, KDA_BF16 = 0, 1
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 
 
 class kda_tokens(ctypes.Structure):
@@ -41,11 +42,43 @@ class kda_replay_ring(ctypes.Structure):
                 ("ctrl", _P), ("depth", _I32), ("dtype", ctypes.c_int)]
 
 
+class kda_conv_tokens(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("x", _P), ("y", _P), ("x_stride", _I64),
+                ("y_stride", _I64), ("weight", _P), ("bias", _P), ("cu_seqlens", _P),
+                ("num_seqs", _I32), ("num_tokens", _I32), ("channels", _I32),
+                ("width", _I32), ("silu", _I32)]
+
+
+class kda_conv_pool(ctypes.Structure):
+    _fields_ = [("base", _P), ("dtype", ctypes.c_int), ("num_slots", _I32),
+                ("channels", _I32), ("width", _I32)]
+
+
+class kda_scan_tokens(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("x", _P), ("dt", _P), ("z", _P), ("B", _P),
+                ("C", _P), ("y", _P), ("x_stride", _I64), ("dt_stride", _I64),
+                ("z_stride", _I64), ("b_stride", _I64), ("c_stride", _I64),
+                ("y_stride", _I64), ("A", _P), ("D", _P), ("dt_bias", _P),
+                ("cu_seqlens", _P), ("num_seqs", _I32), ("num_tokens", _I32),
+                ("channels", _I32), ("state", _I32), ("groups", _I32),
+                ("dt_softplus", _I32)]
+
+
+class kda_scan_pool(ctypes.Structure):
+    _fields_ = [("base", _P), ("num_slots", _I32), ("channels", _I32), ("state", _I32)]
+
+
+class kda_slot_array(ctypes.Structure):
+    _fields_ = [("base", _P), ("slot_bytes", ctypes.c_size_t)]
+
+
 EXPORTS = ("kda_prefill_chunked", "kda_prefill_chunked_raw", "kda_prefill_chunked_noalloc",
            "kda_prefill_workspace_size", "kda_verify", "kda_verify_raw",
            "kda_commit", "kda_commit_layers", "kda_materialize", "kda_ring_reset",
            "kda_gather_states", "kda_copy_slots", "kda_verify_snapshot",
-           "kda_commit_snapshot", "kda_forward_mixed", "kda_get_device_error",
+           "kda_commit_snapshot", "kda_forward_mixed", "kda_conv_prefill", "kda_conv_step",
+           "kda_scan_prefill", "kda_scan_step", "kda_scan_workspace_size",
+           "kda_move_slots", "kda_move_workspace_size", "kda_get_device_error",
            "kda_set_wait_limit", "kda_status_string", "kda_version")
 
 _lib = None
@@ -81,6 +114,18 @@ def lib():
         L.kda_forward_mixed.argtypes = [tp, _I32, _I32, pp, _P, _P, _I32, _I32, _I32,
                                         _P, _P, ctypes.c_size_t, _I32, rp, _P, _P, _P]
         L.kda_commit_snapshot.argtypes = [_P, _P, _I32, pp, _P, _I32, _P]
+        ct, cp = ctypes.POINTER(kda_conv_tokens), ctypes.POINTER(kda_conv_pool)
+        st, sp = ctypes.POINTER(kda_scan_tokens), ctypes.POINTER(kda_scan_pool)
+        ap, size = ctypes.POINTER(kda_slot_array), ctypes.c_size_t
+        L.kda_conv_prefill.argtypes = [ct, cp, _P, _P, _I32, _I32, _P, _P]
+        L.kda_conv_step.argtypes = [ct, cp, _P, _P, _P]
+        L.kda_scan_prefill.argtypes = [st, sp, _P, _P, _I32, _I32, _P, _P, size, _P]
+        L.kda_scan_step.argtypes = [st, sp, _P, _P, _P]
+        L.kda_scan_workspace_size.argtypes = [_I32] * 5
+        L.kda_scan_workspace_size.restype = size
+        L.kda_move_slots.argtypes = [ap, _I32, _I32, _P, _P, _I32, _P, size, _P]
+        L.kda_move_workspace_size.argtypes = [ap, _I32, _I32]
+        L.kda_move_workspace_size.restype = size
         L.kda_get_device_error.argtypes = [ctypes.POINTER(_I32), _P]
         L.kda_set_wait_limit.argtypes = [_I32]
         L.kda_status_string.argtypes = [ctypes.c_int]
@@ -319,6 +364,229 @@ def kda_commit_snapshot(accepted_len, state_slots, pool, snapshots, stream=None)
                                      state_slots.numel(), ctypes.byref(pool.c),
                                      _ptr(snapshots), int(snapshots.shape[1]),
                                      _stream(stream)), "kda_commit_snapshot")
+
+
+def _row_view(t, dt, what):
+    """Row stride of a token tensor [N][...] whose rows are contiguous."""
+    if t.dtype != dt:
+        raise ValueError("%s is %s, the batch %s" % (what, t.dtype, dt))
+    inner = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != inner:
+            raise ValueError("the rows of %s are not contiguous" % what)
+        inner *= size
+    return t.stride(0) if t.shape[0] > 1 else inner
+
+
+def _same(what, got, want):
+    if tuple(got) != tuple(want):
+        raise ValueError("%s has shape %s, expected %s" % (what, tuple(got), tuple(want)))
+
+
+def _param(t, shape, dt, what):
+    if t is not None:
+        _same(what, t.shape, shape)
+        if t.dtype != dt or not t.is_contiguous():
+            raise ValueError("%s must be contiguous %s" % (what, dt))
+    return None if t is None else t.data_ptr()
+
+
+def _cu(cu_seqlens, N):
+    """Pointer and segments of cu_seqlens; None: one token a row (steps)."""
+    if cu_seqlens is None:
+        return None, N
+    if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous int32")
+    return cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
+
+
+def _table(t, n, what):
+    """Pointer of an int32 device table of n entries (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
+        raise ValueError("%s must be contiguous int32 with %d entries" % (what, n))
+    return t.data_ptr()
+
+
+class ConvPool:
+    """Convolution states [num_slots][W - 1][D]: each slot's last W - 1 inputs."""
+
+    def __init__(self, data):
+        if data.dim() != 3 or not data.is_contiguous():
+            raise ValueError("a convolution pool is a contiguous [num_slots][W - 1][D]")
+        self.data = data
+        P, taps, D = data.shape
+        self.c = kda_conv_pool(data.data_ptr(), _dtype_code(data.dtype), P, D, taps + 1)
+        self.ref = ctypes.byref(self.c)
+
+    @classmethod
+    def zeros(cls, num_slots, width, D, dtype, device="cuda"):
+        return cls(torch.zeros(num_slots, width - 1, D, dtype=dtype, device=device))
+
+
+class ConvBatch:
+    """Packed rows x [N][D] (a row stride is fine), weight [D][W], bias [D] or
+    None, outputs y [N][D]; cu_seqlens [B + 1] int32, or None for steps of one
+    token a row; activation None or "silu"."""
+
+    def __init__(self, x, weight, bias=None, cu_seqlens=None, activation="silu", y=None):
+        if activation not in (None, "silu"):
+            raise ValueError("activation must be None or 'silu'")
+        N, D = x.shape
+        dt = x.dtype
+        self.x, self.weight, self.bias, self.cu_seqlens = x, weight, bias, cu_seqlens
+        self.y = y if y is not None else torch.empty(N, D, dtype=dt, device=x.device)
+        _same("y", self.y.shape, (N, D))
+        W = weight.shape[1]
+        cu, B = _cu(cu_seqlens, N)
+        self.c = kda_conv_tokens(
+            _dtype_code(dt), x.data_ptr(), self.y.data_ptr(), _row_view(x, dt, "x"),
+            _row_view(self.y, dt, "y"), _param(weight, (D, W), dt, "weight"),
+            _param(bias, (D,), dt, "bias"), cu, B, N, D, W, 1 if activation else 0)
+        self.ref = ctypes.byref(self.c)
+
+
+class ScanPool:
+    """Scan states fp32 [num_slots][D][S]."""
+
+    def __init__(self, data):
+        if data.dtype != torch.float32 or data.dim() != 3 or not data.is_contiguous():
+            raise ValueError("a scan pool is a contiguous fp32 [num_slots][D][S]")
+        self.data = data
+        self.c = kda_scan_pool(data.data_ptr(), *data.shape)
+        self.ref = ctypes.byref(self.c)
+
+    @classmethod
+    def zeros(cls, num_slots, D, S, device="cuda"):
+        return cls(torch.zeros(num_slots, D, S, dtype=torch.float32, device=device))
+
+
+class ScanBatch:
+    """Packed rows x, dt, z [N][D] and B, C [N][G][S] (row strides are fine),
+    fp32 A [D][S], D [D], dt_bias [D], outputs y [N][D]; D, z, dt_bias may be
+    None; cu_seqlens [B + 1] int32, or None for steps of one token a row."""
+
+    def __init__(self, x, dt, A, B, C, D=None, z=None, dt_bias=None, cu_seqlens=None,
+                 dt_softplus=True, y=None):
+        N, Dm = x.shape
+        _, G, S = B.shape
+        ty, f32 = x.dtype, torch.float32
+        self.x, self.dt, self.A, self.B, self.C = x, dt, A, B, C
+        self.D, self.z, self.dt_bias, self.cu_seqlens = D, z, dt_bias, cu_seqlens
+        self.y = y if y is not None else torch.empty(N, Dm, dtype=ty, device=x.device)
+        for t, shape, what in ((dt, (N, Dm), "dt"), (z, (N, Dm), "z"), (B, (N, G, S), "B"),
+                               (C, (N, G, S), "C"), (self.y, (N, Dm), "y")):
+            if t is not None:
+                _same(what, t.shape, shape)
+        cu, nseq = _cu(cu_seqlens, N)
+        self.c = kda_scan_tokens(
+            _dtype_code(ty), x.data_ptr(), dt.data_ptr(),
+            None if z is None else z.data_ptr(), B.data_ptr(), C.data_ptr(),
+            self.y.data_ptr(), _row_view(x, ty, "x"), _row_view(dt, ty, "dt"),
+            0 if z is None else _row_view(z, ty, "z"), _row_view(B, ty, "B"),
+            _row_view(C, ty, "C"), _row_view(self.y, ty, "y"), _param(A, (Dm, S), f32, "A"),
+            _param(D, (Dm,), f32, "D"), _param(dt_bias, (Dm,), f32, "dt_bias"), cu, nseq,
+            N, Dm, S, G, 1 if dt_softplus else 0)
+        self.ref = ctypes.byref(self.c)
+
+
+def _ckpt(ckpt_slots, B):
+    if ckpt_slots is None:
+        return None, 0
+    if ckpt_slots.dim() != 2:
+        raise ValueError("ckpt_slots is [B][max_ckpt]")
+    n = int(ckpt_slots.shape[1])
+    return _table(ckpt_slots, B * n, "ckpt_slots"), n
+
+
+def kda_conv_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, start_pos=None,
+                     stream=None):
+    """Causal convolution of packed prompts; ckpt_slots [B][max_ckpt] int32."""
+    B = tok.c.num_seqs
+    ckpt, max_ckpt = _ckpt(ckpt_slots, B)
+    _check(lib().kda_conv_prefill(
+        tok.ref, pool.ref, _table(state_slots, B, "state_slots"), ckpt, max_ckpt, ckpt_every,
+        _table(start_pos, B, "start_pos"), _stream(stream)), "kda_conv_prefill")
+
+
+def kda_conv_step(tok, pool, state_slots, commit_len=None, stream=None):
+    """Steps of one or a few tokens a row; commit_len [B] int32: how many of a
+    row's tokens the stored state takes in (None: all)."""
+    B = tok.c.num_seqs
+    _check(lib().kda_conv_step(
+        tok.ref, pool.ref, _table(state_slots, B, "state_slots"),
+        _table(commit_len, B, "commit_len"), _stream(stream)), "kda_conv_step")
+
+
+def kda_scan_workspace_size(num_tokens, num_seqs, channels, state, groups=1):
+    """Workspace bytes with which kda_scan_prefill splits long segments; 0
+    when it would not split at these sizes."""
+    return int(lib().kda_scan_workspace_size(num_tokens, num_seqs, channels, state, groups))
+
+
+def scan_workspace(tok):
+    """A workspace tensor for kda_scan_prefill of this batch (None: not needed)."""
+    n = kda_scan_workspace_size(tok.c.num_tokens, tok.c.num_seqs, tok.c.channels, tok.c.state,
+                                tok.c.groups)
+    return torch.empty(n, dtype=torch.uint8, device=tok.x.device) if n else None
+
+
+def kda_scan_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, start_pos=None,
+                     workspace=None, stream=None):
+    """Selective scan of packed prompts; workspace: from scan_workspace(tok),
+    or None: no segment is split."""
+    B = tok.c.num_seqs
+    ckpt, max_ckpt = _ckpt(ckpt_slots, B)
+    _check(lib().kda_scan_prefill(
+        tok.ref, pool.ref, _table(state_slots, B, "state_slots"), ckpt, max_ckpt, ckpt_every,
+        _table(start_pos, B, "start_pos"), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), _stream(stream)), "kda_scan_prefill")
+
+
+def kda_scan_step(tok, pool, state_slots, commit_len=None, stream=None):
+    """The scan's steps, commit_len as in kda_conv_step."""
+    B = tok.c.num_seqs
+    _check(lib().kda_scan_step(
+        tok.ref, pool.ref, _table(state_slots, B, "state_slots"),
+        _table(commit_len, B, "commit_len"), _stream(stream)), "kda_scan_step")
+
+
+class SlotArrays:
+    """The per-slot tensors [num_slots][...] of a model (pools, rings, of all
+    layers) that kda_move_slots moves together."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("no arrays")
+        self.num_slots = int(self.tensors[0].shape[0])
+        for t in self.tensors:
+            if not t.is_contiguous() or t.shape[0] != self.num_slots:
+                raise ValueError("every array is a contiguous [num_slots][...]")
+        self.c = (kda_slot_array * len(self.tensors))(
+            *[kda_slot_array(t.data_ptr(), t[0].numel() * t.element_size())
+              for t in self.tensors])
+
+
+def kda_move_workspace_size(arrays, n):
+    return int(lib().kda_move_workspace_size(arrays.c, len(arrays.tensors), n))
+
+
+def move_workspace(arrays, n):
+    """A workspace tensor for kda_move_slots of up to n moves."""
+    return torch.empty(max(1, kda_move_workspace_size(arrays, n)), dtype=torch.uint8,
+                       device=arrays.tensors[0].device)
+
+
+def kda_move_slots(arrays, src, dst, workspace=None, stream=None):
+    """In every array: slot dst[i] receives slot src[i] (src < 0: zeros, dst < 0:
+    nothing).  workspace None: src and dst must be disjoint."""
+    n = dst.numel()
+    _check(lib().kda_move_slots(
+        arrays.c, len(arrays.tensors), arrays.num_slots, _table(src, n, "src"),
+        _table(dst, n, "dst"), n, None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), _stream(stream)), "kda_move_slots")
 
 
 def kda_get_device_error(stream=None):

@@ -1,0 +1,459 @@
+"""The state space layers' operators against their fp64 definitions: the short
+causal convolution, the selective scan (prompts and steps) and slot moves."""
+import numpy as np
+import pytest
+import torch
+
+import ssm_ref
+from recurrent_kda_state_gb300 import kda as K
+from recurrent_kda_state_gb300._build import build_library
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(autouse=True)
+def _ready():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build_library()
+    K.kda_get_device_error()
+    yield
+    assert K.kda_get_device_error() == 0
+
+
+def i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rows(rng, n, shape, dt, view):
+    """[n][*shape] on the device; view: the tail of wider rows, off 16 bytes."""
+    size = int(np.prod(shape))
+    wide = torch.from_numpy(rng.standard_normal((n, size + (3 if view else 0))))
+    wide = wide.to("cuda", DT[dt])
+    return (wide[:, 3:] if view else wide).unflatten(1, shape) if len(shape) > 1 else (
+        wide[:, 3:] if view else wide)
+
+
+def within(got, want, tol, what):
+    bad = ~(np.abs(f64(got) - want) <= tol)
+    assert not bad.any(), "%s: %d of %d values out of bounds, first %s" % (
+        what, bad.sum(), bad.size, np.argwhere(bad)[:4].tolist())
+
+
+def cumulate(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+
+
+# ------------------------------------------------------------- convolution
+def conv_case(seed, dt, lens, D, W, bias=True, act=True, view=False, step=False, commit=None,
+              every=0, max_ckpt=0, start=None, extra=3):
+    rng = np.random.default_rng(seed)
+    lens = np.asarray(lens)
+    n, B = int(lens.sum()), len(lens)
+    P = B * (1 + max_ckpt) + extra
+    x = rows(rng, n, (D,), dt, view)
+    w = torch.from_numpy(rng.standard_normal((D, W))).to("cuda", DT[dt])
+    b = torch.from_numpy(rng.standard_normal(D)).to("cuda", DT[dt]) if bias else None
+    data = torch.from_numpy(rng.standard_normal((P, W - 1, D))).to("cuda", DT[dt])
+    ids = rng.permutation(P)
+    slots = ids[:B]
+    ckpt = None
+    if max_ckpt:
+        ckpt = ids[B:B + B * max_ckpt].reshape(B, max_ckpt).copy()
+        ckpt[0, 0] = -1
+    cu = cumulate(lens)
+    want, tol, pool = ssm_ref.conv(
+        f64(x), f64(w), None if b is None else f64(b), cu, f64(data), slots, act, dt,
+        commit, ckpt, every, start)
+    single = step and (lens == 1).all()
+    batch = K.ConvBatch(x, w, b, None if single else i32(cu), "silu" if act else None)
+    cp = K.ConvPool(data)
+    if step:
+        K.kda_conv_step(batch, cp, i32(slots), None if commit is None else i32(commit))
+    else:
+        K.kda_conv_prefill(batch, cp, i32(slots), every, None if ckpt is None else i32(ckpt),
+                           None if start is None else i32(start))
+    within(batch.y, want, tol, "y")
+    np.testing.assert_array_equal(f64(cp.data), pool)
+
+
+LENS = [[1], [2, 0, 1, 3], [7, 8, 9, 0, 0, 64], [130, 1, 517]]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("lens", LENS)
+def test_conv_prefill(dt, W, lens):
+    conv_case(1, dt, lens, 136, W)
+
+
+@pytest.mark.parametrize("D,view", [(1, False), (37, True), (256, True), (1032, False)])
+def test_conv_prefill_channels_and_views(D, view):
+    conv_case(2, "bf16", [33, 5], D, 4, bias=False, act=False, view=view)
+    conv_case(3, "f32", [33, 5], D, 3, view=view)
+
+
+def test_conv_prefill_many_segments():
+    lens = np.random.default_rng(4).integers(0, 4, 700)
+    conv_case(4, "bf16", lens, 40, 4)
+
+
+def test_conv_prefill_long_tiles():
+    """Tiles of the largest size, with a segment border inside."""
+    conv_case(5, "bf16", [4099, 61, 4000], 2048, 4)
+
+
+@pytest.mark.parametrize("start", [None, [0, 5, 30]])
+def test_conv_checkpoints(start):
+    conv_case(6, "bf16", [70, 3, 40], 64, 4, every=16, max_ckpt=3, start=start)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("W", [2, 4])
+def test_conv_step(dt, W):
+    conv_case(7, dt, [1] * 9, 264, W, step=True)
+    conv_case(8, dt, [8, 1, 0, 3, 8, 11], 264, W, step=True, commit=[0, 1, 0, 2, 8, 9])
+    conv_case(9, dt, [8, 1, 0, 3], 51, W, step=True, view=True)
+
+
+def test_conv_steps_follow_a_prompt():
+    """A prompt and then steps give what one longer prompt gives."""
+    rng = np.random.default_rng(10)
+    D, W, n = 96, 4, 29
+    x = rows(rng, n, (D,), "bf16", False)
+    w = torch.from_numpy(rng.standard_normal((D, W))).to("cuda", torch.bfloat16)
+    whole, parts = (K.ConvPool.zeros(2, W, D, torch.bfloat16) for _ in range(2))
+    one = K.ConvBatch(x, w, cu_seqlens=i32([0, n]))
+    K.kda_conv_prefill(one, whole, i32([1]))
+    a = K.ConvBatch(x[:20], w, cu_seqlens=i32([0, 20]))
+    K.kda_conv_prefill(a, parts, i32([1]))
+    b = K.ConvBatch(x[20:25], w, cu_seqlens=i32([0, 5]))  # two of five drafts accepted
+    K.kda_conv_step(b, parts, i32([1]), i32([2]))
+    c = K.ConvBatch(x[22:], w, cu_seqlens=i32([0, 7]))
+    K.kda_conv_step(c, parts, i32([1]))
+    got = torch.cat([a.y, b.y[:2], c.y])
+    assert torch.equal(got, one.y) and torch.equal(whole.data, parts.data)
+
+
+# ------------------------------------------------------------------- scan
+def scan_case(seed, dt, lens, D, S, G=1, gate=True, skip=True, bias=True, softplus=True,
+              view=False, step=False, commit=None, every=0, max_ckpt=0, start=None, split=True,
+              extra=3, dt_scale=1.0, fill=None):
+    rng = np.random.default_rng(seed)
+    lens = np.asarray(lens)
+    n, B = int(lens.sum()), len(lens)
+    P = B * (1 + max_ckpt) + extra
+    x, d = rows(rng, n, (D,), dt, view), rows(rng, n, (D,), dt, view) * dt_scale
+    if not softplus:
+        d = d.abs() * 0.1
+    z = rows(rng, n, (D,), dt, view) if gate else None
+    b, c = rows(rng, n, (G, S), dt, view), rows(rng, n, (G, S), dt, view)
+
+    def par(a):
+        return torch.from_numpy(a).to("cuda", torch.float32)
+    A = par(-np.exp(rng.uniform(-3.0, 3.0, (D, S))))
+    skips = par(rng.standard_normal(D)) if skip else None
+    # without softplus a time step is dt + bias itself, which is not negative
+    dtb = par(rng.uniform(-7.0, 0.0, D) if softplus else rng.uniform(0.0, 0.1, D)) if bias else None
+    data = par(rng.standard_normal((P, D, S)))
+    ids = rng.permutation(P)
+    slots = ids[:B]
+    ckpt = None
+    if max_ckpt:
+        ckpt = ids[B:B + B * max_ckpt].reshape(B, max_ckpt).copy()
+        ckpt[0, 0] = -1
+    cu = cumulate(lens)
+
+    def opt(t):
+        return None if t is None else f64(t)
+    want, tol, pool, pool_tol = ssm_ref.scan(
+        f64(x), f64(d), f64(A), f64(b), f64(c), opt(skips), opt(z),
+        opt(dtb), cu, f64(data), slots, softplus, dt, commit, ckpt,
+        every, start)
+    single = step and (lens == 1).all()
+    batch = K.ScanBatch(x, d, A, b, c, D=skips, z=z, dt_bias=dtb,
+                        cu_seqlens=None if single else i32(cu), dt_softplus=softplus)
+    sp = K.ScanPool(data)
+    if step:
+        K.kda_scan_step(batch, sp, i32(slots), None if commit is None else i32(commit))
+    else:
+        ws = K.scan_workspace(batch) if split else None
+        if ws is not None:
+            ws.fill_(0xff)  # NaN: nothing may be read before it is written
+        K.kda_scan_prefill(batch, sp, i32(slots), every, None if ckpt is None else i32(ckpt),
+                           None if start is None else i32(start), ws)
+    within(batch.y, want, tol, "y")
+    within(sp.data, pool, pool_tol, "states")
+
+
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("S", [16, 32, 64, 128])
+@pytest.mark.parametrize("lens", LENS)
+def test_scan_prefill(split, dt, S, lens):
+    scan_case(11, dt, lens, 72, S, split=split)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D,G,view", [(1, 1, False), (37, 1, True), (130, 2, False),
+                                      (384, 3, True), (513, 1, False)])
+def test_scan_prefill_channels_groups_views(dt, D, G, view):
+    scan_case(12, dt, [40, 3, 90], D, 16, G=G, view=view)
+    scan_case(13, dt, [40, 3, 90], D, 64, G=G, view=view, gate=False, skip=False)
+
+
+@pytest.mark.parametrize("kw", [dict(gate=False), dict(skip=False), dict(bias=False),
+                                dict(softplus=False), dict(dt_scale=20.0),
+                                dict(gate=False, skip=False, bias=False, softplus=False)])
+def test_scan_prefill_options(kw):
+    scan_case(14, "f32", [100, 31], 64, 16, **kw)
+    scan_case(15, "bf16", [100, 31], 64, 16, **kw)
+
+
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("start", [None, [0, 5, 30]])
+@pytest.mark.parametrize("S", [16, 64])
+def test_scan_checkpoints(split, start, S):
+    scan_case(16, "f32", [300, 3, 100], 40, S, every=32, max_ckpt=4, start=start, split=split)
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_scan_prefill_long(split):
+    """Long segments beside short ones: parts that start and end in tiles."""
+    scan_case(17, "bf16", [3001, 17, 0, 700, 1], 160, 16, split=split)
+
+
+def test_scan_prefill_many_segments():
+    lens = np.random.default_rng(18).integers(0, 6, 500)
+    scan_case(18, "f32", lens, 24, 16)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("S", [16, 32, 64, 128])
+def test_scan_step(dt, S):
+    scan_case(19, dt, [1] * 11, 200, S, step=True)
+    scan_case(20, dt, [8, 1, 0, 3, 8, 11], 200, S, step=True, commit=[0, 1, 0, 2, 8, 9])
+    scan_case(21, dt, [8, 1, 0, 3], 51, S, step=True, view=True, gate=False)
+
+
+def test_scan_step_groups():
+    scan_case(22, "bf16", [1] * 5, 384, 16, G=3, step=True, view=True)
+
+
+def test_scan_steps_follow_a_prompt():
+    """Prompt and steps against one prompt, with a draft rejected between."""
+    rng = np.random.default_rng(23)
+    D, S, n = 64, 16, 53
+    t = {k: rows(rng, n, (D,), "f32", False) for k in ("x", "dt", "z")}
+    b, c = (rows(rng, n, (1, S), "f32", False) for _ in range(2))
+    A = torch.from_numpy(-np.exp(rng.uniform(-2, 2, (D, S)))).to("cuda", torch.float32)
+
+    def part(lo, hi):
+        return K.ScanBatch(t["x"][lo:hi], t["dt"][lo:hi], A, b[lo:hi], c[lo:hi],
+                           z=t["z"][lo:hi], cu_seqlens=i32([0, hi - lo]))
+    whole, parts = K.ScanPool.zeros(2, D, S), K.ScanPool.zeros(2, D, S)
+    one = part(0, n)
+    K.kda_scan_prefill(one, whole, i32([1]))
+    a, d, e = part(0, 40), part(40, 46), part(43, n)
+    K.kda_scan_prefill(a, parts, i32([1]))
+    K.kda_scan_step(d, parts, i32([1]), i32([3]))
+    K.kda_scan_step(e, parts, i32([1]))
+    got = torch.cat([a.y, d.y[:3], e.y])
+    scale = float(one.y.abs().max())
+    assert float((got - one.y).abs().max()) <= (8 * n + 64) * ssm_ref.U32 * 16 * scale
+    assert float((whole.data - parts.data).abs().max()) <= \
+        (8 * n + 64) * ssm_ref.U32 * 16 * float(whole.data.abs().max())
+
+
+def test_nan_and_inf_stay_in_their_segment():
+    """A NaN token spoils its own segment from there on, and nothing else."""
+    rng = np.random.default_rng(24)
+    D, S, lens = 64, 16, [40, 300, 50]
+    n, cu = sum(lens), cumulate([40, 300, 50])
+    args = [rows(rng, n, (D,), "f32", False) for _ in range(2)]
+    b, c = (rows(rng, n, (1, S), "f32", False) for _ in range(2))
+    A = torch.from_numpy(-np.exp(rng.uniform(-2, 2, (D, S)))).to("cuda", torch.float32)
+    args[0][60, 7] = float("nan")
+    args[0][70, 9] = float("inf")
+    batch = K.ScanBatch(args[0], args[1], A, b, c, cu_seqlens=i32(cu))
+    pool = K.ScanPool.zeros(3, D, S)
+    K.kda_scan_prefill(batch, pool, i32([0, 1, 2]), workspace=K.scan_workspace(batch))
+    bad = ~torch.isfinite(batch.y).cpu().numpy()
+    assert bad[60:340, 7].all() and bad[70, 9]
+    bad[60:340, 7] = bad[70:340, 9] = False
+    assert not bad.any()
+    w = torch.ones(D, 4, device="cuda")
+    cb = K.ConvBatch(args[0], w, cu_seqlens=i32(cu), activation=None)
+    K.kda_conv_prefill(cb, K.ConvPool.zeros(3, 4, D, torch.float32), i32([0, 1, 2]))
+    bad = ~torch.isfinite(cb.y).cpu().numpy()
+    assert bad[60:64, 7].all() and bad[70:74, 9].all() and bad.sum() == 8
+
+
+def test_time_steps_far_out():
+    """softplus at both ends: steps that vanish and steps that forget all."""
+    D, S = 16, 16
+    v = torch.linspace(-100.0, 100.0, 41, device="cuda")[:, None].expand(41, D).contiguous()
+    x = torch.ones(41, D, device="cuda")
+    b = torch.ones(41, 1, S, device="cuda")
+    A = -torch.ones(D, S, device="cuda")
+    pool = K.ScanPool(torch.ones(1, D, S, device="cuda"))
+    batch = K.ScanBatch(x, v, A, b, b, cu_seqlens=i32([0, 41]))
+    want, tol, end, end_tol = ssm_ref.scan(
+        f64(x), f64(v), f64(A), f64(b), f64(b), None, None, None, np.array([0, 41]),
+        np.ones((1, D, S)), [0])
+    K.kda_scan_prefill(batch, pool, i32([0]))
+    within(batch.y, want, tol, "y")
+    within(pool.data, end, end_tol, "states")
+
+
+# ------------------------------------------------------------------ streams
+def test_calls_take_their_stream_and_can_be_captured():
+    rng = np.random.default_rng(25)
+    D, S, n = 128, 16, 600
+    x, d = (rows(rng, n, (D,), "bf16", False) for _ in range(2))
+    b, c = (rows(rng, n, (1, S), "bf16", False) for _ in range(2))
+    w = torch.from_numpy(rng.standard_normal((D, 4))).to("cuda", torch.bfloat16)
+    A = torch.from_numpy(-np.exp(rng.uniform(-2, 2, (D, S)))).to("cuda", torch.float32)
+    cu, slots = i32([0, n]), i32([0])
+    conv, u = K.ConvPool.zeros(2, 4, D, torch.bfloat16), torch.empty_like(x)
+    scan = K.ScanPool.zeros(2, D, S)
+    cb = K.ConvBatch(x, w, cu_seqlens=cu, y=u)
+    sb = K.ScanBatch(u, d, A, b, c, cu_seqlens=cu)
+    ws, src, dst = K.scan_workspace(sb), i32([0]), i32([1])
+    arrays = K.SlotArrays([conv.data, scan.data])
+    mws = K.move_workspace(arrays, 1)
+
+    def layer(stream=None):
+        K.kda_conv_prefill(cb, conv, slots, stream=stream)
+        K.kda_scan_prefill(sb, scan, slots, workspace=ws, stream=stream)
+        K.kda_move_slots(arrays, src, dst, mws, stream=stream)
+    layer()
+    torch.cuda.synchronize()
+    first = [t.clone() for t in (sb.y, conv.data, scan.data)]
+    for t in (conv.data, scan.data, sb.y, u):
+        t.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    layer(side)
+    side.synchronize()
+    for t, f in zip((sb.y, conv.data, scan.data), first):
+        assert torch.equal(t, f)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer()
+    for t in (conv.data, scan.data, sb.y, u):
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for t, f in zip((sb.y, conv.data, scan.data), first):
+        assert torch.equal(t, f)
+
+
+# --------------------------------------------------------------- device data
+def test_bad_device_data_is_skipped_and_reported():
+    """Slot ids, segment tables and commit counts that are out of range leave
+    the row's outputs and state as they were and set their bit."""
+    rng = np.random.default_rng(26)
+    D, S = 64, 16
+    x, d = (rows(rng, 12, (D,), "f32", False) for _ in range(2))
+    b, c = (rows(rng, 12, (1, S), "f32", False) for _ in range(2))
+    w, A = torch.ones(D, 4, device="cuda"), -torch.ones(D, S, device="cuda")
+    cases = [(i32([0, 4, 8, 12]), i32([0, 9, 2]), None, K.KDA_DERR_SLOT, [1]),
+             (i32([0, 4, 8, 12]), i32([0, -1, 2]), None, K.KDA_DERR_SLOT, [1]),
+             (i32([0, 4, 2, 12]), i32([0, 1, 2]), None, K.KDA_DERR_SEGMENT, [1]),
+             (i32([0, 4, 8, 99]), i32([0, 1, 2]), None, K.KDA_DERR_SEGMENT, [2]),
+             (i32([0, 4, 8, 12]), i32([0, 1, 2]), i32([4, 5, 0]), K.KDA_DERR_ACCEPT, [1]),
+             (i32([0, 4, 8, 12]), i32([0, 1, 2]), i32([4, -1, 0]), K.KDA_DERR_ACCEPT, [1])]
+    for cu, slots, commit, bit, skipped in cases:
+        for step in (True, False):
+            if commit is not None and not step:
+                continue
+            conv, scan = K.ConvPool.zeros(4, 4, D, torch.float32), K.ScanPool.zeros(4, D, S)
+            conv.data.fill_(7.0), scan.data.fill_(7.0)
+            cb = K.ConvBatch(x, w, cu_seqlens=cu)
+            sb = K.ScanBatch(x, d, A, b, c, cu_seqlens=cu)
+            cb.y.fill_(5.0), sb.y.fill_(5.0)
+            for call, batch, pool in (("conv", cb, conv), ("scan", sb, scan)):
+                if step:
+                    getattr(K, "kda_%s_step" % call)(batch, pool, slots, commit)
+                else:
+                    getattr(K, "kda_%s_prefill" % call)(batch, pool, slots)
+                assert K.kda_get_device_error() & bit
+                for i in skipped:
+                    if bit != K.KDA_DERR_SEGMENT:
+                        assert (batch.y[4 * i:4 * i + 4] == 5.0).all()
+                    assert (pool.data[1 if i == 1 else i] == 7.0).all()
+                assert not (batch.y[:4] == 5.0).any()
+    K.kda_get_device_error()
+
+
+# -------------------------------------------------------------------- moves
+def move_case(seed, P, src, dst, ws=True, shapes=((4, 33), (128, 16), (5000, 2))):
+    rng = np.random.default_rng(seed)
+    dts = [torch.bfloat16, torch.float32, torch.int32]
+    ts = [torch.from_numpy(rng.integers(-1000, 1000, (P,) + s)).to("cuda", d)
+          for s, d in zip(shapes, dts)]
+    want = ssm_ref.moves([f64(t) for t in ts], src, dst)
+    arrays = K.SlotArrays(ts)
+    K.kda_move_slots(arrays, i32(src), i32(dst), K.move_workspace(arrays, len(src)) if ws else None)
+    for t, w in zip(ts, want):
+        np.testing.assert_array_equal(f64(t), w)
+
+
+def test_moves():
+    move_case(27, 9, [0], [5], ws=False)                       # fork
+    move_case(28, 9, [0, 0, 0, -1], [5, 6, 8, 1], ws=False)    # one source, many copies; free
+    move_case(29, 9, [0, 1, 2, 3], [1, 2, 3, 0])               # a cycle
+    move_case(30, 9, [3, 5, 5, -1, 7, 2], [0, 3, 1, 5, -1, 2])  # chain, fork, free, none, self
+    move_case(31, 9, [8, 7, -1, -1], [1, 2, 8, 7])             # compaction
+    move_case(32, 1, [-1], [0])
+
+
+def test_moves_permutation_of_many():
+    rng = np.random.default_rng(33)
+    move_case(33, 700, rng.permutation(700), rng.permutation(700), shapes=((1, 2), (3, 5), (7, 1)))
+
+
+def test_moves_out_of_range_are_skipped():
+    t = torch.arange(12, device="cuda", dtype=torch.int32).view(4, 3)
+    arrays = K.SlotArrays([t])
+    K.kda_move_slots(arrays, i32([0, 4, 1]), i32([4, 2, 3]))
+    assert K.kda_get_device_error() == K.KDA_DERR_SLOT
+    assert t.tolist() == [[0, 1, 2], [3, 4, 5], [6, 7, 8], [3, 4, 5]]
+
+
+# ------------------------------------------------------------ long offsets
+def test_offsets_past_31_bits():
+    """Rows and slots whose element offsets pass 2^31."""
+    D, S, n = 64, 16, 6
+    stride = 2 ** 29 + 8
+    wide = torch.zeros(5 * stride + D, dtype=torch.bfloat16, device="cuda")
+    x = wide.as_strided((n, D), (stride, 1))
+    rng = np.random.default_rng(34)
+    x.copy_(rows(rng, n, (D,), "bf16", False))
+    d = rows(rng, n, (D,), "bf16", False)
+    b, c = (rows(rng, n, (1, S), "bf16", False) for _ in range(2))
+    A = torch.from_numpy(-np.exp(rng.uniform(-2, 2, (D, S)))).to("cuda", torch.float32)
+    w = torch.from_numpy(rng.standard_normal((D, 4))).to("cuda", torch.bfloat16)
+    P = 2 ** 31 // (D * S) + 2
+    data = torch.zeros(P, D, S, device="cuda")
+    pool, slots, cu = K.ScanPool(data), i32([P - 1]), i32([0, n])
+    ref = K.ScanPool.zeros(1, D, S)
+    for call in ("prefill", "step"):
+        far = K.ScanBatch(x, d, A, b, c, cu_seqlens=cu)
+        near = K.ScanBatch(x.contiguous(), d, A, b, c, cu_seqlens=cu)
+        getattr(K, "kda_scan_" + call)(far, pool, slots)
+        getattr(K, "kda_scan_" + call)(near, ref, i32([0]))
+        assert torch.equal(far.y, near.y) and torch.equal(data[-1], ref.data[0])
+        cfar, cnear = K.ConvBatch(x, w, cu_seqlens=cu), K.ConvBatch(x.contiguous(), w, cu_seqlens=cu)
+        for bt in (cfar, cnear):
+            getattr(K, "kda_conv_" + call)(bt, K.ConvPool.zeros(1, 4, D, torch.bfloat16), i32([0]))
+        assert torch.equal(cfar.y, cnear.y)
+    arrays = K.SlotArrays([data])
+    K.kda_move_slots(arrays, i32([P - 1]), i32([P - 2]))
+    assert torch.equal(data[-2], data[-1]) and not data[-3].any()
