@@ -110,10 +110,4 @@ cudaError_t launch_scan_step(const ScanParams &p, kda_dtype dt, cudaStream_t s) 
   return dt == KDA_F32 ? launch_step_t<float>(p, s) : launch_step_t<__nv_bfloat16>(p, s);
 }
 
-cudaError_t launch_scan_prefill(const ScanParams &p, kda_dtype dt, cudaStream_t s) {
-  return launch_scan_step(p, dt, s);
-}
-
-size_t scan_workspace_floats(int, int, int, int, int) { return 0; }
-
 }  // namespace kda

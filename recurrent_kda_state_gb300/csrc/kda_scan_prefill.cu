@@ -1,0 +1,528 @@
+// Selective scan of packed prompts:
+//     h[n] = exp(delta A[n]) h[n] + delta x B[n],   y = C . h + D x  (gated)
+//
+// Per (token, channel, state) one ex2 and four fp32 operations, against 8
+// bytes per (token, channel): at S = 16 the arithmetic pipes bound it, not
+// HBM.  So the inner loop holds nothing else: a thread owns eight states of
+// two neighbouring channels in registers (S / 8 lanes a channel pair) and the
+// pair's values travel as packed fp32 pairs, so one instruction serves both.
+// A block stages tiles of tokens in shared memory: delta and delta x per
+// channel (the softplus is computed once, not once per lane), B and C as
+// duplicated pairs.  The next tile's rows arrive by asynchronous copies
+// meanwhile.  After a tile its y, summed over the channel's lanes, goes back
+// through shared memory to the thread that staged the row, which adds the
+// skip, applies the gate and writes 16 bytes.
+//
+// Few long segments leave most of the machine idle, so with a workspace a
+// segment is cut into parts: a first launch computes each part's end state
+// from a zero start and its sum of delta; the second starts part k from
+// h = exp(A sum_j delta) h + end_j over the parts before it, and does the rest.
+// The first launch repeats the exponentials, which is why segments are not
+// cut further than the machine has room for.
+#include "kda_ssm.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kStates = 8;        // states of a thread, for each of two channels
+constexpr int kAlign = 16;        // parts and tiles start on multiples of this
+constexpr int kCarry = 2 * kStates + 2;  // floats a thread carries between parts
+
+// Tokens of a tile: 16, 8 for the wide states whose B and C rows are long.
+template <int S>
+struct Shape {
+  static constexpr int kLanes = S / kStates;         // of a channel pair
+  static constexpr int kPairs = kThreads / kLanes;   // of a block
+  static constexpr int kChans = 2 * kPairs;
+  static constexpr int kTile = S <= 32 ? 16 : 8;
+};
+
+// Packed fp32 pairs: the two channels of a thread.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 exp2_2(f2 v) {
+  const float2 e = unpack2(v);
+  return pack2(ex2f(e.x), ex2f(e.y));
+}
+
+// A log2(e), -inf held at the lowest finite value: a token that pads a tile has
+// delta = 0, and 0 * -inf would be NaN.
+__device__ __forceinline__ float exponent_scale(float a) {
+  const float r = a * kLog2e;
+  return r < -3.4028234e38f ? -3.4028234e38f : r;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void copy16(void *to, const void *from, bool on) {
+  const int n = on ? 16 : 0;  // 0: the 16 bytes become zero
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from),
+               "r"(n) : "memory");
+}
+
+// The part of a segment that a block works on.
+struct Part {
+  int i;           // segment
+  int k, count;    // part of it, number of its parts
+  int v0;          // its first carry slot in the workspace
+  int at;          // local token of the part's first tile (may be below 0)
+  int lo, hi;      // local tokens [lo, hi)
+  long long p0;    // absolute position of the segment's first token
+};
+
+__device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, SegLoc *s) {
+  const SegParams &g = p.seg;
+  int i = v;
+  if (p.part) {  // the last segment with cu[i] / part + 2 i <= v (room for its parts)
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = g.B;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int j = lo + lane * step;
+      const unsigned m = __ballot_sync(~0u, j < hi && g.cu[j] / p.part + 2 * j <= v);
+      lo += m ? (31 - __clz(m)) * step : 0;
+      hi = min(lo + step, hi);
+    }
+    i = lo;
+  }
+  if (!locate_segment(g, i, s) || s->len == 0) return false;
+  q->i = i;
+  q->p0 = g.ckpt_slots && g.start_pos ? g.start_pos[i] : 0;
+  const int r = (int)(q->p0 & (kAlign - 1));  // tiles end on absolute multiples
+  if (!p.part) {
+    q->k = 0;
+    q->count = 1;
+    q->v0 = 0;
+    q->at = -r;
+    q->hi = s->len;
+  } else {
+    q->v0 = s->begin / p.part + 2 * i;
+    q->k = v - q->v0;
+    q->count = (int)(((long long)s->len + r + p.part - 1) / p.part);
+    if (q->k < 0 || q->k >= q->count) return false;
+    const long long at = (long long)q->k * p.part - r;
+    q->at = (int)at;
+    q->hi = (int)min((long long)s->len, at + p.part);
+  }
+  q->lo = max(0, q->at);
+  return true;
+}
+
+// LOCAL: the first launch (end states of the parts, no outputs).
+template <typename T, int S, bool VEC, bool LOCAL>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+    scan_prefill_kernel(const ScanParams p, int nblk) {
+  using Sh = Shape<S>;
+  constexpr int TT = Sh::kTile, V = InVec<T>::kElems, NC = Sh::kChans / V, KP = V / 2;
+  constexpr int ITEMS = TT * NC, NI = (ITEMS + kThreads - 1) / kThreads;
+  constexpr int NB = TT * S / kThreads;
+  constexpr int TENSORS = LOCAL ? 2 : 3;
+  extern __shared__ __align__(16) unsigned char smem[];
+  uint4 *raw = reinterpret_cast<uint4 *>(smem);  // [stage][x, dt, z][ITEMS]
+  float4 *ddx = reinterpret_cast<float4 *>(raw + 2 * TENSORS * ITEMS);  // [TT][kPairs]
+  float2 *sb = reinterpret_cast<float2 *>(ddx + TT * Sh::kPairs);       // [TT][S]
+  float2 *sc = sb + TT * S;
+  float *sskip = reinterpret_cast<float *>(LOCAL ? sc : sc + TT * S);   // [kChans]
+  float *sbias = sskip + Sh::kChans;
+
+  const int tid = threadIdx.x;
+  const int v = blockIdx.x / nblk, blk = blockIdx.x % nblk;
+  Part q;
+  SegLoc s;
+  if (!find_part(p, v, &q, &s)) return;
+  if (LOCAL && q.k + 1 >= q.count) return;
+
+  // the block's channels: kChans of one group
+  const int per = p.C_ / p.G, bpg = nblk / p.G, g = blk / bpg;
+  const int c0 = g * per + (blk % bpg) * Sh::kChans;
+  const int nch = min(Sh::kChans, (g + 1) * per - c0);
+
+  for (int c = tid; c < Sh::kChans; c += kThreads) {
+    sskip[c] = p.D && c < nch ? p.D[c0 + c] : 0.0f;
+    sbias[c] = p.dtb && c < nch ? p.dtb[c0 + c] : 0.0f;
+  }
+
+  // this thread's pair of channels and states 2 (l + kLanes j) + {0, 1}
+  const int l = tid % Sh::kLanes, pr = tid / Sh::kLanes;
+  const int ca = c0 + min(2 * pr, nch - 1), cb = c0 + min(2 * pr + 1, nch - 1);
+  f2 a[kStates], h[kStates];
+#pragma unroll
+  for (int j = 0; j < kStates / 2; ++j) {
+    const int n = 2 * (l + Sh::kLanes * j);
+    const float2 x = *reinterpret_cast<const float2 *>(p.A + (long long)ca * S + n);
+    const float2 y = *reinterpret_cast<const float2 *>(p.A + (long long)cb * S + n);
+    a[2 * j] = pack2(exponent_scale(x.x), exponent_scale(y.x));
+    a[2 * j + 1] = pack2(exponent_scale(x.y), exponent_scale(y.y));
+  }
+
+  const long long row = (long long)p.C_ * S;
+  auto load_state = [&](const float *from) {
+#pragma unroll
+    for (int j = 0; j < kStates / 2; ++j) {
+      const int n = 2 * (l + Sh::kLanes * j);
+      const float2 x = *reinterpret_cast<const float2 *>(from + (long long)ca * S + n);
+      const float2 y = *reinterpret_cast<const float2 *>(from + (long long)cb * S + n);
+      h[2 * j] = pack2(x.x, y.x);
+      h[2 * j + 1] = pack2(x.y, y.y);
+    }
+  };
+  auto store_state = [&](float *to) {
+#pragma unroll
+    for (int j = 0; j < kStates / 2; ++j) {
+      const int n = 2 * (l + Sh::kLanes * j);
+      const float2 x = unpack2(h[2 * j]), y = unpack2(h[2 * j + 1]);
+      if (2 * pr < nch)
+        *reinterpret_cast<float2 *>(to + (long long)ca * S + n) = make_float2(x.x, y.x);
+      if (2 * pr + 1 < nch)
+        *reinterpret_cast<float2 *>(to + (long long)cb * S + n) = make_float2(x.y, y.y);
+    }
+  };
+  // carry slot of a part: [value][thread], so that warps move whole lines
+  auto carry = [&](int slot) {
+    return p.ws + ((long long)slot * nblk + blk) * (kCarry * kThreads) + tid;
+  };
+  auto store_carry = [&](int slot, f2 sum) {
+    float *w = carry(slot);
+#pragma unroll
+    for (int n = 0; n < kStates; ++n) {
+      const float2 x = unpack2(h[n]);
+      w[(2 * n) * kThreads] = x.x;
+      w[(2 * n + 1) * kThreads] = x.y;
+    }
+    const float2 x = unpack2(sum);
+    w[2 * kStates * kThreads] = x.x;
+    w[(2 * kStates + 1) * kThreads] = x.y;
+  };
+
+  // The state at the part's start.  The carry slot of part 0 holds the slot's
+  // own state, since the last part replaces that; slot k holds part k - 1's
+  // end (for k = 1 the whole state, beyond from a zero start) and its sum of
+  // delta.
+  float *mine = p.pool + s.slot * row;
+  if (LOCAL) {
+    if (q.k == 0) {
+      load_state(mine);
+      store_carry(q.v0, 0);
+    } else {
+#pragma unroll
+      for (int n = 0; n < kStates; ++n) h[n] = 0;
+    }
+  } else if (q.count == 1) {
+    load_state(mine);
+  } else {
+    const int first = q.k ? 1 : 0;
+#pragma unroll
+    for (int n = 0; n < kStates; ++n) {
+      const float *w = carry(q.v0 + first);
+      h[n] = pack2(w[(2 * n) * kThreads], w[(2 * n + 1) * kThreads]);
+    }
+    for (int k = 2; k <= q.k; ++k) {
+      const float *w = carry(q.v0 + k);
+      const f2 d = pack2(w[2 * kStates * kThreads], w[(2 * kStates + 1) * kThreads]);
+#pragma unroll
+      for (int n = 0; n < kStates; ++n)
+        h[n] = fma2(exp2_2(mul2(d, a[n])), h[n],
+                    pack2(w[(2 * n) * kThreads], w[(2 * n + 1) * kThreads]));
+    }
+  }
+
+  const T *rows[3] = {static_cast<const T *>(p.x) + s.begin * p.xs + c0,
+                      static_cast<const T *>(p.dt) + s.begin * p.dts + c0,
+                      static_cast<const T *>(p.z) + s.begin * p.zs + c0};
+  const long long strides[3] = {p.xs, p.dts, p.zs};
+  const T *B = static_cast<const T *>(p.B) + s.begin * p.bs + g * S;
+  const T *C = static_cast<const T *>(p.C) + s.begin * p.cs + g * S;
+  T *y = static_cast<T *>(p.y) + s.begin * p.ys + c0;
+  const bool gate = !LOCAL && p.z != nullptr;
+
+  // Item (t, cv): V channels of one token of the tile; staged, consumed in the
+  // epilogue and written by the same thread.
+  auto fetch_rows = [&](int at, int stage) {
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      const int it = tid + k * kThreads;
+      if (ITEMS % kThreads != 0 && it >= ITEMS) break;
+      const int t = at + it / NC, c = (it % NC) * V;
+      const bool on = t >= q.lo && t < q.hi && c < nch;
+#pragma unroll
+      for (int w = 0; w < TENSORS; ++w) {
+        if (w == 2 && !gate) break;
+        uint4 *to = raw + (stage * TENSORS + w) * ITEMS + it;
+        const T *from = rows[w] + (on ? t * strides[w] + c : 0);
+        if (VEC) {
+          copy16(to, on ? static_cast<const void *>(from) : p.A, on);
+        } else {
+          alignas(16) T e[V];
+#pragma unroll
+          for (int u = 0; u < V; ++u) e[u] = on && c + u < nch ? from[u] : out_scalar<T>(0.0f);
+          *to = *reinterpret_cast<const uint4 *>(e);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float rb[NB], rc[NB];
+  auto fetch_bc = [&](int at) {
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int e = tid + k * kThreads, t = at + e / S;
+      const bool on = t >= q.lo && t < q.hi;
+      rb[k] = on ? in_scalar<T>(B + t * p.bs + e % S) : 0.0f;
+      if (!LOCAL) rc[k] = on ? in_scalar<T>(C + t * p.cs + e % S) : 0.0f;
+    }
+  };
+  // slot of a channel pair in a row of ddx: written four (two) pairs an item
+  // and read a warp's pairs in a row, both without bank conflicts
+  auto slot_of = [&](int k, int c) {  // pair KP c + k
+    return k * NC + (NC >= 8 ? c ^ ((k & 1) << 2) : c);
+  };
+  const int my_slot = slot_of(pr % KP, pr / KP);
+
+  f2 sum = 0;
+  const int tiles = (q.hi - q.at + TT - 1) / TT;
+  fetch_rows(q.at, 0);
+  fetch_bc(q.at);
+  __syncthreads();  // sskip, sbias
+  for (int j = 0; j < tiles; ++j) {
+    const int at = q.at + j * TT, stage = j & 1;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      const int it = tid + k * kThreads;
+      if (ITEMS % kThreads != 0 && it >= ITEMS) break;
+      const int t = it / NC, cv = it % NC;
+      const bool on = at + t >= q.lo && at + t < q.hi;
+      float x[V], d[V];
+      const uint4 *from = raw + stage * TENSORS * ITEMS + it;
+      InVec<T>::load(reinterpret_cast<const T *>(from), x);
+      InVec<T>::load(reinterpret_cast<const T *>(from + ITEMS), d);
+#pragma unroll
+      for (int u = 0; u < V; ++u) {
+        d[u] += sbias[cv * V + u];
+        if (p.softplus) d[u] = softplus_f(d[u]);
+        d[u] = on ? d[u] : 0.0f;  // outside the part: the state stays as it is
+        x[u] *= d[u];
+      }
+#pragma unroll
+      for (int u = 0; u < KP; ++u)
+        ddx[t * Sh::kPairs + slot_of(u, cv)] =
+            make_float4(d[2 * u], d[2 * u + 1], x[2 * u], x[2 * u + 1]);
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      sb[tid + k * kThreads] = make_float2(rb[k], rb[k]);
+      if (!LOCAL) sc[tid + k * kThreads] = make_float2(rc[k], rc[k]);
+    }
+    if (j + 1 < tiles) {
+      fetch_rows(at + TT, stage ^ 1);
+      fetch_bc(at + TT);
+    }
+    __syncthreads();
+
+    const int nt = min(TT, q.hi - at);
+    if (LOCAL) {
+#pragma unroll 2
+      for (int t = 0; t < nt; ++t) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(ddx + t * Sh::kPairs + my_slot);
+        const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(sb + t * S) + l;
+        sum = add2(sum, w.x);
+#pragma unroll
+        for (int n = 0; n < kStates; n += 2) {
+          const ulonglong2 b = bp[Sh::kLanes * n / 2];
+          h[n] = fma2(exp2_2(mul2(w.x, a[n])), h[n], mul2(w.y, b.x));
+          h[n + 1] = fma2(exp2_2(mul2(w.x, a[n + 1])), h[n + 1], mul2(w.y, b.y));
+        }
+      }
+    } else {
+#pragma unroll 2
+      for (int t = 0; t < nt; t += 2) {  // TT is even; a token past nt is neutral
+        f2 o[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const ulonglong2 w =
+              *reinterpret_cast<const ulonglong2 *>(ddx + (t + u) * Sh::kPairs + my_slot);
+          const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(sb + (t + u) * S) + l;
+          const ulonglong2 *cp = reinterpret_cast<const ulonglong2 *>(sc + (t + u) * S) + l;
+          f2 o0 = 0, o1 = 0;
+#pragma unroll
+          for (int n = 0; n < kStates; n += 2) {
+            const ulonglong2 b = bp[Sh::kLanes * n / 2], c = cp[Sh::kLanes * n / 2];
+            h[n] = fma2(exp2_2(mul2(w.x, a[n])), h[n], mul2(w.y, b.x));
+            h[n + 1] = fma2(exp2_2(mul2(w.x, a[n + 1])), h[n + 1], mul2(w.y, b.y));
+            o0 = fma2(c.x, h[n], o0);
+            o1 = fma2(c.y, h[n + 1], o1);
+          }
+          o[u] = add2(o0, o1);
+        }
+        // sum over the lanes: neighbours exchange one token each, so that an
+        // even lane ends with token t, an odd one with t + 1
+        const int odd = l & 1;
+        const float2 give = unpack2(odd ? o[0] : o[1]);
+        float2 keep = unpack2(odd ? o[1] : o[0]);
+        keep.x += __shfl_xor_sync(~0u, give.x, 1);
+        keep.y += __shfl_xor_sync(~0u, give.y, 1);
+#pragma unroll
+        for (int m = 2; m < Sh::kLanes; m *= 2) {
+          keep.x += __shfl_xor_sync(~0u, keep.x, m);
+          keep.y += __shfl_xor_sync(~0u, keep.y, m);
+        }
+        // y takes the place of delta, which all lanes of the pair have read
+        // (their shuffles depend on it).  No "memory" clobber: no load before
+        // the barrier reads what this writes, so loads may pass it.
+        if (l < 2)
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::
+                       "r"(smem_addr(ddx + (t + odd) * Sh::kPairs + my_slot)),
+                       "f"(keep.x), "f"(keep.y));
+      }
+    }
+    if (p.seg.ckpt_slots) {
+      const int end = at + TT;
+      const int ck = end <= q.hi ? checkpoint_slot(p.seg, q.i, q.p0, end) : -1;
+      if (!LOCAL && ck >= 0) store_state(p.pool + ck * row);
+    }
+    __syncthreads();
+    if (!LOCAL) {
+#pragma unroll
+      for (int k = 0; k < NI; ++k) {
+        const int it = tid + k * kThreads;
+        if (ITEMS % kThreads != 0 && it >= ITEMS) break;
+        const int t = it / NC, cv = it % NC, c = cv * V;
+        if (at + t < q.lo || at + t >= q.hi || c >= nch) continue;
+        float x[V], z[V], o[V];
+        const uint4 *from = raw + stage * TENSORS * ITEMS + it;
+        InVec<T>::load(reinterpret_cast<const T *>(from), x);
+        if (gate) InVec<T>::load(reinterpret_cast<const T *>(from + 2 * ITEMS), z);
+#pragma unroll
+        for (int u = 0; u < KP; ++u) {
+          const float2 w = *reinterpret_cast<const float2 *>(ddx + t * Sh::kPairs + slot_of(u, cv));
+          o[2 * u] = w.x;
+          o[2 * u + 1] = w.y;
+        }
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+          o[u] = fmaf(sskip[c + u], x[u], o[u]);
+          if (gate) o[u] *= silu_f(z[u]);
+        }
+        T *to = y + (at + t) * p.ys + c;
+        if (VEC) {
+          store_elems<T, V>(to, o);
+        } else {
+#pragma unroll
+          for (int u = 0; u < V; ++u)
+            if (c + u < nch) to[u] = out_scalar<T>(o[u]);
+        }
+      }
+    }
+  }
+  if (LOCAL) store_carry(q.v0 + q.k + 1, sum);
+  else if (q.hi == s.len) store_state(mine);
+}
+
+template <typename T, int S, bool LOCAL>
+constexpr size_t smem_bytes() {
+  using Sh = Shape<S>;
+  const size_t items = Sh::kTile * Sh::kChans * sizeof(T);
+  return 2 * (LOCAL ? 2 : 3) * items + Sh::kTile * Sh::kPairs * sizeof(float4) +
+         (LOCAL ? 1 : 2) * Sh::kTile * S * sizeof(float2) + 2 * Sh::kChans * sizeof(float);
+}
+
+int blocks_of_row(int C, int S, int G) {
+  const int chans = 2 * kThreads / (S / kStates);
+  return G * ((C / G + chans - 1) / chans);
+}
+
+// Tokens of a part, 0 to walk segments whole.  A part is an equal share of
+// the batch's work for 152 SMs of four blocks, so a batch that fills them
+// anyway is not cut, and a long segment beside short ones is.
+int part_tokens(int N, int B, int C, int S, int G) {
+  const long long nblk = blocks_of_row(C, S, G), room = 152 * 4;
+  long long part = ((long long)N * nblk + room - 1) / room;
+  part = (part + kAlign - 1) / kAlign * kAlign;
+  if (part < 128) part = 128;
+  if (part >= N) return 0;
+  while (((long long)N / part + 2LL * B) * nblk > 0x7fffffffLL) part *= 2;
+  return (int)part;
+}
+
+template <typename T, int S, bool VEC, bool LOCAL>
+cudaError_t launch_pass(const ScanParams &p, int nblk, int parts, cudaStream_t st) {
+  constexpr size_t smem = smem_bytes<T, S, LOCAL>();
+  auto *kernel = scan_prefill_kernel<T, S, VEC, LOCAL>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<(unsigned)((long long)nblk * parts), kThreads, smem, st>>>(p, nblk);
+  return cudaGetLastError();
+}
+
+template <typename T, int S, bool VEC>
+cudaError_t launch_prefill_v(ScanParams p, cudaStream_t st) {
+  const int nblk = blocks_of_row(p.C_, S, p.G);
+  p.part = p.ws ? part_tokens(p.seg.N, p.seg.B, p.C_, S, p.G) : 0;
+  if (!p.part) return launch_pass<T, S, VEC, false>(p, nblk, p.seg.B, st);
+  const int parts = p.seg.N / p.part + 2 * p.seg.B;
+  const cudaError_t e = launch_pass<T, S, VEC, true>(p, nblk, parts, st);
+  return e != cudaSuccess ? e : launch_pass<T, S, VEC, false>(p, nblk, parts, st);
+}
+
+template <typename T, int S>
+cudaError_t launch_prefill_s(const ScanParams &p, cudaStream_t st) {
+  constexpr int V = InVec<T>::kElems;
+  uintptr_t bits = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.dt) |
+                   reinterpret_cast<uintptr_t>(p.z) | reinterpret_cast<uintptr_t>(p.y);
+  bits |= (uintptr_t)((p.xs | p.dts | p.ys | (p.z ? p.zs : 0)) * (long long)sizeof(T));
+  const bool vec = (bits & 15) == 0 && (p.C_ / p.G) % V == 0;
+  return vec ? launch_prefill_v<T, S, true>(p, st) : launch_prefill_v<T, S, false>(p, st);
+}
+
+template <typename T>
+cudaError_t launch_prefill_t(const ScanParams &p, cudaStream_t st) {
+  switch (p.S) {
+    case 16: return launch_prefill_s<T, 16>(p, st);
+    case 32: return launch_prefill_s<T, 32>(p, st);
+    case 64: return launch_prefill_s<T, 64>(p, st);
+    default: return launch_prefill_s<T, 128>(p, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_scan_prefill(const ScanParams &p, kda_dtype dt, cudaStream_t s) {
+  return dt == KDA_F32 ? launch_prefill_t<float>(p, s) : launch_prefill_t<__nv_bfloat16>(p, s);
+}
+
+size_t scan_workspace_floats(int N, int B, int C, int S, int G) {
+  const int part = part_tokens(N, B, C, S, G);
+  if (!part) return 0;
+  return ((size_t)N / part + 2 * (size_t)B) * blocks_of_row(C, S, G) * kCarry * kThreads;
+}
+
+}  // namespace kda
