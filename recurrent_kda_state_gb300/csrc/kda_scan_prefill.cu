@@ -7,8 +7,7 @@
 // two neighbouring channels in registers (S / 8 lanes a channel pair) and the
 // pair's values travel as packed fp32 pairs, so one instruction serves both.
 // A block stages tiles of tokens in shared memory: delta and delta x per
-// channel (the softplus is computed once, not once per lane), B and C as
-// duplicated pairs.  The next tile's rows arrive by asynchronous copies
+// channel (the softplus is computed once, not once per lane), B and C in fp32.  The next tile's rows arrive by asynchronous copies
 // meanwhile.  After a tile its y, summed over the channel's lanes, goes back
 // through shared memory to the thread that staged the row, which adds the
 // skip, applies the gate and writes 16 bytes.
@@ -37,38 +36,6 @@ struct Shape {
   static constexpr int kChans = 2 * kPairs;
   static constexpr int kTile = S <= 32 ? 16 : 8;
 };
-
-// Packed fp32 pairs: the two channels of a thread.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pack2(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(f2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 exp2_2(f2 v) {
-  const float2 e = unpack2(v);
-  return pack2(ex2f(e.x), ex2f(e.y));
-}
 
 // A log2(e), -inf held at the lowest finite value: a token that pads a tile has
 // delta = 0, and 0 * -inf would be NaN.
@@ -146,9 +113,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
   extern __shared__ __align__(16) unsigned char smem[];
   uint4 *raw = reinterpret_cast<uint4 *>(smem);  // [stage][x, dt, z][ITEMS]
   float4 *ddx = reinterpret_cast<float4 *>(raw + 2 * TENSORS * ITEMS);  // [TT][kPairs]
-  float2 *sb = reinterpret_cast<float2 *>(ddx + TT * Sh::kPairs);       // [TT][S]
-  float2 *sc = sb + TT * S;
-  float *sskip = reinterpret_cast<float *>(LOCAL ? sc : sc + TT * S);   // [kChans]
+  float *sb = reinterpret_cast<float *>(ddx + TT * Sh::kPairs);         // [TT][S]
+  float *sc = sb + TT * S;
+  float *sskip = LOCAL ? sc : sc + TT * S;                              // [kChans]
   float *sbias = sskip + Sh::kChans;
 
   const int tid = threadIdx.x;
@@ -168,39 +135,44 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     sbias[c] = p.dtb && c < nch ? p.dtb[c0 + c] : 0.0f;
   }
 
-  // this thread's pair of channels and states 2 (l + kLanes j) + {0, 1}
+  // this thread's pair of channels and states 4 (l + kLanes j) + {0 .. 3}
   const int l = tid % Sh::kLanes, pr = tid / Sh::kLanes;
   const int ca = c0 + min(2 * pr, nch - 1), cb = c0 + min(2 * pr + 1, nch - 1);
   f2 a[kStates], h[kStates];
 #pragma unroll
-  for (int j = 0; j < kStates / 2; ++j) {
-    const int n = 2 * (l + Sh::kLanes * j);
-    const float2 x = *reinterpret_cast<const float2 *>(p.A + (long long)ca * S + n);
-    const float2 y = *reinterpret_cast<const float2 *>(p.A + (long long)cb * S + n);
-    a[2 * j] = pack2(exponent_scale(x.x), exponent_scale(y.x));
-    a[2 * j + 1] = pack2(exponent_scale(x.y), exponent_scale(y.y));
+  for (int j = 0; j < kStates / 4; ++j) {
+    const int n = 4 * (l + Sh::kLanes * j);
+    const float4 x = *reinterpret_cast<const float4 *>(p.A + (long long)ca * S + n);
+    const float4 y = *reinterpret_cast<const float4 *>(p.A + (long long)cb * S + n);
+    a[4 * j] = pack2(exponent_scale(x.x), exponent_scale(y.x));
+    a[4 * j + 1] = pack2(exponent_scale(x.y), exponent_scale(y.y));
+    a[4 * j + 2] = pack2(exponent_scale(x.z), exponent_scale(y.z));
+    a[4 * j + 3] = pack2(exponent_scale(x.w), exponent_scale(y.w));
   }
 
   const long long row = (long long)p.C_ * S;
   auto load_state = [&](const float *from) {
 #pragma unroll
-    for (int j = 0; j < kStates / 2; ++j) {
-      const int n = 2 * (l + Sh::kLanes * j);
-      const float2 x = *reinterpret_cast<const float2 *>(from + (long long)ca * S + n);
-      const float2 y = *reinterpret_cast<const float2 *>(from + (long long)cb * S + n);
-      h[2 * j] = pack2(x.x, y.x);
-      h[2 * j + 1] = pack2(x.y, y.y);
+    for (int j = 0; j < kStates / 4; ++j) {
+      const int n = 4 * (l + Sh::kLanes * j);
+      const float4 x = *reinterpret_cast<const float4 *>(from + (long long)ca * S + n);
+      const float4 y = *reinterpret_cast<const float4 *>(from + (long long)cb * S + n);
+      h[4 * j] = pack2(x.x, y.x);
+      h[4 * j + 1] = pack2(x.y, y.y);
+      h[4 * j + 2] = pack2(x.z, y.z);
+      h[4 * j + 3] = pack2(x.w, y.w);
     }
   };
   auto store_state = [&](float *to) {
 #pragma unroll
-    for (int j = 0; j < kStates / 2; ++j) {
-      const int n = 2 * (l + Sh::kLanes * j);
-      const float2 x = unpack2(h[2 * j]), y = unpack2(h[2 * j + 1]);
+    for (int j = 0; j < kStates / 4; ++j) {
+      const int n = 4 * (l + Sh::kLanes * j);
+      const float2 x = unpack2(h[4 * j]), y = unpack2(h[4 * j + 1]), z = unpack2(h[4 * j + 2]),
+                   w = unpack2(h[4 * j + 3]);
       if (2 * pr < nch)
-        *reinterpret_cast<float2 *>(to + (long long)ca * S + n) = make_float2(x.x, y.x);
+        *reinterpret_cast<float4 *>(to + (long long)ca * S + n) = make_float4(x.x, y.x, z.x, w.x);
       if (2 * pr + 1 < nch)
-        *reinterpret_cast<float2 *>(to + (long long)cb * S + n) = make_float2(x.y, y.y);
+        *reinterpret_cast<float4 *>(to + (long long)cb * S + n) = make_float4(x.y, y.y, z.y, w.y);
     }
   };
   // carry slot of a part: [value][thread], so that warps move whole lines
@@ -311,33 +283,33 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
   __syncthreads();  // sskip, sbias
   for (int j = 0; j < tiles; ++j) {
     const int at = q.at + j * TT, stage = j & 1;
+    const bool whole = at >= q.lo && at + TT <= q.hi;
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
       const int it = tid + k * kThreads;
       if (ITEMS % kThreads != 0 && it >= ITEMS) break;
       const int t = it / NC, cv = it % NC;
-      const bool on = at + t >= q.lo && at + t < q.hi;
-      float x[V], d[V];
       const uint4 *from = raw + stage * TENSORS * ITEMS + it;
-      InVec<T>::load(reinterpret_cast<const T *>(from), x);
-      InVec<T>::load(reinterpret_cast<const T *>(from + ITEMS), d);
+      f2 x[KP], d[KP];
+      load_pairs<T>(from, x);
+      load_pairs<T>(from + ITEMS, d);
 #pragma unroll
-      for (int u = 0; u < V; ++u) {
-        d[u] += sbias[cv * V + u];
-        if (p.softplus) d[u] = softplus_f(d[u]);
-        d[u] = on ? d[u] : 0.0f;  // outside the part: the state stays as it is
-        x[u] *= d[u];
+      for (int u = 0; u < KP; ++u) {
+        d[u] = add2(d[u], *reinterpret_cast<const f2 *>(sbias + cv * V + 2 * u));
+        if (p.softplus) d[u] = softplus2(d[u]);
+        // outside the part (x is zero there): the state stays as it is
+        if (!whole && !(at + t >= q.lo && at + t < q.hi)) d[u] = 0;
+        ulonglong2 w;
+        w.x = d[u];
+        w.y = mul2(d[u], x[u]);
+        *reinterpret_cast<ulonglong2 *>(ddx + t * Sh::kPairs + slot_of(u, cv)) = w;
       }
-#pragma unroll
-      for (int u = 0; u < KP; ++u)
-        ddx[t * Sh::kPairs + slot_of(u, cv)] =
-            make_float4(d[2 * u], d[2 * u + 1], x[2 * u], x[2 * u + 1]);
     }
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
-      sb[tid + k * kThreads] = make_float2(rb[k], rb[k]);
-      if (!LOCAL) sc[tid + k * kThreads] = make_float2(rc[k], rc[k]);
+      sb[tid + k * kThreads] = rb[k];
+      if (!LOCAL) sc[tid + k * kThreads] = rc[k];
     }
     if (j + 1 < tiles) {
       fetch_rows(at + TT, stage ^ 1);
@@ -350,13 +322,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
 #pragma unroll 2
       for (int t = 0; t < nt; ++t) {
         const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(ddx + t * Sh::kPairs + my_slot);
-        const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(sb + t * S) + l;
+        const float4 *bp = reinterpret_cast<const float4 *>(sb + t * S) + l;
         sum = add2(sum, w.x);
 #pragma unroll
-        for (int n = 0; n < kStates; n += 2) {
-          const ulonglong2 b = bp[Sh::kLanes * n / 2];
-          h[n] = fma2(exp2_2(mul2(w.x, a[n])), h[n], mul2(w.y, b.x));
-          h[n + 1] = fma2(exp2_2(mul2(w.x, a[n + 1])), h[n + 1], mul2(w.y, b.y));
+        for (int n = 0; n < kStates; n += 4) {
+          const float4 b4 = bp[Sh::kLanes * n / 4];
+          const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            h[n + e] = fma2(exp2_2(mul2(w.x, a[n + e])), h[n + e], mul2(w.y, both(b[e])));
         }
       }
     } else {
@@ -367,16 +341,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
         for (int u = 0; u < 2; ++u) {
           const ulonglong2 w =
               *reinterpret_cast<const ulonglong2 *>(ddx + (t + u) * Sh::kPairs + my_slot);
-          const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(sb + (t + u) * S) + l;
-          const ulonglong2 *cp = reinterpret_cast<const ulonglong2 *>(sc + (t + u) * S) + l;
+          const float4 *bp = reinterpret_cast<const float4 *>(sb + (t + u) * S) + l;
+          const float4 *cp = reinterpret_cast<const float4 *>(sc + (t + u) * S) + l;
           f2 o0 = 0, o1 = 0;
 #pragma unroll
-          for (int n = 0; n < kStates; n += 2) {
-            const ulonglong2 b = bp[Sh::kLanes * n / 2], c = cp[Sh::kLanes * n / 2];
-            h[n] = fma2(exp2_2(mul2(w.x, a[n])), h[n], mul2(w.y, b.x));
-            h[n + 1] = fma2(exp2_2(mul2(w.x, a[n + 1])), h[n + 1], mul2(w.y, b.y));
-            o0 = fma2(c.x, h[n], o0);
-            o1 = fma2(c.y, h[n + 1], o1);
+          for (int n = 0; n < kStates; n += 4) {
+            const float4 b4 = bp[Sh::kLanes * n / 4], c4 = cp[Sh::kLanes * n / 4];
+            const float b[4] = {b4.x, b4.y, b4.z, b4.w}, c[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h[n + e] = fma2(exp2_2(mul2(w.x, a[n + e])), h[n + e], mul2(w.y, both(b[e])));
+              f2 &to = e & 1 ? o1 : o0;
+              to = fma2(both(c[e]), h[n + e], to);
+            }
           }
           o[u] = add2(o0, o1);
         }
@@ -414,20 +391,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
         if (ITEMS % kThreads != 0 && it >= ITEMS) break;
         const int t = it / NC, cv = it % NC, c = cv * V;
         if (at + t < q.lo || at + t >= q.hi || c >= nch) continue;
-        float x[V], z[V], o[V];
         const uint4 *from = raw + stage * TENSORS * ITEMS + it;
-        InVec<T>::load(reinterpret_cast<const T *>(from), x);
-        if (gate) InVec<T>::load(reinterpret_cast<const T *>(from + 2 * ITEMS), z);
+        f2 x[KP], z[KP];
+        float o[V];
+        load_pairs<T>(from, x);
+        if (gate) load_pairs<T>(from + 2 * ITEMS, z);
 #pragma unroll
         for (int u = 0; u < KP; ++u) {
-          const float2 w = *reinterpret_cast<const float2 *>(ddx + t * Sh::kPairs + slot_of(u, cv));
-          o[2 * u] = w.x;
-          o[2 * u + 1] = w.y;
-        }
-#pragma unroll
-        for (int u = 0; u < V; ++u) {
-          o[u] = fmaf(sskip[c + u], x[u], o[u]);
-          if (gate) o[u] *= silu_f(z[u]);
+          f2 w = *reinterpret_cast<const f2 *>(ddx + t * Sh::kPairs + slot_of(u, cv));
+          w = fma2(*reinterpret_cast<const f2 *>(sskip + c + 2 * u), x[u], w);
+          if (gate) w = mul2(w, silu2(z[u]));
+          const float2 r = unpack2(w);
+          o[2 * u] = r.x;
+          o[2 * u + 1] = r.y;
         }
         T *to = y + (at + t) * p.ys + c;
         if (VEC) {
@@ -449,7 +425,7 @@ constexpr size_t smem_bytes() {
   using Sh = Shape<S>;
   const size_t items = Sh::kTile * Sh::kChans * sizeof(T);
   return 2 * (LOCAL ? 2 : 3) * items + Sh::kTile * Sh::kPairs * sizeof(float4) +
-         (LOCAL ? 1 : 2) * Sh::kTile * S * sizeof(float2) + 2 * Sh::kChans * sizeof(float);
+         (LOCAL ? 1 : 2) * Sh::kTile * S * sizeof(float) + 2 * Sh::kChans * sizeof(float);
 }
 
 int blocks_of_row(int C, int S, int G) {
