@@ -24,7 +24,20 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kStates = 8;        // states of a thread, for each of two channels
+#ifndef KST
+#define KST 8
+#endif
+#ifndef MINB
+#define MINB 4
+#endif
+#ifndef PIPE
+#define PIPE 0
+#endif
+#ifndef UNR
+#define UNR 2
+#endif
+constexpr int kUnr = UNR;
+constexpr int kStates = KST;        // states of a thread, for each of two channels
 constexpr int kAlign = 16;        // parts and tiles start on multiples of this
 constexpr int kCarry = 2 * kStates + 2;  // floats a thread carries between parts
 
@@ -103,7 +116,7 @@ __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, S
 
 // LOCAL: the first launch (end states of the parts, no outputs).
 template <typename T, int S, bool VEC, bool LOCAL>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? MINB : 3)
     scan_prefill_kernel(const ScanParams p, int nblk) {
   using Sh = Shape<S>;
   constexpr int TT = Sh::kTile, V = InVec<T>::kElems, NC = Sh::kChans / V, KP = V / 2;
@@ -130,9 +143,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
   const int c0 = g * per + (blk % bpg) * Sh::kChans;
   const int nch = min(Sh::kChans, (g + 1) * per - c0);
 
-  for (int c = tid; c < Sh::kChans; c += kThreads) {
-    sskip[c] = p.D && c < nch ? p.D[c0 + c] : 0.0f;
-    sbias[c] = p.dtb && c < nch ? p.dtb[c0 + c] : 0.0f;
+  for (int c = tid; c < Sh::kChans; c += kThreads) {  // pairs, by (pair of a vector, vector)
+    const int at = 2 * ((c % V) / 2 * NC + c / V) + c % 2;
+    sskip[at] = p.D && c < nch ? p.D[c0 + c] : 0.0f;
+    sbias[at] = p.dtb && c < nch ? p.dtb[c0 + c] : 0.0f;
   }
 
   // this thread's pair of channels and states 4 (l + kLanes j) + {0 .. 3}
@@ -192,38 +206,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     w[(2 * kStates + 1) * kThreads] = x.y;
   };
 
-  // The state at the part's start.  The carry slot of part 0 holds the slot's
-  // own state, since the last part replaces that; slot k holds part k - 1's
-  // end (for k = 1 the whole state, beyond from a zero start) and its sum of
-  // delta.
-  float *mine = p.pool + s.slot * row;
-  if (LOCAL) {
-    if (q.k == 0) {
-      load_state(mine);
-      store_carry(q.v0, 0);
-    } else {
-#pragma unroll
-      for (int n = 0; n < kStates; ++n) h[n] = 0;
-    }
-  } else if (q.count == 1) {
-    load_state(mine);
-  } else {
-    const int first = q.k ? 1 : 0;
-#pragma unroll
-    for (int n = 0; n < kStates; ++n) {
-      const float *w = carry(q.v0 + first);
-      h[n] = pack2(w[(2 * n) * kThreads], w[(2 * n + 1) * kThreads]);
-    }
-    for (int k = 2; k <= q.k; ++k) {
-      const float *w = carry(q.v0 + k);
-      const f2 d = pack2(w[2 * kStates * kThreads], w[(2 * kStates + 1) * kThreads]);
-#pragma unroll
-      for (int n = 0; n < kStates; ++n)
-        h[n] = fma2(exp2_2(mul2(d, a[n])), h[n],
-                    pack2(w[(2 * n) * kThreads], w[(2 * n + 1) * kThreads]));
-    }
-  }
-
   const T *rows[3] = {static_cast<const T *>(p.x) + s.begin * p.xs + c0,
                       static_cast<const T *>(p.dt) + s.begin * p.dts + c0,
                       static_cast<const T *>(p.z) + s.begin * p.zs + c0};
@@ -259,14 +241,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  float rb[NB], rc[NB];
+  T rb[NB], rc[NB];  // converted when they are staged, not when they are asked for
   auto fetch_bc = [&](int at) {
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int e = tid + k * kThreads, t = at + e / S;
       const bool on = t >= q.lo && t < q.hi;
-      rb[k] = on ? in_scalar<T>(B + t * p.bs + e % S) : 0.0f;
-      if (!LOCAL) rc[k] = on ? in_scalar<T>(C + t * p.cs + e % S) : 0.0f;
+      rb[k] = on ? B[t * p.bs + e % S] : out_scalar<T>(0.0f);
+      if (!LOCAL) rc[k] = on ? C[t * p.cs + e % S] : out_scalar<T>(0.0f);
     }
   };
   // slot of a channel pair in a row of ddx: written four (two) pairs an item
@@ -280,6 +262,39 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
   const int tiles = (q.hi - q.at + TT - 1) / TT;
   fetch_rows(q.at, 0);
   fetch_bc(q.at);
+
+  // The state at the part's start.  The carry slot of part 0 holds the slot's
+  // own state, since the last part replaces that; slot k holds part k - 1's
+  // end (for k = 1 the whole state, beyond from a zero start) and its sum of
+  // delta.
+  float *mine = p.pool + s.slot * row;
+  if (LOCAL) {
+    if (q.k == 0) {
+      load_state(mine);
+      store_carry(q.v0, 0);
+    } else {
+#pragma unroll
+      for (int n = 0; n < kStates; ++n) h[n] = 0;
+    }
+  } else if (q.count == 1) {
+    load_state(mine);
+  } else {
+    const int first = q.k ? 1 : 0;
+#pragma unroll
+    for (int n = 0; n < kStates; ++n) {
+      const float *w = carry(q.v0 + first);
+      h[n] = pack2(w[(2 * n) * kThreads], w[(2 * n + 1) * kThreads]);
+    }
+#pragma unroll 4
+    for (int k = 2; k <= q.k; ++k) {
+      const float *w = carry(q.v0 + k);
+      const f2 d = pack2(w[2 * kStates * kThreads], w[(2 * kStates + 1) * kThreads]);
+#pragma unroll
+      for (int n = 0; n < kStates; ++n)
+        h[n] = fma2(exp2_2(mul2(d, a[n])), h[n],
+                    pack2(w[(2 * n) * kThreads], w[(2 * n + 1) * kThreads]));
+    }
+  }
   __syncthreads();  // sskip, sbias
   for (int j = 0; j < tiles; ++j) {
     const int at = q.at + j * TT, stage = j & 1;
@@ -296,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
       load_pairs<T>(from + ITEMS, d);
 #pragma unroll
       for (int u = 0; u < KP; ++u) {
-        d[u] = add2(d[u], *reinterpret_cast<const f2 *>(sbias + cv * V + 2 * u));
+        d[u] = add2(d[u], *reinterpret_cast<const f2 *>(sbias + 2 * (u * NC + cv)));
         if (p.softplus) d[u] = softplus2(d[u]);
         // outside the part (x is zero there): the state stays as it is
         if (!whole && !(at + t >= q.lo && at + t < q.hi)) d[u] = 0;
@@ -308,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     }
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
-      sb[tid + k * kThreads] = rb[k];
-      if (!LOCAL) sc[tid + k * kThreads] = rc[k];
+      sb[tid + k * kThreads] = in_scalar<T>(&rb[k]);
+      if (!LOCAL) sc[tid + k * kThreads] = in_scalar<T>(&rc[k]);
     }
     if (j + 1 < tiles) {
       fetch_rows(at + TT, stage ^ 1);
@@ -319,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
 
     const int nt = min(TT, q.hi - at);
     if (LOCAL) {
-#pragma unroll 2
+#pragma unroll (kUnr)
       for (int t = 0; t < nt; ++t) {
         const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(ddx + t * Sh::kPairs + my_slot);
         const float4 *bp = reinterpret_cast<const float4 *>(sb + t * S) + l;
@@ -334,7 +349,46 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
         }
       }
     } else {
-#pragma unroll 2
+#if PIPE
+      // The exponentials of a token are under way while the one before it is
+      // used, so the h chain never waits for the special function unit.
+      f2 e0[kStates], e1[kStates];
+      auto delta_of = [&](int t) {
+        return *reinterpret_cast<const ulonglong2 *>(ddx + t * Sh::kPairs + my_slot);
+      };
+      auto decays = [&](const ulonglong2 &w, f2 *e) {
+#pragma unroll
+        for (int n = 0; n < kStates; ++n) e[n] = exp2_2(mul2(w.x, a[n]));
+      };
+      auto token = [&](int t, const ulonglong2 &w, const f2 *e) {
+        const float4 *bp = reinterpret_cast<const float4 *>(sb + t * S) + l;
+        const float4 *cp = reinterpret_cast<const float4 *>(sc + t * S) + l;
+        f2 o[2] = {0, 0};
+#pragma unroll
+        for (int n = 0; n < kStates; n += 4) {
+          const float4 b4 = bp[Sh::kLanes * n / 4], c4 = cp[Sh::kLanes * n / 4];
+          const float b[4] = {b4.x, b4.y, b4.z, b4.w}, c[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h[n + i] = fma2(e[n + i], h[n + i], mul2(w.y, both(b[i])));
+            o[i & 1] = fma2(both(c[i]), h[n + i], o[i & 1]);
+          }
+        }
+        return add2(o[0], o[1]);
+      };
+      ulonglong2 w0 = delta_of(0), w1;
+      decays(w0, e0);
+#pragma unroll (kUnr)
+      for (int t = 0; t < nt; t += 2) {  // TT is even; a token past nt is neutral
+        f2 o[2];
+        w1 = delta_of(t + 1);
+        decays(w1, e1);
+        o[0] = token(t, w0, e0);
+        w0 = delta_of(min(t + 2, TT - 1));  // past the last one: not used
+        decays(w0, e0);
+        o[1] = token(t + 1, w1, e1);
+#else
+#pragma unroll (kUnr)
       for (int t = 0; t < nt; t += 2) {  // TT is even; a token past nt is neutral
         f2 o[2];
 #pragma unroll
@@ -357,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
           }
           o[u] = add2(o0, o1);
         }
+#endif
         // sum over the lanes: neighbours exchange one token each, so that an
         // even lane ends with token t, an odd one with t + 1
         const int odd = l & 1;
@@ -369,12 +424,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
           keep.x += __shfl_xor_sync(~0u, keep.x, m);
           keep.y += __shfl_xor_sync(~0u, keep.y, m);
         }
-        // y takes the place of delta, which all lanes of the pair have read
-        // (their shuffles depend on it).  No "memory" clobber: no load before
+        // y takes the place of delta (delta x where t is odd: other banks), which
+        // all lanes of the pair have read (their shuffles depend on it).  No "memory" clobber: no load before
         // the barrier reads what this writes, so loads may pass it.
         if (l < 2)
           asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::
-                       "r"(smem_addr(ddx + (t + odd) * Sh::kPairs + my_slot)),
+                       "r"(smem_addr(ddx + (t + odd) * Sh::kPairs + my_slot) + 8 * odd),
                        "f"(keep.x), "f"(keep.y));
       }
     }
@@ -398,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
         if (gate) load_pairs<T>(from + 2 * ITEMS, z);
 #pragma unroll
         for (int u = 0; u < KP; ++u) {
-          f2 w = *reinterpret_cast<const f2 *>(ddx + t * Sh::kPairs + slot_of(u, cv));
-          w = fma2(*reinterpret_cast<const f2 *>(sskip + c + 2 * u), x[u], w);
+          f2 w = reinterpret_cast<const f2 *>(ddx + t * Sh::kPairs + slot_of(u, cv))[t & 1];
+          w = fma2(*reinterpret_cast<const f2 *>(sskip + 2 * (u * NC + cv)), x[u], w);
           if (gate) w = mul2(w, silu2(z[u]));
           const float2 r = unpack2(w);
           o[2 * u] = r.x;
@@ -437,7 +492,7 @@ int blocks_of_row(int C, int S, int G) {
 // the batch's work for 152 SMs of four blocks, so a batch that fills them
 // anyway is not cut, and a long segment beside short ones is.
 int part_tokens(int N, int B, int C, int S, int G) {
-  const long long nblk = blocks_of_row(C, S, G), room = 152 * 4;
+  const long long nblk = blocks_of_row(C, S, G), room = 152 * MINB;
   long long part = ((long long)N * nblk + room - 1) / room;
   part = (part + kAlign - 1) / kAlign * kAlign;
   if (part < 128) part = 128;

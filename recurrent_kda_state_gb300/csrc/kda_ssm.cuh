@@ -123,25 +123,28 @@ constexpr float kLog2e = 1.4426950408889634f;
 // value in fp32; -inf gives NaN, as -inf / (1 + inf) does.
 __device__ __forceinline__ float silu_f(float v) { return v * rcpf(1.0f + ex2f(-kLog2e * v)); }
 
-// log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v| in (0, 1], with
-// log1p(u) = 2 artanh(s), s = u / (2 + u) <= 1/3, and artanh(s) / s a
-// polynomial of degree 4 in s^2: its Chebyshev expansion on [0, 1/9], within
-// 8e-9.  Relative, not only absolute, accuracy matters: time steps of 1e-3 and
-// less are ordinary.
-__host__ __device__ constexpr float artanh_coef(int i) {
-  return i == 0   ? 1.0f
-         : i == 1 ? 0.33333158f
-         : i == 2 ? 0.20012426f
-         : i == 3 ? 0.13980709f
-                  : 0.14087328f;
+// log(1 + e^v) = max(v, 0) + log1p(u), u = e^-|v| in (0, 1], with log1p(u) / u
+// a polynomial of degree 8: its Chebyshev expansion on [0, 1], within 4e-8.
+// Relative, not only absolute, accuracy matters: time steps of 1e-3 and less
+// are ordinary.  No division: the special function unit is what the scan
+// needs most.
+__host__ __device__ constexpr float log1p_coef(int i) {
+  return i == 0   ? 0.99999994f
+         : i == 1 ? -0.49999437f
+         : i == 2 ? 0.33317935f
+         : i == 3 ? -0.24833946f
+         : i == 4 ? 0.19071309f
+         : i == 5 ? -0.13590600f
+         : i == 6 ? 0.077380739f
+         : i == 7 ? -0.028991956f
+                  : 0.0051058256f;
 }
 __device__ __forceinline__ float softplus_f(float v) {
   const float u = ex2f(-kLog2e * fabsf(v));
-  const float s = u * rcpf(2.0f + u), q = s * s;
-  float r = artanh_coef(4);
+  float r = log1p_coef(8);
 #pragma unroll
-  for (int i = 3; i >= 0; --i) r = fmaf(r, q, artanh_coef(i));
-  return fmaf(2.0f * s, r, fmaxf(v, 0.0f));
+  for (int i = 7; i >= 0; --i) r = fmaf(r, u, log1p_coef(i));
+  return fmaf(u, r, fmaxf(v, 0.0f));
 }
 
 // Packed fp32 pairs: one instruction for two values.
@@ -181,12 +184,10 @@ __device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
 __device__ __forceinline__ f2 softplus2(f2 v) {
   const float2 w = unpack2(v);
   const f2 u = exp2_2(mul2(pack2(fabsf(w.x), fabsf(w.y)), both(-kLog2e)));
-  const float2 d = unpack2(add2(u, both(2.0f)));
-  const f2 s = mul2(u, pack2(rcpf(d.x), rcpf(d.y))), q = mul2(s, s);
-  f2 r = both(artanh_coef(4));
+  f2 r = both(log1p_coef(8));
 #pragma unroll
-  for (int i = 3; i >= 0; --i) r = fma2(r, q, both(artanh_coef(i)));
-  return fma2(add2(s, s), r, pack2(fmaxf(w.x, 0.0f), fmaxf(w.y, 0.0f)));
+  for (int i = 7; i >= 0; --i) r = fma2(r, u, both(log1p_coef(i)));
+  return fma2(u, r, pack2(fmaxf(w.x, 0.0f), fmaxf(w.y, 0.0f)));
 }
 __device__ __forceinline__ f2 silu2(f2 v) {
   const float2 d = unpack2(add2(exp2_2(mul2(v, both(-kLog2e))), both(1.0f)));
