@@ -24,30 +24,24 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-#ifndef KST
-#define KST 8
-#endif
 #ifndef MINB
 #define MINB 4
 #endif
-#ifndef PIPE
-#define PIPE 0
-#endif
-#ifndef UNR
-#define UNR 2
-#endif
-constexpr int kUnr = UNR;
-constexpr int kStates = KST;        // states of a thread, for each of two channels
+constexpr int kStates = 8;          // states of a thread, for each of two channels
 constexpr int kAlign = 16;        // parts and tiles start on multiples of this
 constexpr int kCarry = 2 * kStates + 2;  // floats a thread carries between parts
 
-// Tokens of a tile: 16, 8 for the wide states whose B and C rows are long.
-template <int S>
+constexpr int kTile = 16;         // tokens of a tile
+
+template <typename T, int S>
 struct Shape {
-  static constexpr int kLanes = S / kStates;         // of a channel pair
-  static constexpr int kPairs = kThreads / kLanes;   // of a block
+  static constexpr int kLanes = S / kStates;        // of a channel pair
+  static constexpr int kPairs = kThreads / kLanes;  // of a block
   static constexpr int kChans = 2 * kPairs;
-  static constexpr int kTile = S <= 32 ? 16 : 8;
+  // bytes of a staged row: the padding lets kLanes tokens of a warp's pairs be
+  // read without bank conflicts
+  static constexpr int kPad = 64 * (int)sizeof(T) / kLanes;
+  static constexpr int kPitch = kChans * (int)sizeof(T) + (kPad < 16 ? 16 : kPad);
 };
 
 // A log2(e), -inf held at the lowest finite value: a token that pads a tile has
@@ -118,18 +112,17 @@ __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, S
 template <typename T, int S, bool VEC, bool LOCAL>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? MINB : 3)
     scan_prefill_kernel(const ScanParams p, int nblk) {
-  using Sh = Shape<S>;
-  constexpr int TT = Sh::kTile, V = InVec<T>::kElems, NC = Sh::kChans / V, KP = V / 2;
-  constexpr int ITEMS = TT * NC, NI = (ITEMS + kThreads - 1) / kThreads;
-  constexpr int NB = TT * S / kThreads;
+  using Sh = Shape<T, S>;
+  constexpr int V = InVec<T>::kElems, NC = Sh::kChans / V, L = Sh::kLanes;
+  constexpr int ITEMS = kTile * NC, NI = (ITEMS + kThreads - 1) / kThreads;
+  constexpr int NB = kTile * S / kThreads;
   constexpr int TENSORS = LOCAL ? 2 : 3;
+  constexpr int kRaw = kTile * Sh::kPitch;  // bytes of a tensor's tile
   extern __shared__ __align__(16) unsigned char smem[];
-  uint4 *raw = reinterpret_cast<uint4 *>(smem);  // [stage][x, dt, z][ITEMS]
-  float4 *ddx = reinterpret_cast<float4 *>(raw + 2 * TENSORS * ITEMS);  // [TT][kPairs]
-  float *sb = reinterpret_cast<float *>(ddx + TT * Sh::kPairs);         // [TT][S]
-  float *sc = sb + TT * S;
-  float *sskip = LOCAL ? sc : sc + TT * S;                              // [kChans]
-  float *sbias = sskip + Sh::kChans;
+  unsigned char *raw = smem;                                     // [2][x, dt, z][kRaw]
+  float *sbc = reinterpret_cast<float *>(raw + 2 * TENSORS * kRaw);  // [2][B, C][kTile][S]
+  constexpr int kBC = (LOCAL ? 1 : 2) * kTile * S;
+  float4 *swarp = reinterpret_cast<float4 *>(sbc + 2 * kBC);     // [2][kThreads]
 
   const int tid = threadIdx.x;
   const int v = blockIdx.x / nblk, blk = blockIdx.x % nblk;
@@ -142,12 +135,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? MINB : 3)
   const int per = p.C_ / p.G, bpg = nblk / p.G, g = blk / bpg;
   const int c0 = g * per + (blk % bpg) * Sh::kChans;
   const int nch = min(Sh::kChans, (g + 1) * per - c0);
-
-  for (int c = tid; c < Sh::kChans; c += kThreads) {  // pairs, by (pair of a vector, vector)
-    const int at = 2 * ((c % V) / 2 * NC + c / V) + c % 2;
-    sskip[at] = p.D && c < nch ? p.D[c0 + c] : 0.0f;
-    sbias[at] = p.dtb && c < nch ? p.dtb[c0 + c] : 0.0f;
-  }
 
   // this thread's pair of channels and states 4 (l + kLanes j) + {0 .. 3}
   const int l = tid % Sh::kLanes, pr = tid / Sh::kLanes;
@@ -206,17 +193,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? MINB : 3)
     w[(2 * kStates + 1) * kThreads] = x.y;
   };
 
+  f2 bias = 0, skip = 0;
+  if (p.dtb) bias = pack2(p.dtb[ca], p.dtb[cb]);
+  if (!LOCAL && p.D) skip = pack2(p.D[ca], p.D[cb]);
+
   const T *rows[3] = {static_cast<const T *>(p.x) + s.begin * p.xs + c0,
                       static_cast<const T *>(p.dt) + s.begin * p.dts + c0,
                       static_cast<const T *>(p.z) + s.begin * p.zs + c0};
   const long long strides[3] = {p.xs, p.dts, p.zs};
   const T *B = static_cast<const T *>(p.B) + s.begin * p.bs + g * S;
   const T *C = static_cast<const T *>(p.C) + s.begin * p.cs + g * S;
-  T *y = static_cast<T *>(p.y) + s.begin * p.ys + c0;
+  T *y = static_cast<T *>(p.y) + s.begin * p.ys + c0 + 2 * pr;
   const bool gate = !LOCAL && p.z != nullptr;
 
-  // Item (t, cv): V channels of one token of the tile; staged, consumed in the
-  // epilogue and written by the same thread.
+  // 16 bytes (V channels of one token) at a time; what lies outside the part
+  // or the block's channels becomes zero
   auto fetch_rows = [&](int at, int stage) {
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
@@ -227,7 +218,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? MINB : 3)
 #pragma unroll
       for (int w = 0; w < TENSORS; ++w) {
         if (w == 2 && !gate) break;
-        uint4 *to = raw + (stage * TENSORS + w) * ITEMS + it;
+        unsigned char *to =
+            raw + (stage * TENSORS + w) * kRaw + it / NC * Sh::kPitch + it % NC * 16;
         const T *from = rows[w] + (on ? t * strides[w] + c : 0);
         if (VEC) {
           copy16(to, on ? static_cast<const void *>(from) : p.A, on);
@@ -235,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? MINB : 3)
           alignas(16) T e[V];
 #pragma unroll
           for (int u = 0; u < V; ++u) e[u] = on && c + u < nch ? from[u] : out_scalar<T>(0.0f);
-          *to = *reinterpret_cast<const uint4 *>(e);
+          *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(e);
         }
       }
     }
@@ -251,15 +243,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? MINB : 3)
       if (!LOCAL) rc[k] = on ? C[t * p.cs + e % S] : out_scalar<T>(0.0f);
     }
   };
-  // slot of a channel pair in a row of ddx: written four (two) pairs an item
-  // and read a warp's pairs in a row, both without bank conflicts
-  auto slot_of = [&](int k, int c) {  // pair KP c + k
-    return k * NC + (NC >= 8 ? c ^ ((k & 1) << 2) : c);
-  };
-  const int my_slot = slot_of(pr % KP, pr / KP);
 
   f2 sum = 0;
-  const int tiles = (q.hi - q.at + TT - 1) / TT;
+  const int tiles = (q.hi - q.at + kTile - 1) / kTile;
   fetch_rows(q.at, 0);
   fetch_bc(q.at);
 
@@ -295,180 +281,115 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? MINB : 3)
                     pack2(w[(2 * n) * kThreads], w[(2 * n + 1) * kThreads]));
     }
   }
-  __syncthreads();  // sskip, sbias
+
   for (int j = 0; j < tiles; ++j) {
-    const int at = q.at + j * TT, stage = j & 1;
-    const bool whole = at >= q.lo && at + TT <= q.hi;
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-#pragma unroll
-    for (int k = 0; k < NI; ++k) {
-      const int it = tid + k * kThreads;
-      if (ITEMS % kThreads != 0 && it >= ITEMS) break;
-      const int t = it / NC, cv = it % NC;
-      const uint4 *from = raw + stage * TENSORS * ITEMS + it;
-      f2 x[KP], d[KP];
-      load_pairs<T>(from, x);
-      load_pairs<T>(from + ITEMS, d);
-#pragma unroll
-      for (int u = 0; u < KP; ++u) {
-        d[u] = add2(d[u], *reinterpret_cast<const f2 *>(sbias + 2 * (u * NC + cv)));
-        if (p.softplus) d[u] = softplus2(d[u]);
-        // outside the part (x is zero there): the state stays as it is
-        if (!whole && !(at + t >= q.lo && at + t < q.hi)) d[u] = 0;
-        ulonglong2 w;
-        w.x = d[u];
-        w.y = mul2(d[u], x[u]);
-        *reinterpret_cast<ulonglong2 *>(ddx + t * Sh::kPairs + slot_of(u, cv)) = w;
-      }
-    }
+    const int at = q.at + j * kTile, stage = j & 1;
+    const bool whole = at >= q.lo && at + kTile <= q.hi;
+    const int nt = min(kTile, q.hi - at);
+    float *sb = sbc + stage * kBC, *sc = sb + kTile * S;
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       sb[tid + k * kThreads] = in_scalar<T>(&rb[k]);
       if (!LOCAL) sc[tid + k * kThreads] = in_scalar<T>(&rc[k]);
     }
-    if (j + 1 < tiles) {
-      fetch_rows(at + TT, stage ^ 1);
-      fetch_bc(at + TT);
-    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // The tile is there for all, and all are done with the one before it,
+    // whose place the next one takes.
     __syncthreads();
+    if (j + 1 < tiles) {
+      fetch_rows(at + kTile, stage ^ 1);
+      fetch_bc(at + kTile);
+    }
 
-    const int nt = min(TT, q.hi - at);
-    if (LOCAL) {
-#pragma unroll (kUnr)
-      for (int t = 0; t < nt; ++t) {
-        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(ddx + t * Sh::kPairs + my_slot);
-        const float4 *bp = reinterpret_cast<const float4 *>(sb + t * S) + l;
-        sum = add2(sum, w.x);
-#pragma unroll
-        for (int n = 0; n < kStates; n += 4) {
-          const float4 b4 = bp[Sh::kLanes * n / 4];
-          const float b[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            h[n + e] = fma2(exp2_2(mul2(w.x, a[n + e])), h[n + e], mul2(w.y, both(b[e])));
-        }
+    // Lane l prepares token t + l of a group of L for its pair of channels,
+    // hands it to the pair's lanes, and ends with that token's y.
+    const unsigned char *mine_raw =
+        raw + stage * TENSORS * kRaw + l * Sh::kPitch + 2 * pr * (int)sizeof(T);
+    auto pair_of = [&](int w, int t) {
+      const unsigned char *from = mine_raw + w * kRaw + t * Sh::kPitch;
+      if constexpr (sizeof(T) == 4) {
+        return *reinterpret_cast<const f2 *>(from);
+      } else {
+        const uint32_t e = *reinterpret_cast<const uint32_t *>(from);
+        return pack2(__uint_as_float(e << 16), __uint_as_float(e & 0xffff0000u));
       }
-    } else {
-#if PIPE
-      // The exponentials of a token are under way while the one before it is
-      // used, so the h chain never waits for the special function unit.
-      f2 e0[kStates], e1[kStates];
-      auto delta_of = [&](int t) {
-        return *reinterpret_cast<const ulonglong2 *>(ddx + t * Sh::kPairs + my_slot);
-      };
-      auto decays = [&](const ulonglong2 &w, f2 *e) {
+    };
+    auto prepare = [&](int t) {  // the group's {delta, delta x}; returns x
+      const f2 x = pair_of(0, t);
+      f2 d = add2(pair_of(1, t), bias);
+      if (p.softplus) d = softplus2(d);
+      // outside the part (x is zero there): the state stays as it is
+      if (!whole && !(at + t + l >= q.lo && at + t + l < q.hi)) d = 0;
+      ulonglong2 w;
+      w.x = d;
+      w.y = mul2(d, x);
+      reinterpret_cast<ulonglong2 *>(swarp)[(t / L & 1) * kThreads + tid] = w;
+      return x;
+    };
+    f2 xnext = prepare(0);
+    for (int t = 0; t < nt; t += L) {
+      __syncwarp();
+      const f2 x = xnext;
+      const ulonglong2 *grp = reinterpret_cast<const ulonglong2 *>(swarp) +
+                              (t / L & 1) * kThreads + (tid - l);
+      if (t + L < nt) xnext = prepare(t + L);
+      f2 part[5];  // sums over 1, 2, 4, .. lanes that wait for their neighbours
+      f2 out = 0;
 #pragma unroll
-        for (int n = 0; n < kStates; ++n) e[n] = exp2_2(mul2(w.x, a[n]));
-      };
-      auto token = [&](int t, const ulonglong2 &w, const f2 *e) {
-        const float4 *bp = reinterpret_cast<const float4 *>(sb + t * S) + l;
-        const float4 *cp = reinterpret_cast<const float4 *>(sc + t * S) + l;
+      for (int u = 0; u < L; ++u) {
+        const ulonglong2 w = grp[u];
+        const float4 *bp = reinterpret_cast<const float4 *>(sb + (t + u) * S) + l;
+        const float4 *cp = reinterpret_cast<const float4 *>(sc + (t + u) * S) + l;
+        if (LOCAL) sum = add2(sum, w.x);
         f2 o[2] = {0, 0};
 #pragma unroll
         for (int n = 0; n < kStates; n += 4) {
-          const float4 b4 = bp[Sh::kLanes * n / 4], c4 = cp[Sh::kLanes * n / 4];
+          const float4 b4 = bp[L * n / 4];
+          float4 c4;
+          if (!LOCAL) c4 = cp[L * n / 4];
           const float b[4] = {b4.x, b4.y, b4.z, b4.w}, c[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            h[n + i] = fma2(e[n + i], h[n + i], mul2(w.y, both(b[i])));
-            o[i & 1] = fma2(both(c[i]), h[n + i], o[i & 1]);
+            h[n + i] = fma2(exp2_2(mul2(w.x, a[n + i])), h[n + i], mul2(w.y, both(b[i])));
+            if (!LOCAL) o[i & 1] = fma2(both(c[i]), h[n + i], o[i & 1]);
           }
         }
-        return add2(o[0], o[1]);
-      };
-      ulonglong2 w0 = delta_of(0), w1;
-      decays(w0, e0);
-#pragma unroll (kUnr)
-      for (int t = 0; t < nt; t += 2) {  // TT is even; a token past nt is neutral
-        f2 o[2];
-        w1 = delta_of(t + 1);
-        decays(w1, e1);
-        o[0] = token(t, w0, e0);
-        w0 = delta_of(min(t + 2, TT - 1));  // past the last one: not used
-        decays(w0, e0);
-        o[1] = token(t + 1, w1, e1);
-#else
-#pragma unroll (kUnr)
-      for (int t = 0; t < nt; t += 2) {  // TT is even; a token past nt is neutral
-        f2 o[2];
+        if (!LOCAL) {
+          // neighbours exchange: of two tokens (pairs, fours, ..) the lane
+          // whose bit is set keeps the second, the other the first
+          f2 s2 = add2(o[0], o[1]);
+          int m = 1, lev = 0;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const ulonglong2 w =
-              *reinterpret_cast<const ulonglong2 *>(ddx + (t + u) * Sh::kPairs + my_slot);
-          const float4 *bp = reinterpret_cast<const float4 *>(sb + (t + u) * S) + l;
-          const float4 *cp = reinterpret_cast<const float4 *>(sc + (t + u) * S) + l;
-          f2 o0 = 0, o1 = 0;
-#pragma unroll
-          for (int n = 0; n < kStates; n += 4) {
-            const float4 b4 = bp[Sh::kLanes * n / 4], c4 = cp[Sh::kLanes * n / 4];
-            const float b[4] = {b4.x, b4.y, b4.z, b4.w}, c[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              h[n + e] = fma2(exp2_2(mul2(w.x, a[n + e])), h[n + e], mul2(w.y, both(b[e])));
-              f2 &to = e & 1 ? o1 : o0;
-              to = fma2(both(c[e]), h[n + e], to);
-            }
+          for (int bits = u; bits & 1; bits >>= 1, m *= 2, ++lev) {
+            const bool up = l & m;
+            const float2 give = unpack2(up ? part[lev] : s2);
+            s2 = add2(up ? s2 : part[lev], pack2(__shfl_xor_sync(~0u, give.x, m),
+                                                 __shfl_xor_sync(~0u, give.y, m)));
           }
-          o[u] = add2(o0, o1);
+          part[lev] = s2;
+          out = s2;
         }
-#endif
-        // sum over the lanes: neighbours exchange one token each, so that an
-        // even lane ends with token t, an odd one with t + 1
-        const int odd = l & 1;
-        const float2 give = unpack2(odd ? o[0] : o[1]);
-        float2 keep = unpack2(odd ? o[1] : o[0]);
-        keep.x += __shfl_xor_sync(~0u, give.x, 1);
-        keep.y += __shfl_xor_sync(~0u, give.y, 1);
-#pragma unroll
-        for (int m = 2; m < Sh::kLanes; m *= 2) {
-          keep.x += __shfl_xor_sync(~0u, keep.x, m);
-          keep.y += __shfl_xor_sync(~0u, keep.y, m);
+      }
+      if (!LOCAL) {
+        out = fma2(skip, x, out);
+        if (gate) out = mul2(out, silu2(pair_of(2, t)));
+        const float2 r = unpack2(out);
+        const int tt = at + t + l;
+        if (tt >= q.lo && tt < q.hi) {
+          T *to = y + tt * p.ys;
+          if (VEC) {
+            if (2 * pr < nch) store_pair<T>(to, r);
+          } else {
+            if (2 * pr < nch) to[0] = out_scalar<T>(r.x);
+            if (2 * pr + 1 < nch) to[1] = out_scalar<T>(r.y);
+          }
         }
-        // y takes the place of delta (delta x where t is odd: other banks), which
-        // all lanes of the pair have read (their shuffles depend on it).  No "memory" clobber: no load before
-        // the barrier reads what this writes, so loads may pass it.
-        if (l < 2)
-          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::
-                       "r"(smem_addr(ddx + (t + odd) * Sh::kPairs + my_slot) + 8 * odd),
-                       "f"(keep.x), "f"(keep.y));
       }
     }
-    if (p.seg.ckpt_slots) {
-      const int end = at + TT;
+    if (!LOCAL && p.seg.ckpt_slots) {
+      const int end = at + kTile;
       const int ck = end <= q.hi ? checkpoint_slot(p.seg, q.i, q.p0, end) : -1;
-      if (!LOCAL && ck >= 0) store_state(p.pool + ck * row);
-    }
-    __syncthreads();
-    if (!LOCAL) {
-#pragma unroll
-      for (int k = 0; k < NI; ++k) {
-        const int it = tid + k * kThreads;
-        if (ITEMS % kThreads != 0 && it >= ITEMS) break;
-        const int t = it / NC, cv = it % NC, c = cv * V;
-        if (at + t < q.lo || at + t >= q.hi || c >= nch) continue;
-        const uint4 *from = raw + stage * TENSORS * ITEMS + it;
-        f2 x[KP], z[KP];
-        float o[V];
-        load_pairs<T>(from, x);
-        if (gate) load_pairs<T>(from + 2 * ITEMS, z);
-#pragma unroll
-        for (int u = 0; u < KP; ++u) {
-          f2 w = reinterpret_cast<const f2 *>(ddx + t * Sh::kPairs + slot_of(u, cv))[t & 1];
-          w = fma2(*reinterpret_cast<const f2 *>(sskip + 2 * (u * NC + cv)), x[u], w);
-          if (gate) w = mul2(w, silu2(z[u]));
-          const float2 r = unpack2(w);
-          o[2 * u] = r.x;
-          o[2 * u + 1] = r.y;
-        }
-        T *to = y + (at + t) * p.ys + c;
-        if (VEC) {
-          store_elems<T, V>(to, o);
-        } else {
-#pragma unroll
-          for (int u = 0; u < V; ++u)
-            if (c + u < nch) to[u] = out_scalar<T>(o[u]);
-        }
-      }
+      if (ck >= 0) store_state(p.pool + ck * row);
     }
   }
   if (LOCAL) store_carry(q.v0 + q.k + 1, sum);
@@ -477,10 +398,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? MINB : 3)
 
 template <typename T, int S, bool LOCAL>
 constexpr size_t smem_bytes() {
-  using Sh = Shape<S>;
-  const size_t items = Sh::kTile * Sh::kChans * sizeof(T);
-  return 2 * (LOCAL ? 2 : 3) * items + Sh::kTile * Sh::kPairs * sizeof(float4) +
-         (LOCAL ? 1 : 2) * Sh::kTile * S * sizeof(float) + 2 * Sh::kChans * sizeof(float);
+  return 2 * (LOCAL ? 2 : 3) * (size_t)(kTile * Shape<T, S>::kPitch) +
+         2 * (LOCAL ? 1 : 2) * kTile * S * sizeof(float) + 2 * kThreads * sizeof(float4);
 }
 
 int blocks_of_row(int C, int S, int G) {

@@ -235,6 +235,12 @@ __device__ __forceinline__ void store_elems(T *p, const float *v) {
   }
 }
 
+template <typename T>
+__device__ __forceinline__ void store_pair(T *p, float2 v) {
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<float2 *>(p) = v;
+  else *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+
 cudaError_t launch_conv(const ConvParams &p, kda_dtype dt, bool step, cudaStream_t s);
 cudaError_t launch_scan_prefill(const ScanParams &p, kda_dtype dt, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanParams &p, kda_dtype dt, cudaStream_t s);
