@@ -24,14 +24,12 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-#ifndef MINB
-#define MINB 4
-#endif
 constexpr int kStates = 8;          // states of a thread, for each of two channels
 constexpr int kAlign = 16;        // parts and tiles start on multiples of this
 constexpr int kCarry = 2 * kStates + 2;  // floats a thread carries between parts
 
 constexpr int kTile = 16;         // tokens of a tile
+constexpr int kBlocks = 5;        // on an SM (registers)
 
 template <typename T, int S>
 struct Shape {
@@ -110,7 +108,7 @@ __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, S
 
 // LOCAL: the first launch (end states of the parts, no outputs).
 template <typename T, int S, bool VEC, bool LOCAL>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? MINB : 3)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBlocks : 3)
     scan_prefill_kernel(const ScanParams p, int nblk) {
   using Sh = Shape<T, S>;
   constexpr int V = InVec<T>::kElems, NC = Sh::kChans / V, L = Sh::kLanes;
@@ -408,10 +406,12 @@ int blocks_of_row(int C, int S, int G) {
 }
 
 // Tokens of a part, 0 to walk segments whole.  A part is an equal share of
-// the batch's work for 152 SMs of four blocks, so a batch that fills them
-// anyway is not cut, and a long segment beside short ones is.
+// the batch's work for 152 SMs of five blocks and two waves, so a batch that
+// fills them anyway is not cut, and a long segment beside short ones is.  One
+// wave: 268 us for one prompt of 8192 tokens, 571 us for 16384 tokens in 37
+// prompts; two waves even out the parts' lengths.
 int part_tokens(int N, int B, int C, int S, int G) {
-  const long long nblk = blocks_of_row(C, S, G), room = 152 * MINB;
+  const long long nblk = blocks_of_row(C, S, G), room = 152LL * kBlocks * 2;
   long long part = ((long long)N * nblk + room - 1) / room;
   part = (part + kAlign - 1) / kAlign * kAlign;
   if (part < 128) part = 128;
