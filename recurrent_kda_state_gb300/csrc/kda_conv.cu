@@ -3,109 +3,188 @@
 //     y[t] = act(bias + sum_j w[j] u[t + j]),  u = [slot's W - 1 rows; x rows]
 //
 // Memory bound: x is read and y written once, 2 W + 4 flops a value.  A
-// thread owns one 16-byte vector of channels and walks down a run of tokens
-// with the W - 1 previous rows in registers, eight rows of loads in flight.
+// thread owns four neighbouring channels and walks down a run of tokens with
+// the W - 1 previous rows in registers and eight rows ahead under way, as
+// raw elements: the place of a row that was used takes the row eight on.  Four channels, not the eight of a
+// 16-byte bf16 vector: those took 190 registers, which left eight warps an SM
+// and 165 us where this takes 73, 81 % of the copy bandwidth (8192 x 12288, W = 4).
 // A prompt's segments are cut into tiles of p.tile tokens, each with its own
 // W - 1 rows before it.  Tile 0 alone reads the slot and alone writes it (it
 // fetches the segment's last rows itself), so no other block can see a state
 // that is already replaced.
+#include <type_traits>
+
 #include "kda_ssm.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kRows = 8;  // rows of loads in flight
+constexpr int kBlocks = 6;    // of 128 threads on an SM (registers)
+constexpr int kTileUnit = 8;  // tiles are multiples of this many tokens,
+constexpr int kMaxTile = 32;  // and this long where there are enough of them
+
+// V elements as they are in memory (V = 1, or 4 of them aligned as a whole).
+template <typename T, int V>
+struct Elems {
+  using Raw = typename std::conditional<V == 1, T,
+              typename std::conditional<sizeof(T) == 4, uint4, uint2>::type>::type;
+  Raw r;
+  __device__ __forceinline__ void load(const T *p) { r = *reinterpret_cast<const Raw *>(p); }
+  __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<Raw *>(p) = r; }
+  __device__ __forceinline__ void get(float *v) const {
+    if constexpr (V == 1) {
+      v[0] = in_scalar<T>(&r);
+    } else if constexpr (sizeof(T) == 4) {
+      v[0] = __uint_as_float(r.x);
+      v[1] = __uint_as_float(r.y);
+      v[2] = __uint_as_float(r.z);
+      v[3] = __uint_as_float(r.w);
+    } else {
+      v[0] = __uint_as_float(r.x << 16);
+      v[1] = __uint_as_float(r.x & 0xffff0000u);
+      v[2] = __uint_as_float(r.y << 16);
+      v[3] = __uint_as_float(r.y & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float *v) {
+    if constexpr (V == 1) {
+      r = out_scalar<T>(v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+      r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                     __float_as_uint(v[3]));
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2], v[3]);
+      r = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
+                     *reinterpret_cast<const uint32_t *>(&b));
+    }
+  }
+};
+
+// The taps and biases of a thread's channels; asked for before the segment is
+// looked up, which they do not depend on.
+template <typename T, int V, int W>
+struct Taps {
+  float w[W][V], bias[V];
+  __device__ __forceinline__ Taps(const ConvParams &p, int c) {
+    const T *bp = static_cast<const T *>(p.bias);
+    float flat[V * W];  // [channel][tap]
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      Elems<T, V> e;
+      e.load(static_cast<const T *>(p.weight) + (long long)c * W + j * V);
+      e.get(flat + j * V);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      bias[e] = bp ? in_scalar<T>(bp + c + e) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][e] = flat[e * W + j];
+    }
+  }
+};
 
 // Tokens [t0, t1) of the segment (local indices; t0 = 0 or t0 >= W - 1).
 template <typename T, int V, int W>
-__device__ __forceinline__ void conv_run(const ConvParams &p, const SegLoc &s, int i, int c,
-                                         int t0, int t1) {
+__device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W> &f,
+                                         const SegLoc &s, int i, int c, int t0, int t1) {
+  using E = Elems<T, V>;
+  constexpr int kRows = sizeof(T) == 2 ? 8 : 4;  // of loads in flight
   const long long D = p.D;
   const T *x = static_cast<const T *>(p.x) + (long long)s.begin * p.xs + c;
   T *y = static_cast<T *>(p.y) + (long long)s.begin * p.ys + c;
   T *state = static_cast<T *>(p.pool) + (long long)s.slot * (W - 1) * D + c;
-  const T *wp = static_cast<const T *>(p.weight) + (long long)c * W;
-  const T *bp = static_cast<const T *>(p.bias);
 
-  float w[W][V], bias[V], win[W - 1][V];
+  E in[kRows], win[W - 1];
+  const T *ahead = x + t0 * p.xs;  // the next row to ask for
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    bias[e] = bp ? in_scalar<T>(bp + c + e) : 0.0f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][e] = in_scalar<T>(wp + e * W + j);
+  for (int r = 0; r < kRows; ++r) {
+    if (t0 + r < t1) in[r].load(ahead);
+    ahead += p.xs;
   }
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
-    if (t0 == 0) load_elems<T, V>(state + j * D, win[j]);
-    else load_elems<T, V>(x + (long long)(t0 - (W - 1) + j) * p.xs, win[j]);
+    if (t0 == 0) win[j].load(state + j * D);
+    else win[j].load(x + (long long)(t0 - (W - 1) + j) * p.xs);
   }
-  if (t0 == 0 && s.keep > 0) {  // the state after `keep` tokens: u[keep .. keep + W - 2]
-    float row[W - 1][V];
+  // the state after k tokens, u[k .. k + W - 2], into a slot
+  auto write_state = [&](int k, int slot) {
+    E row[W - 1];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-      const int at = s.keep + j - (W - 1);
+      const int at = k + j - (W - 1);
       if (at >= 0) {
-        load_elems<T, V>(x + (long long)at * p.xs, row[j]);
-      } else {
+        row[j].load(x + at * p.xs);
+      } else {  // only where t0 = 0: win is the slot's
 #pragma unroll
         for (int q = 0; q < W - 1; ++q)
-          if (q == s.keep + j) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) row[j][e] = win[q][e];
-          }
+          if (q == k + j) row[j] = win[q];
       }
     }
+    T *to = static_cast<T *>(p.pool) + (long long)slot * (W - 1) * D + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) store_elems<T, V>(state + j * D, row[j]);
+    for (int j = 0; j < W - 1; ++j) row[j].store(to + j * D);
+  };
+  if (t0 == 0 && s.keep > 0) write_state(s.keep, s.slot);
+  if (p.seg.ckpt_slots) {
+    const long long p0 = p.seg.start_pos ? p.seg.start_pos[i] : 0, every = p.seg.ckpt_every;
+    for (long long k = ((p0 + t0) / every + 1) * every - p0; k <= t1; k += every) {
+      const int slot = checkpoint_slot(p.seg, i, p0, k);
+      if (slot >= 0) write_state((int)k, slot);
+    }
   }
 
-  const bool ckpt = p.seg.ckpt_slots != nullptr;
-  const long long p0 = ckpt && p.seg.start_pos ? p.seg.start_pos[i] : 0;
-  const long long every = p.seg.ckpt_every;
-  long long next = ckpt ? ((p0 + t0) / every + 1) * every - p0 : 0;  // tokens to the next checkpoint
-  for (int t = t0; t < t1; t += kRows) {
-    float in[kRows][V];
+  T *out = y + t0 * p.ys;
+  auto token = [&](const E &cur) {
+    float acc[V], v[V];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      if (t + r < t1) load_elems<T, V>(x + (long long)(t + r) * p.xs, in[r]);
+    for (int e = 0; e < V; ++e) acc[e] = f.bias[e];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      (j < W - 1 ? win[j] : cur).get(v);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(f.w[j][e], v[e], acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (p.silu) acc[e] = silu_f(acc[e]);
+#pragma unroll
+    for (int j = 0; j + 1 < W - 1; ++j) win[j] = win[j + 1];
+    win[W - 2] = cur;
+    E o;
+    o.set(acc);
+    o.store(out);
+    out += p.ys;
+  };
+  int t = t0;
+  for (; t + 2 * kRows <= t1; t += kRows) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      if (t + r >= t1) break;
-      float o[V];
+      token(in[r]);
+      in[r].load(ahead);
+      ahead += p.xs;
+    }
+  }
+  for (; t < t1; t += kRows) {  // the last rows, fewer than twice kRows
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float acc = bias[e];
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) acc = fmaf(w[j][e], win[j][e], acc);
-        acc = fmaf(w[W - 1][e], in[r][e], acc);
-        o[e] = p.silu ? silu_f(acc) : acc;
-#pragma unroll
-        for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
-        win[W - 2][e] = in[r][e];
-      }
-      store_elems<T, V>(y + (long long)(t + r) * p.ys, o);
-      if (ckpt && t + r + 1 == next) {
-        next += every;
-        const int slot = checkpoint_slot(p.seg, i, p0, t + r + 1);
-        if (slot >= 0) {
-          T *to = static_cast<T *>(p.pool) + (long long)slot * (W - 1) * D + c;
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) store_elems<T, V>(to + j * D, win[j]);
-        }
-      }
+    for (int r = 0; r < kRows; ++r) {
+      if (t + r < t1) token(in[r]);
+      if (t + r + kRows < t1) in[r].load(ahead);
+      ahead += p.xs;
     }
   }
 }
 
 // One row of threads (threadIdx.y) per tile; blockIdx.x: channels.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(128, kBlocks) conv_step_kernel(const ConvParams p) {
   const int i = blockIdx.y * blockDim.y + threadIdx.y;
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V;
   if (i >= p.seg.B || c >= p.D) return;
+  const Taps<T, V, W> f(p, c);
   SegLoc s;
   if (!locate_segment(p.seg, i, &s) || s.len == 0) return;
-  conv_run<T, V, W>(p, s, i, c, 0, s.len);
+  conv_run<T, V, W>(p, f, s, i, c, 0, s.len);
 }
 
 // Tile g of the batch belongs to the last segment i with
@@ -125,16 +204,17 @@ __device__ __forceinline__ int find_segment(const SegParams &p, int g, int tile)
 }
 
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(128) conv_prefill_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(128, kBlocks) conv_prefill_kernel(const ConvParams p) {
   const int g = blockIdx.y * blockDim.y + threadIdx.y;
-  const int i = find_segment(p.seg, g, p.tile);
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V;
+  const Taps<T, V, W> f(p, c < p.D ? c : 0);
+  const int i = find_segment(p.seg, g, p.tile);
   if (c >= p.D) return;
   SegLoc s;
   if (!locate_segment(p.seg, i, &s)) return;
   const long long t0 = (long long)(g - (s.begin / p.tile + i)) * p.tile;
   if (t0 < 0 || t0 >= s.len) return;
-  conv_run<T, V, W>(p, s, i, c, (int)t0, (int)min((long long)s.len, t0 + p.tile));
+  conv_run<T, V, W>(p, f, s, i, c, (int)t0, (int)min((long long)s.len, t0 + p.tile));
 }
 
 template <typename T, int V, int W>
@@ -148,11 +228,11 @@ cudaError_t launch_w(const ConvParams &p, bool step, cudaStream_t st) {
     conv_step_kernel<T, V, W><<<grid, block, 0, st>>>(p);
     return cudaGetLastError();
   }
-  // Tiles as long as they leave every SM its four blocks of 128 threads.
+  // Tiles as long as they leave every SM its blocks of 128 threads twice.
   ConvParams q = p;
-  const long long want = 152LL * 4 * 128;
-  long long tile = (long long)p.seg.N * nvec / want / kRows * kRows;
-  q.tile = (int)(tile < kRows ? kRows : tile > 64 ? 64 : tile);
+  const long long want = 152LL * kBlocks * 2 * 128;
+  long long tile = (long long)p.seg.N * nvec / want / kTileUnit * kTileUnit;
+  q.tile = (int)(tile < kTileUnit ? kTileUnit : tile > kMaxTile ? kMaxTile : tile);
   long long tiles = (long long)p.seg.N / q.tile + p.seg.B;
   while ((tiles + block.y - 1) / block.y > 65535) {  // the grid's y limit
     q.tile *= 2;
@@ -174,11 +254,10 @@ cudaError_t launch_v(const ConvParams &p, bool step, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_t(const ConvParams &p, bool step, cudaStream_t st) {
-  constexpr int V = InVec<T>::kElems;
+  constexpr int V = 4;
   const uintptr_t bits = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.y) |
-                         (uintptr_t)(p.xs * (long long)sizeof(T)) |
-                         (uintptr_t)(p.ys * (long long)sizeof(T));
-  const bool vec = (bits & 15) == 0 && p.D % V == 0;
+                         (uintptr_t)((p.xs | p.ys) * (long long)sizeof(T));
+  const bool vec = bits % (V * sizeof(T)) == 0 && p.D % V == 0;
   return vec ? launch_v<T, V>(p, step, st) : launch_v<T, 1>(p, step, st);
 }
 
