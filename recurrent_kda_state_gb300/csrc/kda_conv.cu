@@ -12,8 +12,6 @@
 // W - 1 rows before it.  Tile 0 alone reads the slot and alone writes it (it
 // fetches the segment's last rows itself), so no other block can see a state
 // that is already replaced.
-#include <type_traits>
-
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -91,21 +89,21 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
   using E = Elems<T, V>;
   constexpr int kRows = sizeof(T) == 2 ? 8 : 4;  // of loads in flight
   const long long D = p.D;
-  const T *x = static_cast<const T *>(p.x) + (long long)s.begin * p.xs + c;
-  T *y = static_cast<T *>(p.y) + (long long)s.begin * p.ys + c;
+  const T *x = row_at(static_cast<const T *>(p.x), s.begin, p.xs) + c;
+  T *y = row_at(static_cast<T *>(p.y), s.begin, p.ys) + c;
   T *state = static_cast<T *>(p.pool) + (long long)s.slot * (W - 1) * D + c;
 
   E in[kRows], win[W - 1];
-  const T *ahead = x + t0 * p.xs;  // the next row to ask for
+  const T *ahead = row_at(x, t0, p.xs);  // the next row to ask for
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     if (t0 + r < t1) in[r].load(ahead);
-    ahead += p.xs;
+    ahead = row_at(ahead, 1, p.xs);
   }
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     if (t0 == 0) win[j].load(state + j * D);
-    else win[j].load(x + (long long)(t0 - (W - 1) + j) * p.xs);
+    else win[j].load(row_at(x, t0 - (W - 1) + j, p.xs));
   }
   // the state after k tokens, u[k .. k + W - 2], into a slot
   auto write_state = [&](int k, int slot) {
@@ -114,7 +112,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
     for (int j = 0; j < W - 1; ++j) {
       const int at = k + j - (W - 1);
       if (at >= 0) {
-        row[j].load(x + at * p.xs);
+        row[j].load(row_at(x, at, p.xs));
       } else {  // only where t0 = 0: win is the slot's
 #pragma unroll
         for (int q = 0; q < W - 1; ++q)
@@ -134,7 +132,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
     }
   }
 
-  T *out = y + t0 * p.ys;
+  T *out = row_at(y, t0, p.ys);
   auto token = [&](const E &cur) {
     float acc[V], v[V];
 #pragma unroll
@@ -154,7 +152,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
     E o;
     o.set(acc);
     o.store(out);
-    out += p.ys;
+    out = row_at(out, 1, p.ys);
   };
   int t = t0;
   for (; t + 2 * kRows <= t1; t += kRows) {
@@ -162,7 +160,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
     for (int r = 0; r < kRows; ++r) {
       token(in[r]);
       in[r].load(ahead);
-      ahead += p.xs;
+      ahead = row_at(ahead, 1, p.xs);
     }
   }
   for (; t < t1; t += kRows) {  // the last rows, fewer than twice kRows
@@ -170,7 +168,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
     for (int r = 0; r < kRows; ++r) {
       if (t + r < t1) token(in[r]);
       if (t + r + kRows < t1) in[r].load(ahead);
-      ahead += p.xs;
+      ahead = row_at(ahead, 1, p.xs);
     }
   }
 }
@@ -256,7 +254,7 @@ template <typename T>
 cudaError_t launch_t(const ConvParams &p, bool step, cudaStream_t st) {
   constexpr int V = 4;
   const uintptr_t bits = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.y) |
-                         (uintptr_t)((p.xs | p.ys) * (long long)sizeof(T));
+                         (uintptr_t)(p.xs | p.ys);
   const bool vec = bits % (V * sizeof(T)) == 0 && p.D % V == 0;
   return vec ? launch_v<T, V>(p, step, st) : launch_v<T, 1>(p, step, st);
 }

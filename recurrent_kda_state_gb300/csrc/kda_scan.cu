@@ -10,11 +10,11 @@
 // memory, where each thread reads back only what it copied itself: no
 // barriers, and enough bytes in flight for HBM with few registers.
 // Rows of one token (no segment table) ask for the next row's token one row
-// ahead; rows that may have several load kChunk tokens at a time, since a
-// token's latency, not its work, is what a draft of eight costs.  The sum over
+// ahead.  Rows that may have several take them from shared memory, up to kTake
+// at a time and two such items ahead: a draft of eight costs its work, not
+// eight latencies (64 rows, eight of them of eight tokens, 4096 channels: TODO us,
+// 15 to 19 with the tokens loaded to registers in chunks).  The sum over
 // states is a butterfly over the channel's lanes.
-#include <type_traits>
-
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -51,6 +51,74 @@ struct Four {
   }
 };
 
+// The recurrence of a thread's states over one token; returns its share of
+// C . h.
+template <typename T>
+__device__ __forceinline__ float scan_token(f2 (&h)[2 * kQuads], const f2 (&a)[2 * kQuads],
+                                            float d, float dx, const Four<T> *b,
+                                            const Four<T> *c) {
+  const f2 dd = both(d), dx2 = both(dx);
+  f2 o = 0;
+#pragma unroll
+  for (int j = 0; j < kQuads; ++j) {
+    f2 bb[2], cc[2];
+    b[j].get(bb);
+    c[j].get(cc);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      f2 &v = h[2 * j + e];
+      v = fma2(exp2_2(mul2(dd, a[2 * j + e])), v, mul2(dx2, bb[e]));
+      o = fma2(cc[e], v, o);
+    }
+  }
+  const float2 u = unpack2(o);
+  return u.x + u.y;
+}
+
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < L; m *= 2) v += __shfl_xor_sync(~0u, v, m);
+  return v;
+}
+
+template <int S>
+__device__ __forceinline__ void load_decay(const float *A, int c, int l, f2 (&a)[2 * kQuads]) {
+  constexpr int L = S / kStates;
+#pragma unroll
+  for (int j = 0; j < kQuads; ++j) {  // states 4 (l + L j) + {0 .. 3}, as pairs
+    const ulonglong2 v =
+        *reinterpret_cast<const ulonglong2 *>(A + (long long)c * S + 4 * (l + L * j));
+    a[2 * j] = mul2(v.x, both(kLog2e));
+    a[2 * j + 1] = mul2(v.y, both(kLog2e));
+  }
+}
+
+__device__ __forceinline__ void async16(void *to, const void *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The rows of a block: blockIdx.y, + gridDim.y, ..; checked, once.
+__device__ __forceinline__ int take_rows(const SegParams &p, SegLoc *rec) {
+  const int di = gridDim.y, rows = (p.B - (int)blockIdx.y + di - 1) / di;
+  for (int r = threadIdx.x; r < rows; r += kThreads) {
+    SegLoc s;
+    if (!locate_segment(p, blockIdx.y + r * di, &s)) s.len = 0;
+    rec[r] = s;
+  }
+  return rows;
+}
+
 // One token's inputs of a thread.
 template <typename T>
 struct Token {
@@ -58,17 +126,11 @@ struct Token {
   Four<T> b[kQuads], c[kQuads];
 };
 
-// Blocks on an SM (registers).
-template <typename T>
-__host__ __device__ constexpr int step_blocks(bool one) {
-  return one && sizeof(T) == 2 ? 4 : 3;
-}
-
-// ONE: every row is one token, row i token i.  VEC: B and C by fours.
-template <typename T, int S, bool VEC, bool ONE>
-__global__ void __launch_bounds__(kThreads, step_blocks<T>(ONE)) scan_step_kernel(const ScanParams p) {
+// Rows of one token, row i token i.  VEC: B and C are read by fours.
+template <typename T, int S, bool VEC>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+    scan_one_kernel(const ScanParams p) {
   constexpr int L = S / kStates;  // lanes of a channel
-  constexpr int kChunk = ONE ? 1 : sizeof(T) == 2 ? 4 : 2;
   __shared__ SegLoc rec[kMaxRows];
   __shared__ ulonglong2 ring[kRing][kQuads][kThreads];
 
@@ -77,23 +139,11 @@ __global__ void __launch_bounds__(kThreads, step_blocks<T>(ONE)) scan_step_kerne
   const bool on = ch < p.C_;
   const int c = on ? ch : p.C_ - 1;
   const int g = c / (p.C_ / p.G);
-  const int i0 = blockIdx.y, di = gridDim.y;  // the block's rows
-  const int rows = (p.seg.B - i0 + di - 1) / di;
-  for (int r = tid; r < rows; r += kThreads) {
-    SegLoc s;
-    if (!locate_segment(p.seg, i0 + r * di, &s)) s.len = 0;
-    rec[r] = s;
-  }
+  const int i0 = blockIdx.y, di = gridDim.y;
+  const int rows = take_rows(p.seg, rec);
 
-  // states 4 (l + L j) + {0 .. 3}, as pairs
   f2 a[2 * kQuads];
-#pragma unroll
-  for (int j = 0; j < kQuads; ++j) {
-    const ulonglong2 v =
-        *reinterpret_cast<const ulonglong2 *>(p.A + (long long)c * S + 4 * (l + L * j));
-    a[2 * j] = mul2(v.x, both(kLog2e));
-    a[2 * j + 1] = mul2(v.y, both(kLog2e));
-  }
+  load_decay<S>(p.A, c, l, a);
   const float skip = p.D ? p.D[c] : 0.0f, bias = p.dtb ? p.dtb[c] : 0.0f;
   const long long row = (long long)p.C_ * S;
   float *pool = p.pool + (long long)c * S + 4 * l;
@@ -104,30 +154,27 @@ __global__ void __launch_bounds__(kThreads, step_blocks<T>(ONE)) scan_step_kerne
   T *yb = static_cast<T *>(p.y) + c;
 
   auto fetch = [&](Token<T> &k, int t) {
-    k.x = xb[t * p.xs];
-    k.d = db[t * p.dts];
-    if (zb) k.z = zb[t * p.zs];
+    k.x = *row_at(xb, t, p.xs);
+    k.d = *row_at(db, t, p.dts);
+    if (zb) k.z = *row_at(zb, t, p.zs);
+    const T *b = row_at(Bb, t, p.bs), *c4 = row_at(Cb, t, p.cs);
 #pragma unroll
     for (int j = 0; j < kQuads; ++j) {
-      k.b[j].template load<VEC>(Bb + t * p.bs + 4 * L * j);
-      k.c[j].template load<VEC>(Cb + t * p.cs + 4 * L * j);
+      k.b[j].template load<VEC>(b + 4 * L * j);
+      k.c[j].template load<VEC>(c4 + 4 * L * j);
     }
   };
-  Token<T> in[kChunk];
-  if (ONE) fetch(in[0], i0);
+  Token<T> ahead;  // the next row's
+  fetch(ahead, i0);
   __syncthreads();
 
   auto ask = [&](int r) {  // row r's states into the ring
     if (r < rows && rec[r].len > 0) {
       const float *from = pool + rec[r].slot * row;
 #pragma unroll
-      for (int j = 0; j < kQuads; ++j)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                         (uint32_t)__cvta_generic_to_shared(&ring[r % kRing][j][tid])),
-                     "l"(from + 4 * L * j)
-                     : "memory");
+      for (int j = 0; j < kQuads; ++j) async16(&ring[r % kRing][j][tid], from + 4 * L * j);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    async_commit();
   };
 #pragma unroll
   for (int r = 0; r < kRing - 1; ++r) ask(r);
@@ -135,67 +182,176 @@ __global__ void __launch_bounds__(kThreads, step_blocks<T>(ONE)) scan_step_kerne
   for (int r = 0; r < rows; ++r) {
     ask(r + kRing - 1);
     const SegLoc s = rec[r];
+    const Token<T> now = ahead;
+    if (r + 1 < rows) fetch(ahead, i0 + (r + 1) * di);
+    async_wait<kRing - 1>();
+    if (s.len == 0) continue;
     f2 h[2 * kQuads];
-    // Token t of the row: h steps on, and its y goes out.
-    auto token = [&](const Token<T> &k, int t) {
-      const float x = in_scalar<T>(&k.x);
-      float d = in_scalar<T>(&k.d) + bias;
-      if (p.softplus) d = softplus_f(d);
-      const f2 dd = both(d), dx = both(d * x);
-      f2 o = 0;
 #pragma unroll
-      for (int j = 0; j < kQuads; ++j) {
-        f2 b[2], cc[2];
-        k.b[j].get(b);
-        k.c[j].get(cc);
+    for (int j = 0; j < kQuads; ++j) {
+      const ulonglong2 v = ring[r % kRing][j][tid];
+      h[2 * j] = v.x;
+      h[2 * j + 1] = v.y;
+    }
+    const float x = in_scalar<T>(&now.x);
+    float d = in_scalar<T>(&now.d) + bias;
+    if (p.softplus) d = softplus_f(d);
+    float o = scan_token<T>(h, a, d, d * x, now.b, now.c);
+    if (s.keep > 0 && on) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          f2 &v = h[2 * j + e];
-          v = fma2(exp2_2(mul2(dd, a[2 * j + e])), v, mul2(dx, b[e]));
-          o = fma2(cc[e], v, o);
+      for (int j = 0; j < kQuads; ++j)
+        *reinterpret_cast<ulonglong2 *>(pool + s.slot * row + 4 * L * j) =
+            make_ulonglong2(h[2 * j], h[2 * j + 1]);
+    }
+    o = lanes_sum<L>(o);
+    if (on && l == 0) {
+      o = fmaf(skip, x, o);
+      if (zb) o *= silu_f(in_scalar<T>(&now.z));
+      *row_at(yb, s.begin, p.ys) = out_scalar<T>(o);
+    }
+  }
+}
+
+// Rows of any number of tokens.  VEC: every row of a token tensor starts on 16
+// bytes and a group's channels are a multiple of 16 bytes.
+template <typename T, int S, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) scan_rows_kernel(const ScanParams p, int bpg) {
+  constexpr int L = S / kStates, V = InVec<T>::kElems;
+  constexpr int kTake = 16 / sizeof(T);             // tokens of an item
+  constexpr int kStages = 3;                        // items in shared memory
+  constexpr int kChans = kThreads / L;              // of a block, all of one group
+  constexpr int NC = kChans / V, NS = S / V;        // 16-byte pieces of a token's rows
+  constexpr int kPieces = 3 * NC + 2 * NS;
+  __shared__ SegLoc rec[kMaxRows];
+  __shared__ ulonglong2 ring[kStages][kQuads][kThreads];
+  __shared__ uint4 toks[kStages][kTake][kPieces];   // x, dt, z, B, C of a token
+
+  const int tid = threadIdx.x, l = tid % L, cl = tid / L;
+  const int per = p.C_ / p.G, g = blockIdx.x / bpg;
+  const int c0 = g * per + (blockIdx.x % bpg) * kChans;
+  const int nch = min(kChans, (g + 1) * per - c0);
+  const bool on = cl < nch;
+  const int c = c0 + (on ? cl : nch - 1);
+  const int rows = take_rows(p.seg, rec);
+
+  f2 a[2 * kQuads];
+  load_decay<S>(p.A, c, l, a);
+  const float skip = p.D ? p.D[c] : 0.0f, bias = p.dtb ? p.dtb[c] : 0.0f;
+  const long long row = (long long)p.C_ * S;
+  float *pool = p.pool + (long long)c * S + 4 * l;
+  T *yb = static_cast<T *>(p.y) + c;
+  __syncthreads();
+
+  // Items: kTake tokens of a row, from token t of row r on.
+  auto skip_empty = [&](int r) {
+    while (r < rows && rec[r].len == 0) ++r;
+    return r;
+  };
+  auto advance = [&](int &r, int &t) {
+    t += kTake;
+    if (t >= rec[r].len) {
+      r = skip_empty(r + 1);
+      t = 0;
+    }
+  };
+  auto ask = [&](int stage, int r, int t) {
+    if (r < rows) {
+      const SegLoc s = rec[r];
+      if (t == 0) {
+        const float *from = pool + s.slot * row;
+#pragma unroll
+        for (int j = 0; j < kQuads; ++j) async16(&ring[stage][j][tid], from + 4 * L * j);
+      }
+      const int n = min(kTake, s.len - t) * kPieces;
+      for (int k = tid; k < n; k += kThreads) {
+        const int u = k / kPieces, at = k % kPieces, tok = s.begin + t + u;
+        const T *from;
+        int first, left;  // element of the row, elements there are from it on
+        if (at < 3 * NC) {
+          const int w = at / NC;
+          if (w == 2 && !p.z) continue;
+          first = at % NC * V;
+          left = nch - first;
+          const T *base = static_cast<const T *>(w == 0 ? p.x : w == 1 ? p.dt : p.z) + c0;
+          from = row_at(base, tok, w == 0 ? p.xs : w == 1 ? p.dts : p.zs) + first;
+        } else {
+          const bool is_b = at < 3 * NC + NS;
+          first = (at - 3 * NC - (is_b ? 0 : NS)) * V;
+          left = S;
+          const T *base = static_cast<const T *>(is_b ? p.B : p.C) + g * S;
+          from = row_at(base, tok, is_b ? p.bs : p.cs) + first;
+        }
+        if (left <= 0) continue;
+        if (VEC) {
+          async16(&toks[stage][u][at], from);
+        } else {
+          alignas(16) T e[V];
+#pragma unroll
+          for (int q = 0; q < V; ++q) e[q] = q < left ? from[q] : out_scalar<T>(0.0f);
+          toks[stage][u][at] = *reinterpret_cast<const uint4 *>(e);
         }
       }
-      if (t + 1 == s.keep && on) {
+    }
+    async_commit();
+  };
+
+  int r = skip_empty(0), t = 0;
+  int ra = r, ta = 0;  // the item to ask for next
+  int sa = 0, st = 0;
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) {
+    ask(sa, ra, ta);
+    sa = sa + 1 == kStages ? 0 : sa + 1;
+    if (ra < rows) advance(ra, ta);
+  }
+  f2 h[2 * kQuads];
+  while (r < rows) {
+    async_wait<kStages - 2>();
+    // The item is there for all, and all are done with the one before it,
+    // whose place the next one takes.
+    __syncthreads();
+    ask(sa, ra, ta);
+    sa = sa + 1 == kStages ? 0 : sa + 1;
+    if (ra < rows) advance(ra, ta);
+
+    const SegLoc s = rec[r];
+    if (t == 0) {
+#pragma unroll
+      for (int j = 0; j < kQuads; ++j) {
+        const ulonglong2 v = ring[st][j][tid];
+        h[2 * j] = v.x;
+        h[2 * j + 1] = v.y;
+      }
+    }
+    const int n = min(kTake, s.len - t);
+    for (int u = 0; u < n; ++u) {
+      const T *in = reinterpret_cast<const T *>(toks[st][u]);
+      const T *bc = in + 3 * kChans + 4 * l;
+      Four<T> b[kQuads], cc[kQuads];
+#pragma unroll
+      for (int j = 0; j < kQuads; ++j) {
+        b[j].template load<true>(bc + 4 * L * j);
+        cc[j].template load<true>(bc + S + 4 * L * j);
+      }
+      const float x = in_scalar<T>(in + cl);
+      float d = in_scalar<T>(in + kChans + cl) + bias;
+      if (p.softplus) d = softplus_f(d);
+      float o = scan_token<T>(h, a, d, d * x, b, cc);
+      if (t + u + 1 == s.keep && on) {
 #pragma unroll
         for (int j = 0; j < kQuads; ++j)
           *reinterpret_cast<ulonglong2 *>(pool + s.slot * row + 4 * L * j) =
               make_ulonglong2(h[2 * j], h[2 * j + 1]);
       }
-      const float2 u = unpack2(o);
-      float sum = u.x + u.y;
-#pragma unroll
-      for (int m = 1; m < L; m *= 2) sum += __shfl_xor_sync(~0u, sum, m);
+      o = lanes_sum<L>(o);
       if (on && l == 0) {
-        sum = fmaf(skip, x, sum);
-        if (zb) sum *= silu_f(in_scalar<T>(&k.z));
-        yb[(s.begin + t) * p.ys] = out_scalar<T>(sum);
-      }
-    };
-    auto take = [&]() {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-#pragma unroll
-      for (int j = 0; j < kQuads; ++j) {
-        const ulonglong2 v = ring[r % kRing][j][tid];
-        h[2 * j] = v.x;
-        h[2 * j + 1] = v.y;
-      }
-    };
-    if constexpr (ONE) {
-      const Token<T> now = in[0];
-      if (r + 1 < rows) fetch(in[0], i0 + (r + 1) * di);
-      take();
-      if (s.len > 0) token(now, 0);
-    } else {
-      for (int t = 0; t < s.len; t += kChunk) {
-#pragma unroll
-        for (int u = 0; u < kChunk; ++u)
-          if (t + u < s.len) fetch(in[u], s.begin + t + u);
-        if (t == 0) take();
-#pragma unroll
-        for (int u = 0; u < kChunk; ++u)
-          if (t + u < s.len) token(in[u], t + u);
+        o = fmaf(skip, x, o);
+        if (p.z) o *= silu_f(in_scalar<T>(in + 2 * kChans + cl));
+        *row_at(yb, s.begin + t + u, p.ys) = out_scalar<T>(o);
       }
     }
+    advance(r, t);
+    st = st + 1 == kStages ? 0 : st + 1;
   }
 }
 
@@ -203,14 +359,14 @@ __global__ void __launch_bounds__(kThreads, step_blocks<T>(ONE)) scan_step_kerne
 // `room` blocks on the machine: the number that ends first, if a block takes
 // the time of its rows and of two more (its start).  Groups that overflow one
 // wave by a few blocks cost a second one: 256 rows of 4096 channels with 64
-// states took 115 us in 640 blocks where 608 fit, and TODO us by this rule.
+// states took 115 us in 640 blocks where 608 fit, and 89 us by this rule.
 int row_groups(int gx, int B, int room) {
   long long best = 0;
   int groups = 0;
   for (int gy = (B + kMaxRows - 1) / kMaxRows; gy <= B; ++gy) {
     const long long waves = ((long long)gx * gy + room - 1) / room;
     const long long cost = waves * ((B + gy - 1) / gy + 2);
-    if (!groups || cost < best) {
+    if (!groups || cost <= best) {
       best = cost;
       groups = gy;
     }
@@ -221,18 +377,25 @@ int row_groups(int gx, int B, int room) {
 
 template <typename T, int S>
 cudaError_t launch_step(const ScanParams &p, cudaStream_t st) {
-  constexpr int cpb = kThreads / (S / kStates);
-  const bool one = p.seg.cu == nullptr;
-  const int gx = (p.C_ + cpb - 1) / cpb, B = p.seg.B;
-  const int gy = row_groups(gx, B, 152 * step_blocks<T>(one));
-  const uintptr_t bits = reinterpret_cast<uintptr_t>(p.B) | reinterpret_cast<uintptr_t>(p.C) |
-                         (uintptr_t)((p.bs | p.cs) * (long long)sizeof(T));
-  const bool vec = (bits & (4 * sizeof(T) - 1)) == 0;
-  const dim3 grid(gx, gy);
-  if (one && vec) scan_step_kernel<T, S, true, true><<<grid, kThreads, 0, st>>>(p);
-  else if (one) scan_step_kernel<T, S, false, true><<<grid, kThreads, 0, st>>>(p);
-  else if (vec) scan_step_kernel<T, S, true, false><<<grid, kThreads, 0, st>>>(p);
-  else scan_step_kernel<T, S, false, false><<<grid, kThreads, 0, st>>>(p);
+  constexpr int kChans = kThreads / (S / kStates);
+  const uintptr_t bc = reinterpret_cast<uintptr_t>(p.B) | reinterpret_cast<uintptr_t>(p.C) |
+                       (uintptr_t)(p.bs | p.cs);
+  if (!p.seg.cu) {
+    const int gx = (p.C_ + kChans - 1) / kChans;
+    const dim3 grid(gx, row_groups(gx, p.seg.B, 152 * (sizeof(T) == 2 ? 4 : 3)));
+    if (bc % (4 * sizeof(T)) == 0) scan_one_kernel<T, S, true><<<grid, kThreads, 0, st>>>(p);
+    else scan_one_kernel<T, S, false><<<grid, kThreads, 0, st>>>(p);
+  } else {
+    const uintptr_t all = bc | reinterpret_cast<uintptr_t>(p.x) |
+                          reinterpret_cast<uintptr_t>(p.dt) | reinterpret_cast<uintptr_t>(p.z) |
+                          (uintptr_t)(p.xs | p.dts | p.zs);
+    const int per = p.C_ / p.G, bpg = (per + kChans - 1) / kChans, gx = p.G * bpg;
+    const dim3 grid(gx, row_groups(gx, p.seg.B, 152 * 4));
+    if (all % 16 == 0 && per % InVec<T>::kElems == 0)
+      scan_rows_kernel<T, S, true><<<grid, kThreads, 0, st>>>(p, bpg);
+    else
+      scan_rows_kernel<T, S, false><<<grid, kThreads, 0, st>>>(p, bpg);
+  }
   return cudaGetLastError();
 }
 

@@ -29,7 +29,10 @@ constexpr int kAlign = 16;        // parts and tiles start on multiples of this
 constexpr int kCarry = 2 * kStates + 2;  // floats a thread carries between parts
 
 constexpr int kTile = 16;         // tokens of a tile
-constexpr int kBlocks = 5;        // on an SM (registers)
+// Blocks on an SM (registers).
+__host__ __device__ constexpr int blocks_of(int elem, int S) {
+  return elem == 4 ? 3 : S <= 32 ? 5 : 4;
+}
 
 template <typename T, int S>
 struct Shape {
@@ -108,7 +111,7 @@ __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, S
 
 // LOCAL: the first launch (end states of the parts, no outputs).
 template <typename T, int S, bool VEC, bool LOCAL>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBlocks : 3)
+__global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S))
     scan_prefill_kernel(const ScanParams p, int nblk) {
   using Sh = Shape<T, S>;
   constexpr int V = InVec<T>::kElems, NC = Sh::kChans / V, L = Sh::kLanes;
@@ -195,13 +198,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBlocks : 3)
   if (p.dtb) bias = pack2(p.dtb[ca], p.dtb[cb]);
   if (!LOCAL && p.D) skip = pack2(p.D[ca], p.D[cb]);
 
-  const T *rows[3] = {static_cast<const T *>(p.x) + s.begin * p.xs + c0,
-                      static_cast<const T *>(p.dt) + s.begin * p.dts + c0,
-                      static_cast<const T *>(p.z) + s.begin * p.zs + c0};
-  const long long strides[3] = {p.xs, p.dts, p.zs};
-  const T *B = static_cast<const T *>(p.B) + s.begin * p.bs + g * S;
-  const T *C = static_cast<const T *>(p.C) + s.begin * p.cs + g * S;
-  T *y = static_cast<T *>(p.y) + s.begin * p.ys + c0 + 2 * pr;
+  const T *rows[3] = {row_at(static_cast<const T *>(p.x), s.begin, p.xs) + c0,
+                      row_at(static_cast<const T *>(p.dt), s.begin, p.dts) + c0,
+                      row_at(static_cast<const T *>(p.z), s.begin, p.zs) + c0};
+  const int strides[3] = {p.xs, p.dts, p.zs};
+  const T *B = row_at(static_cast<const T *>(p.B), s.begin, p.bs) + g * S;
+  const T *C = row_at(static_cast<const T *>(p.C), s.begin, p.cs) + g * S;
+  T *y = row_at(static_cast<T *>(p.y), s.begin, p.ys) + c0 + 2 * pr;
   const bool gate = !LOCAL && p.z != nullptr;
 
   // 16 bytes (V channels of one token) at a time; what lies outside the part
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBlocks : 3)
         if (w == 2 && !gate) break;
         unsigned char *to =
             raw + (stage * TENSORS + w) * kRaw + it / NC * Sh::kPitch + it % NC * 16;
-        const T *from = rows[w] + (on ? t * strides[w] + c : 0);
+        const T *from = on ? row_at(rows[w], t, strides[w]) + c : rows[w];
         if (VEC) {
           copy16(to, on ? static_cast<const void *>(from) : p.A, on);
         } else {
@@ -237,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBlocks : 3)
     for (int k = 0; k < NB; ++k) {
       const int e = tid + k * kThreads, t = at + e / S;
       const bool on = t >= q.lo && t < q.hi;
-      rb[k] = on ? B[t * p.bs + e % S] : out_scalar<T>(0.0f);
-      if (!LOCAL) rc[k] = on ? C[t * p.cs + e % S] : out_scalar<T>(0.0f);
+      rb[k] = on ? row_at(B, t, p.bs)[e % S] : out_scalar<T>(0.0f);
+      if (!LOCAL) rc[k] = on ? row_at(C, t, p.cs)[e % S] : out_scalar<T>(0.0f);
     }
   };
 
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kBlocks : 3)
         const float2 r = unpack2(out);
         const int tt = at + t + l;
         if (tt >= q.lo && tt < q.hi) {
-          T *to = y + tt * p.ys;
+          T *to = row_at(y, tt, p.ys);
           if (VEC) {
             if (2 * pr < nch) store_pair<T>(to, r);
           } else {
@@ -411,7 +414,7 @@ int blocks_of_row(int C, int S, int G) {
 // wave: 268 us for one prompt of 8192 tokens, 571 us for 16384 tokens in 37
 // prompts; two waves even out the parts' lengths.
 int part_tokens(int N, int B, int C, int S, int G) {
-  const long long nblk = blocks_of_row(C, S, G), room = 152LL * kBlocks * 2;
+  const long long nblk = blocks_of_row(C, S, G), room = 152LL * blocks_of(2, S) * 2;
   long long part = ((long long)N * nblk + room - 1) / room;
   part = (part + kAlign - 1) / kAlign * kAlign;
   if (part < 128) part = 128;
@@ -448,7 +451,7 @@ cudaError_t launch_prefill_s(const ScanParams &p, cudaStream_t st) {
   constexpr int V = InVec<T>::kElems;
   uintptr_t bits = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.dt) |
                    reinterpret_cast<uintptr_t>(p.z) | reinterpret_cast<uintptr_t>(p.y);
-  bits |= (uintptr_t)((p.xs | p.dts | p.ys | (p.z ? p.zs : 0)) * (long long)sizeof(T));
+  bits |= (uintptr_t)(p.xs | p.dts | p.ys | p.zs);
   const bool vec = (bits & 15) == 0 && (p.C_ / p.G) % V == 0;
   return vec ? launch_prefill_v<T, S, true>(p, st) : launch_prefill_v<T, S, false>(p, st);
 }

@@ -3,6 +3,8 @@
 // after validating the public arguments.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -27,7 +29,7 @@ struct ConvParams {
   SegParams seg;
   const void *x, *weight, *bias;
   void *y, *pool;
-  long long xs, ys;  // row strides in elements
+  int xs, ys;  // row strides in bytes
   int D, W, silu;
   int tile;  // prompts: tokens of a tile
 };
@@ -36,7 +38,7 @@ struct ScanParams {
   SegParams seg;
   const void *x, *dt, *z, *B, *C;
   void *y;
-  long long xs, dts, zs, bs, cs, ys;  // row strides in elements
+  int xs, dts, zs, bs, cs, ys;  // row strides in bytes
   const float *A, *D, *dtb;
   float *pool;
   float *ws;  // prompts: carried states of split segments, or NULL
@@ -210,6 +212,13 @@ __device__ __forceinline__ float out_scalar<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 out_scalar<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
+}
+
+// Row t of a token tensor: one multiply-add, since strides are 32-bit bytes.
+template <typename T>
+__device__ __forceinline__ T *row_at(T *base, int t, int stride) {
+  using B = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+  return reinterpret_cast<T *>(reinterpret_cast<B *>(base) + (long long)t * stride);
 }
 
 // V consecutive elements (V = 1: plain scalars; else one 16-byte vector).

@@ -10,13 +10,13 @@ bool dtype_ok(int dt) { return dt == KDA_F32 || dt == KDA_BF16; }
 size_t elem(int dt) { return dt == KDA_F32 ? 4 : 2; }
 constexpr int kMaxSeqs = 65535;
 constexpr int kMaxChannels = 1 << 20;
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxStride = 0x7fffffff;  // bytes
 
 // A token view: pointer, element alignment, row stride.
 int check_view(const void *p, int64_t stride, int row, int dt) {
   if (!p) return KDA_EINVAL;
   if (!aligned(p, elem(dt))) return KDA_EALIGN;
-  if (stride < row || stride > kMaxStride) return KDA_ESHAPE;
+  if (stride < row || stride > kMaxStride / (int64_t)elem(dt)) return KDA_ESHAPE;
   return KDA_OK;
 }
 int check_param(const void *p, bool needed) {
@@ -77,13 +77,14 @@ int conv_impl(const kda_conv_tokens *t, kda_conv_pool *pool, const int32_t *slot
   p.seg.P = pool->num_slots;
   p.seg.max_ckpt = max_ckpt;
   p.seg.ckpt_every = every;
+  const int64_t es = (int64_t)elem(t->dtype);
   p.x = t->x;
   p.weight = t->weight;
   p.bias = t->bias;
   p.y = t->y;
   p.pool = pool->base;
-  p.xs = t->x_stride;
-  p.ys = t->y_stride;
+  p.xs = (int)(t->x_stride * es);
+  p.ys = (int)(t->y_stride * es);
   p.D = t->channels;
   p.W = t->width;
   p.silu = t->silu != 0;
@@ -139,18 +140,19 @@ int scan_impl(const kda_scan_tokens *t, kda_scan_pool *pool, const int32_t *slot
   p.seg.P = pool->num_slots;
   p.seg.max_ckpt = max_ckpt;
   p.seg.ckpt_every = every;
+  const int64_t es = (int64_t)elem(t->dtype);
   p.x = t->x;
   p.dt = t->dt;
   p.z = t->z;
   p.B = t->B;
   p.C = t->C;
   p.y = t->y;
-  p.xs = t->x_stride;
-  p.dts = t->dt_stride;
-  p.zs = t->z_stride;
-  p.bs = t->b_stride;
-  p.cs = t->c_stride;
-  p.ys = t->y_stride;
+  p.xs = (int)(t->x_stride * es);
+  p.dts = (int)(t->dt_stride * es);
+  p.zs = t->z ? (int)(t->z_stride * es) : 0;
+  p.bs = (int)(t->b_stride * es);
+  p.cs = (int)(t->c_stride * es);
+  p.ys = (int)(t->y_stride * es);
   p.A = t->A;
   p.D = t->D;
   p.dtb = t->dt_bias;
