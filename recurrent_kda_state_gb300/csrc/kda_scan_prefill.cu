@@ -131,6 +131,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S))
   SegLoc s;
   if (!find_part(p, v, &q, &s)) return;
   if (LOCAL && q.k + 1 >= q.count) return;
+  // the second launch may begin: it waits before it reads anything of this one
+  if (LOCAL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // the block's channels: kChans of one group
   const int per = p.C_ / p.G, bpg = nblk / p.G, g = blk / bpg;
@@ -249,6 +251,9 @@ __global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S))
   const int tiles = (q.hi - q.at + kTile - 1) / kTile;
   fetch_rows(q.at, 0);
   fetch_bc(q.at);
+
+  // What the first launch wrote is read from here on.
+  if (!LOCAL && p.part) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // The state at the part's start.  The carry slot of part 0 holds the slot's
   // own state, since the last part replaces that; slot k holds part k - 1's
@@ -417,7 +422,11 @@ int part_tokens(int N, int B, int C, int S, int G) {
   const long long nblk = blocks_of_row(C, S, G), room = 152LL * blocks_of(2, S) * 2;
   long long part = ((long long)N * nblk + room - 1) / room;
   part = (part + kAlign - 1) / kAlign * kAlign;
-  if (part < 128) part = 128;
+  // A part walks its tokens and then the parts before it, at about the same
+  // time each, so parts below sqrt(N) tokens gain nothing; and 32 tokens are
+  // what a part's start costs (333 tokens of 500 channels with 64 states: 37 us
+  // in parts of 128 tokens, 19 in parts of 32).
+  while (part < 32 || part * part < N) part += kAlign;
   if (part >= N) return 0;
   while (((long long)N / part + 2LL * B) * nblk > 0x7fffffffLL) part *= 2;
   return (int)part;
@@ -432,8 +441,17 @@ cudaError_t launch_pass(const ScanParams &p, int nblk, int parts, cudaStream_t s
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<(unsigned)((long long)nblk * parts), kThreads, smem, st>>>(p, nblk);
-  return cudaGetLastError();
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)((long long)nblk * parts));
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = !LOCAL && p.part ? 1 : 0;  // behind the first launch, its start overlaps
+  return cudaLaunchKernelEx(&c, kernel, p, nblk);
 }
 
 template <typename T, int S, bool VEC>
