@@ -29,6 +29,16 @@ struct Elems {
   Raw r;
   __device__ __forceinline__ void load(const T *p) { r = *reinterpret_cast<const Raw *>(p); }
   __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<Raw *>(p) = r; }
+  // Rows pass through once: marked to leave L2 first (5003 x 1000 fp32: 12.3 us
+  // without the marks, 10.3 with them; no difference where the data passes L2).
+  __device__ __forceinline__ void load_once(const T *p) {
+    if constexpr (V == 1) load(p);
+    else r = __ldcs(reinterpret_cast<const Raw *>(p));
+  }
+  __device__ __forceinline__ void store_once(T *p) const {
+    if constexpr (V == 1) store(p);
+    else __stcs(reinterpret_cast<Raw *>(p), r);
+  }
   __device__ __forceinline__ void get(float *v) const {
     if constexpr (V == 1) {
       v[0] = in_scalar<T>(&r);
@@ -97,7 +107,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
   const T *ahead = row_at(x, t0, p.xs);  // the next row to ask for
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    if (t0 + r < t1) in[r].load(ahead);
+    if (t0 + r < t1) in[r].load_once(ahead);
     ahead = row_at(ahead, 1, p.xs);
   }
 #pragma unroll
@@ -151,7 +161,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
     win[W - 2] = cur;
     E o;
     o.set(acc);
-    o.store(out);
+    o.store_once(out);
     out = row_at(out, 1, p.ys);
   };
   int t = t0;
@@ -159,7 +169,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       token(in[r]);
-      in[r].load(ahead);
+      in[r].load_once(ahead);
       ahead = row_at(ahead, 1, p.xs);
     }
   }
@@ -167,7 +177,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       if (t + r < t1) token(in[r]);
-      if (t + r + kRows < t1) in[r].load(ahead);
+      if (t + r + kRows < t1) in[r].load_once(ahead);
       ahead = row_at(ahead, 1, p.xs);
     }
   }
@@ -226,10 +236,10 @@ cudaError_t launch_w(const ConvParams &p, bool step, cudaStream_t st) {
     conv_step_kernel<T, V, W><<<grid, block, 0, st>>>(p);
     return cudaGetLastError();
   }
-  // Tiles as long as they leave every SM its blocks of 128 threads twice.
+  // Tiles as long as leaves every SM its blocks of 128 threads once.
   ConvParams q = p;
-  const long long want = 152LL * kBlocks * 2 * 128;
-  long long tile = (long long)p.seg.N * nvec / want / kTileUnit * kTileUnit;
+  const long long want = 152LL * kBlocks * 128;
+  long long tile = (long long)p.seg.N * nvec / want / kTileUnit * kTileUnit + kTileUnit;
   q.tile = (int)(tile < kTileUnit ? kTileUnit : tile > kMaxTile ? kMaxTile : tile);
   long long tiles = (long long)p.seg.N / q.tile + p.seg.B;
   while ((tiles + block.y - 1) / block.y > 65535) {  // the grid's y limit

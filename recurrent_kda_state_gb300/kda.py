@@ -451,7 +451,7 @@ class ConvBatch:
             _dtype_code(dt), x.data_ptr(), self.y.data_ptr(), _row_view(x, dt, "x"),
             _row_view(self.y, dt, "y"), _param(weight, (D, W), dt, "weight"),
             _param(bias, (D,), dt, "bias"), cu, B, N, D, W, 1 if activation else 0)
-        self.ref = ctypes.byref(self.c)
+        self.ref, self.num_seqs = ctypes.byref(self.c), B
 
 
 class ScanPool:
@@ -495,7 +495,7 @@ class ScanBatch:
             _row_view(C, ty, "C"), _row_view(self.y, ty, "y"), _param(A, (Dm, S), f32, "A"),
             _param(D, (Dm,), f32, "D"), _param(dt_bias, (Dm,), f32, "dt_bias"), cu, nseq,
             N, Dm, S, G, 1 if dt_softplus else 0)
-        self.ref = ctypes.byref(self.c)
+        self.ref, self.num_seqs = ctypes.byref(self.c), nseq
 
 
 def _ckpt(ckpt_slots, B):
@@ -510,7 +510,7 @@ def _ckpt(ckpt_slots, B):
 def kda_conv_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, start_pos=None,
                      stream=None):
     """Causal convolution of packed prompts; ckpt_slots [B][max_ckpt] int32."""
-    B = tok.c.num_seqs
+    B = tok.num_seqs
     ckpt, max_ckpt = _ckpt(ckpt_slots, B)
     _check(lib().kda_conv_prefill(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots"), ckpt, max_ckpt, ckpt_every,
@@ -520,7 +520,7 @@ def kda_conv_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, star
 def kda_conv_step(tok, pool, state_slots, commit_len=None, stream=None):
     """Steps of one or a few tokens a row; commit_len [B] int32: how many of a
     row's tokens the stored state takes in (None: all)."""
-    B = tok.c.num_seqs
+    B = tok.num_seqs
     _check(lib().kda_conv_step(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots"),
         _table(commit_len, B, "commit_len"), _stream(stream)), "kda_conv_step")
@@ -543,7 +543,7 @@ def kda_scan_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, star
                      workspace=None, stream=None):
     """Selective scan of packed prompts; workspace: from scan_workspace(tok),
     or None: no segment is split."""
-    B = tok.c.num_seqs
+    B = tok.num_seqs
     ckpt, max_ckpt = _ckpt(ckpt_slots, B)
     _check(lib().kda_scan_prefill(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots"), ckpt, max_ckpt, ckpt_every,
@@ -553,7 +553,7 @@ def kda_scan_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, star
 
 def kda_scan_step(tok, pool, state_slots, commit_len=None, stream=None):
     """The scan's steps, commit_len as in kda_conv_step."""
-    B = tok.c.num_seqs
+    B = tok.num_seqs
     _check(lib().kda_scan_step(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots"),
         _table(commit_len, B, "commit_len"), _stream(stream)), "kda_scan_step")
