@@ -3,35 +3,48 @@
 //
 // Per (token, channel, state) one ex2 and four fp32 operations, against 8
 // bytes per (token, channel): at S = 16 the arithmetic pipes bound it, not
-// HBM.  So the inner loop holds nothing else: a thread owns eight states of
-// two neighbouring channels in registers (S / 8 lanes a channel pair) and the
-// pair's values travel as packed fp32 pairs, so one instruction serves both.
-// A block stages tiles of tokens in shared memory: delta and delta x per
-// channel (the softplus is computed once, not once per lane), B and C in fp32.  The next tile's rows arrive by asynchronous copies
-// meanwhile.  After a tile its y, summed over the channel's lanes, goes back
-// through shared memory to the thread that staged the row, which adds the
-// skip, applies the gate and writes 16 bytes.
+// HBM.  The bare loop over tokens (ex2, the products and sums, the loads of B
+// and C from shared memory) takes 105 cycles per SM quarter for 512 states,
+// whichever way states and channels are packed; MUFU alone would take 64,
+// the fp32 pipe 72.
+//   - A thread owns eight states of two neighbouring channels in registers
+//     (S / 8 lanes a channel pair).  The pair's values travel as packed fp32
+//     pairs, one instruction for both.
+//   - A block takes tiles of 16 tokens: x, dt and z rows by asynchronous
+//     copies, B and C through registers, the next tile's while this one's
+//     are used; one barrier a tile.
+//   - Of each group of S / 8 tokens, lane l prepares token l for its pair
+//     (softplus, delta x), hands it to the pair's lanes through shared memory,
+//     and ends with that token's y, since the sums over lanes are exchanged
+//     token against token.  So skip, gate and the store need no second pass
+//     through shared memory and every lane has its share of them.
 //
 // Few long segments leave most of the machine idle, so with a workspace a
 // segment is cut into parts: a first launch computes each part's end state
 // from a zero start and its sum of delta; the second starts part k from
 // h = exp(A sum_j delta) h + end_j over the parts before it, and does the rest.
-// The first launch repeats the exponentials, which is why segments are not
-// cut further than the machine has room for.
+// Where segments have many parts, a launch between the two joins the ends
+// once instead of every part for itself (8192 tokens of 4096 channels in 48
+// parts: 281 us without it, 266 with it).  The first launch repeats the
+// exponentials (two fifths of the time), which is why segments are not cut
+// further than the machine has room for.
+// 266 us for 8192 x 4096 channels x 16 states in bf16 (268 MB: 40 us at the
+// copy bandwidth; the two bare loops alone 163 us).
 #include "kda_ssm.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kStates = 8;          // states of a thread, for each of two channels
-constexpr int kAlign = 16;        // parts and tiles start on multiples of this
+constexpr int kStates = 8;  // of a thread, for each of two channels
+constexpr int kTile = 16;   // tokens of a tile; parts and tiles start on multiples of it
 constexpr int kCarry = 2 * kStates + 2;  // floats a thread carries between parts
 
-constexpr int kTile = 16;         // tokens of a tile
-// Blocks on an SM (registers).
-__host__ __device__ constexpr int blocks_of(int elem, int S) {
-  return elem == 4 ? 3 : S <= 32 ? 5 : 4;
+// Blocks on an SM, set by registers.  The first launch is faster with four of
+// more registers (266 us the pair, 269 with five and 270 with six, 8192 tokens
+// of 4096 channels), the second with five (274 with four).
+__host__ __device__ constexpr int blocks_of(int elem, int S, bool local) {
+  return elem == 4 ? 3 : S <= 32 && !local ? 5 : 4;
 }
 
 template <typename T, int S>
@@ -71,6 +84,13 @@ struct Part {
   long long p0;    // absolute position of the segment's first token
 };
 
+__device__ __forceinline__ long long first_position(const SegParams &g, int i) {
+  return g.ckpt_slots && g.start_pos ? g.start_pos[i] : 0;
+}
+__device__ __forceinline__ int part_count(int len, int r, int part) {
+  return (int)(((long long)len + r + part - 1) / part);
+}
+
 __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, SegLoc *s) {
   const SegParams &g = p.seg;
   int i = v;
@@ -88,8 +108,8 @@ __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, S
   }
   if (!locate_segment(g, i, s) || s->len == 0) return false;
   q->i = i;
-  q->p0 = g.ckpt_slots && g.start_pos ? g.start_pos[i] : 0;
-  const int r = (int)(q->p0 & (kAlign - 1));  // tiles end on absolute multiples
+  q->p0 = first_position(g, i);
+  const int r = (int)(q->p0 & (kTile - 1));  // tiles end on absolute multiples
   if (!p.part) {
     q->k = 0;
     q->count = 1;
@@ -99,7 +119,7 @@ __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, S
   } else {
     q->v0 = s->begin / p.part + 2 * i;
     q->k = v - q->v0;
-    q->count = (int)(((long long)s->len + r + p.part - 1) / p.part);
+    q->count = part_count(s->len, r, p.part);
     if (q->k < 0 || q->k >= q->count) return false;
     const long long at = (long long)q->k * p.part - r;
     q->at = (int)at;
@@ -111,7 +131,7 @@ __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, S
 
 // LOCAL: the first launch (end states of the parts, no outputs).
 template <typename T, int S, bool VEC, bool LOCAL>
-__global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S))
+__global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S, LOCAL))
     scan_prefill_kernel(const ScanParams p, int nblk) {
   using Sh = Shape<T, S>;
   constexpr int V = InVec<T>::kElems, NC = Sh::kChans / V, L = Sh::kLanes;
@@ -271,14 +291,14 @@ __global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S))
   } else if (q.count == 1) {
     load_state(mine);
   } else {
-    const int first = q.k ? 1 : 0;
+    const int from = q.k == 0 ? 0 : p.joined ? q.k : 1;
 #pragma unroll
     for (int n = 0; n < kStates; ++n) {
-      const float *w = carry(q.v0 + first);
+      const float *w = carry(q.v0 + from);
       h[n] = pack2(w[(2 * n) * kThreads], w[(2 * n + 1) * kThreads]);
     }
 #pragma unroll 4
-    for (int k = 2; k <= q.k; ++k) {
+    for (int k = 2; k <= (p.joined ? 0 : q.k); ++k) {
       const float *w = carry(q.v0 + k);
       const f2 d = pack2(w[2 * kStates * kThreads], w[(2 * kStates + 1) * kThreads]);
 #pragma unroll
@@ -402,6 +422,54 @@ __global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S))
   else if (q.hi == s.len) store_state(mine);
 }
 
+// Joins the parts of each segment: carry slot k, which holds the end of part
+// k - 1 from a zero start, becomes the state that part k starts from.  One
+// thread per two states (blockIdx.y: which of a thread's); the loads of eight
+// parts are under way at a time.
+template <int S>
+__global__ void __launch_bounds__(kThreads) scan_join_kernel(const ScanParams p, int nblk) {
+  constexpr int L = S / kStates, kChans = 2 * kThreads / L, kAhead = 8;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int i = blockIdx.x / nblk, blk = blockIdx.x % nblk, n = blockIdx.y, tid = threadIdx.x;
+  SegLoc s;
+  if (!locate_segment(p.seg, i, &s) || s.len == 0) return;
+  const int count = part_count(s.len, (int)(first_position(p.seg, i) & (kTile - 1)), p.part);
+  if (count <= 2) return;
+  const int per = p.C_ / p.G, bpg = nblk / p.G, g = blk / bpg;
+  const int c0 = g * per + (blk % bpg) * kChans;
+  const int nch = min(kChans, (g + 1) * per - c0);
+  const int l = tid % L, pr = tid / L, st = 4 * (l + L * (n / 4)) + n % 4;
+  const long long ca = c0 + min(2 * pr, nch - 1), cb = c0 + min(2 * pr + 1, nch - 1);
+  const f2 a = pack2(exponent_scale(p.A[ca * S + st]), exponent_scale(p.A[cb * S + st]));
+
+  const long long step = (long long)nblk * kCarry * kThreads;
+  float *w = p.ws + (s.begin / p.part + 2 * i + 1LL) * step +
+             (long long)blk * kCarry * kThreads + tid;  // carry slot 1
+  f2 h = pack2(w[(2 * n) * kThreads], w[(2 * n + 1) * kThreads]);
+  for (int k = 2; k < count; k += kAhead) {
+    f2 v[kAhead], d[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (k + u < count) {
+        const float *from = w + (u + 1) * step;
+        v[u] = pack2(from[(2 * n) * kThreads], from[(2 * n + 1) * kThreads]);
+        d[u] = pack2(from[2 * kStates * kThreads], from[(2 * kStates + 1) * kThreads]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      w += step;
+      if (k + u < count) {
+        h = fma2(exp2_2(mul2(d[u], a)), h, v[u]);
+        const float2 o = unpack2(h);
+        w[(2 * n) * kThreads] = o.x;
+        w[(2 * n + 1) * kThreads] = o.y;
+      }
+    }
+  }
+}
+
 template <typename T, int S, bool LOCAL>
 constexpr size_t smem_bytes() {
   return 2 * (LOCAL ? 2 : 3) * (size_t)(kTile * Shape<T, S>::kPitch) +
@@ -415,21 +483,39 @@ int blocks_of_row(int C, int S, int G) {
 
 // Tokens of a part, 0 to walk segments whole.  A part is an equal share of
 // the batch's work for 152 SMs of five blocks and two waves, so a batch that
-// fills them anyway is not cut, and a long segment beside short ones is.  One
-// wave: 268 us for one prompt of 8192 tokens, 571 us for 16384 tokens in 37
-// prompts; two waves even out the parts' lengths.
+// fills them anyway is not cut, and a long segment beside short ones is.  Two
+// waves even out the parts' lengths (16384 tokens in 37 prompts: 495 us, 597 in
+// one wave, 503 in three).
 int part_tokens(int N, int B, int C, int S, int G) {
-  const long long nblk = blocks_of_row(C, S, G), room = 152LL * blocks_of(2, S) * 2;
+  const long long nblk = blocks_of_row(C, S, G), room = 152LL * blocks_of(2, S, false) * 2;
+  if (2LL * B * nblk > 0x7fffffffLL) return 0;
   long long part = ((long long)N * nblk + room - 1) / room;
-  part = (part + kAlign - 1) / kAlign * kAlign;
+  part = (part + kTile - 1) / kTile * kTile;
   // A part walks its tokens and then the parts before it, at about the same
   // time each, so parts below sqrt(N) tokens gain nothing; and 32 tokens are
   // what a part's start costs (333 tokens of 500 channels with 64 states: 37 us
   // in parts of 128 tokens, 19 in parts of 32).
-  while (part < 32 || part * part < N) part += kAlign;
+  while (part < 32 || part * part < N) part += kTile;
   if (part >= N) return 0;
   while (((long long)N / part + 2LL * B) * nblk > 0x7fffffffLL) part *= 2;
   return (int)part;
+}
+
+// Launches a kernel; behind: its start overlaps the end of the launch before
+// it, whose results it waits for itself.
+cudaError_t launch_behind(void (*kernel)(ScanParams, int), dim3 grid, size_t smem, bool behind,
+                          cudaStream_t st, const ScanParams &p, int nblk) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, p, nblk);
 }
 
 template <typename T, int S, bool VEC, bool LOCAL>
@@ -441,17 +527,8 @@ cudaError_t launch_pass(const ScanParams &p, int nblk, int parts, cudaStream_t s
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)((long long)nblk * parts));
-  c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = smem;
-  c.stream = st;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &at;
-  c.numAttrs = !LOCAL && p.part ? 1 : 0;  // behind the first launch, its start overlaps
-  return cudaLaunchKernelEx(&c, kernel, p, nblk);
+  const dim3 grid((unsigned)((long long)nblk * parts));
+  return launch_behind(kernel, grid, smem, !LOCAL && p.part != 0, st, p, nblk);
 }
 
 template <typename T, int S, bool VEC>
@@ -460,7 +537,11 @@ cudaError_t launch_prefill_v(ScanParams p, cudaStream_t st) {
   p.part = p.ws ? part_tokens(p.seg.N, p.seg.B, p.C_, S, p.G) : 0;
   if (!p.part) return launch_pass<T, S, VEC, false>(p, nblk, p.seg.B, st);
   const int parts = p.seg.N / p.part + 2 * p.seg.B;
-  const cudaError_t e = launch_pass<T, S, VEC, true>(p, nblk, parts, st);
+  p.joined = p.seg.N / p.part > 16 * p.seg.B;
+  cudaError_t e = launch_pass<T, S, VEC, true>(p, nblk, parts, st);
+  if (e == cudaSuccess && p.joined)
+    e = launch_behind(scan_join_kernel<S>, dim3((unsigned)((long long)nblk * p.seg.B), kStates), 0,
+                      true, st, p, nblk);
   return e != cudaSuccess ? e : launch_pass<T, S, VEC, false>(p, nblk, parts, st);
 }
 
@@ -488,6 +569,10 @@ cudaError_t launch_prefill_t(const ScanParams &p, cudaStream_t st) {
 
 cudaError_t launch_scan_prefill(const ScanParams &p, kda_dtype dt, cudaStream_t s) {
   return dt == KDA_F32 ? launch_prefill_t<float>(p, s) : launch_prefill_t<__nv_bfloat16>(p, s);
+}
+
+long long scan_prefill_blocks(int B, int C, int S, int G) {
+  return (long long)B * blocks_of_row(C, S, G);
 }
 
 size_t scan_workspace_floats(int N, int B, int C, int S, int G) {

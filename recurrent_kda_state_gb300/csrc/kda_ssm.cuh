@@ -44,6 +44,7 @@ struct ScanParams {
   float *ws;  // prompts: carried states of split segments, or NULL
   int C_, S, G, softplus;
   int part;  // prompts: tokens of a part, 0 = segments are not split
+  int joined;  // prompts: a launch of its own has joined the parts' states
 };
 
 constexpr int kMaxSlotArrays = 64;
@@ -259,6 +260,8 @@ cudaError_t launch_moves(const MoveParams &p, cudaStream_t s);
 constexpr int kMoveChunk = 16384;
 inline long long move_chunks(long long bytes) { return (bytes + kMoveChunk - 1) / kMoveChunk; }
 
+// Blocks of the scan of B whole segments.
+long long scan_prefill_blocks(int B, int C, int S, int G);
 // Workspace floats of the split scan (0: segments are not split).
 size_t scan_workspace_floats(int N, int B, int C, int S, int G);
 

@@ -119,6 +119,8 @@ int scan_impl(const kda_scan_tokens *t, kda_scan_pool *pool, const int32_t *slot
   if ((st = check_param(t->A, true))) return st;
   if ((st = check_param(t->D, false))) return st;
   if ((st = check_param(t->dt_bias, false))) return st;
+  if (!step && kda::scan_prefill_blocks(t->num_seqs, t->channels, t->state, t->groups) > 0x7fffffffLL)
+    return KDA_ESHAPE;
   size_t need = 0;
   if (ws) {
     if (!aligned(ws, 256)) return KDA_EALIGN;

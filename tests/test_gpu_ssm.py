@@ -228,6 +228,14 @@ def test_scan_prefill_long(split):
     scan_case(17, "bf16", [3001, 17, 0, 700, 1], 160, 16, split=split)
 
 
+@pytest.mark.parametrize("lens,D,S", [([3001], 40, 16), ([2500, 2500], 24, 32),
+                                      ([1100], 520, 128), ([0, 1300, 0], 33, 64)])
+def test_scan_prefill_many_parts(lens, D, S):
+    """Segments of so many parts that a launch of its own joins them."""
+    scan_case(35, "bf16", lens, D, S, start=[7] * len(lens), every=64, max_ckpt=2)
+    scan_case(36, "f32", lens, D, S)
+
+
 def test_scan_prefill_many_segments():
     lens = np.random.default_rng(18).integers(0, 6, 500)
     scan_case(18, "f32", lens, 24, 16)
