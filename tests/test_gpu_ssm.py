@@ -481,3 +481,32 @@ def test_example_serves_what_whole_prefills_give():
     spec.loader.exec_module(mod)
     worst, bits = mod.main()
     assert bits == 0 and worst < 2.0 ** -7
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_moves_in_columns(seed):
+    """Slots so large that every thread does all moves at its place: chains,
+    forks out of chains, cycles with tails, frees, and entries to skip."""
+    rng = np.random.default_rng(seed)
+    P = 40
+    slots = rng.permutation(P).tolist()
+    src, dst = [], []
+    for n in (2, 3, 5):                             # cycles
+        c, slots = slots[:n], slots[n:]
+        src += c
+        dst += c[1:] + c[:1]
+        src += [c[0], c[n - 1]]                     # copies of what a cycle moves
+        dst += slots[:2]
+        src.append(dst[-1])                         # and what was there goes on
+        dst.append(slots[2])
+        slots = slots[3:]
+    c, slots = slots[:6], slots[6:]                 # a chain with a fork, its start freed
+    src += c[:-1] + [c[2], -1]
+    dst += c[1:] + [slots[0], c[0]]
+    src += [5, 7, -1]
+    dst += [-1, 7 if 7 not in dst else -1, -1]      # nothing, itself, nothing
+    k = rng.permutation(len(src))
+    src, dst = np.array(src)[k], np.array(dst)[k]
+    live = dst[dst >= 0]
+    assert len(set(live.tolist())) == len(live)
+    move_case(40 + seed, P, src, dst, shapes=((512, 516), (1024, 513), (4, 4)))
