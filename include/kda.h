@@ -425,6 +425,9 @@ int kda_commit_snapshot(const int32_t *accepted_len, const int32_t *state_slots,
  *   - Outputs have the inputs' dtype, rounded once from fp32, and must not
  *     overlap any input.
  *   - The slots of one call must be distinct, checkpoint slots included.
+ *   - The kernels are launched as programmatic dependents of the previous work
+ *     on the stream: they may start while it finishes, but touch no memory
+ *     until it has, so stream order holds for every value they read or write.
  */
 
 /* One packed batch of the convolution. */

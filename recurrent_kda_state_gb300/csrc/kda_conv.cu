@@ -186,6 +186,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
 // One row of threads (threadIdx.y) per tile; blockIdx.x: channels.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(128, kBlocks) conv_step_kernel(const ConvParams p) {
+  begin_after_stream();
   const int i = blockIdx.y * blockDim.y + threadIdx.y;
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V;
   if (i >= p.seg.B || c >= p.D) return;
@@ -213,6 +214,7 @@ __device__ __forceinline__ int find_segment(const SegParams &p, int g, int tile)
 
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(128, kBlocks) conv_prefill_kernel(const ConvParams p) {
+  begin_after_stream();
   const int g = blockIdx.y * blockDim.y + threadIdx.y;
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V;
   const Taps<T, V, W> f(p, c < p.D ? c : 0);
@@ -233,8 +235,7 @@ cudaError_t launch_w(const ConvParams &p, bool step, cudaStream_t st) {
   const int gx = (nvec + bx - 1) / bx;
   if (step) {
     const dim3 grid(gx, (p.seg.B + block.y - 1) / block.y);
-    conv_step_kernel<T, V, W><<<grid, block, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_after(conv_step_kernel<T, V, W>, grid, block, 0, st, p);
   }
   // Tiles as long as leaves every SM its blocks of 128 threads once.
   ConvParams q = p;
@@ -247,8 +248,7 @@ cudaError_t launch_w(const ConvParams &p, bool step, cudaStream_t st) {
     tiles = (long long)p.seg.N / q.tile + p.seg.B;
   }
   const dim3 grid(gx, (unsigned)((tiles + block.y - 1) / block.y));
-  conv_prefill_kernel<T, V, W><<<grid, block, 0, st>>>(q);
-  return cudaGetLastError();
+  return launch_after(conv_prefill_kernel<T, V, W>, grid, block, 0, st, q);
 }
 
 template <typename T, int V>

@@ -50,6 +50,7 @@ __device__ __forceinline__ void copy_chunk(V *to, const V *from, long long n) {
 
 template <bool STAGE>
 __global__ void __launch_bounds__(kThreads) move_kernel(const MoveParams p) {
+  begin_after_stream();
   for (int i = blockIdx.y; i < p.n; i += gridDim.y) {
     const int src = p.src[i], dst = p.dst[i];
     if (dst < 0 || src == dst) continue;
@@ -138,6 +139,7 @@ __device__ __forceinline__ void make_plan(const MoveParams &p, Plan &s) {
 
 __global__ void __launch_bounds__(kThreads, 4) move_columns_kernel(const MoveParams p) {
   __shared__ Plan s;
+  begin_after_stream();
   make_plan(p, s);
   int a = 0;
   while (a + 1 < p.L && p.first[a + 1] <= (int)blockIdx.x) ++a;
@@ -185,18 +187,15 @@ cudaError_t launch_moves(const MoveParams &p, cudaStream_t s) {
     }
     q.first[p.L] = (int)blocks;
     if (whole && (p.n <= 16 || blocks >= 2 * p.n)) {
-      move_columns_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(q);
-      return cudaGetLastError();
+      return launch_after(move_columns_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, q);
     }
   }
   const dim3 grid(p.first[p.L], p.n < 65535 ? p.n : 65535);
   if (p.ws) {
-    move_kernel<true><<<grid, kThreads, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(move_kernel<true>, grid, dim3(kThreads), 0, s, p);
     if (e != cudaSuccess) return e;
   }
-  move_kernel<false><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(move_kernel<false>, grid, dim3(kThreads), 0, s, p);
 }
 
 }  // namespace kda

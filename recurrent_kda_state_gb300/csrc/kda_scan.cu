@@ -21,6 +21,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kPerSm = 4;      // blocks on an SM; fp32 inputs, one token a row: 3
 constexpr int kStates = 8;     // of a thread
 constexpr int kQuads = kStates / 4;
 constexpr int kRing = 4;       // rows of states in flight, the current one among them
@@ -128,11 +129,12 @@ struct Token {
 
 // Rows of one token, row i token i.  VEC: B and C are read by fours.
 template <typename T, int S, bool VEC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? kPerSm : 3)
     scan_one_kernel(const ScanParams p) {
   constexpr int L = S / kStates;  // lanes of a channel
   __shared__ SegLoc rec[kMaxRows];
   __shared__ ulonglong2 ring[kRing][kQuads][kThreads];
+  begin_after_stream();
 
   const int tid = threadIdx.x, l = tid % L;
   const int ch = blockIdx.x * (kThreads / L) + tid / L;
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
 // Rows of any number of tokens.  VEC: every row of a token tensor starts on 16
 // bytes and a group's channels are a multiple of 16 bytes.
 template <typename T, int S, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4) scan_rows_kernel(const ScanParams p, int bpg) {
+__global__ void __launch_bounds__(kThreads, kPerSm) scan_rows_kernel(const ScanParams p, int bpg) {
   constexpr int L = S / kStates, V = InVec<T>::kElems;
   constexpr int kTake = 16 / sizeof(T);             // tokens of an item
   constexpr int kStages = 3;                        // items in shared memory
@@ -225,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_rows_kernel(const ScanParams
   __shared__ SegLoc rec[kMaxRows];
   __shared__ ulonglong2 ring[kStages][kQuads][kThreads];
   __shared__ uint4 toks[kStages][kTake][kPieces];   // x, dt, z, B, C of a token
+  begin_after_stream();
 
   const int tid = threadIdx.x, l = tid % L, cl = tid / L;
   const int per = p.C_ / p.G, g = blockIdx.x / bpg;
@@ -382,21 +385,19 @@ cudaError_t launch_step(const ScanParams &p, cudaStream_t st) {
                        (uintptr_t)(p.bs | p.cs);
   if (!p.seg.cu) {
     const int gx = (p.C_ + kChans - 1) / kChans;
-    const dim3 grid(gx, row_groups(gx, p.seg.B, 152 * (sizeof(T) == 2 ? 4 : 3)));
-    if (bc % (4 * sizeof(T)) == 0) scan_one_kernel<T, S, true><<<grid, kThreads, 0, st>>>(p);
-    else scan_one_kernel<T, S, false><<<grid, kThreads, 0, st>>>(p);
-  } else {
-    const uintptr_t all = bc | reinterpret_cast<uintptr_t>(p.x) |
-                          reinterpret_cast<uintptr_t>(p.dt) | reinterpret_cast<uintptr_t>(p.z) |
-                          (uintptr_t)(p.xs | p.dts | p.zs);
-    const int per = p.C_ / p.G, bpg = (per + kChans - 1) / kChans, gx = p.G * bpg;
-    const dim3 grid(gx, row_groups(gx, p.seg.B, 152 * 4));
-    if (all % 16 == 0 && per % InVec<T>::kElems == 0)
-      scan_rows_kernel<T, S, true><<<grid, kThreads, 0, st>>>(p, bpg);
-    else
-      scan_rows_kernel<T, S, false><<<grid, kThreads, 0, st>>>(p, bpg);
+    const dim3 grid(gx, row_groups(gx, p.seg.B, 152 * (sizeof(T) == 2 ? kPerSm : 3)));
+    return launch_after(bc % (4 * sizeof(T)) == 0 ? scan_one_kernel<T, S, true>
+                                                  : scan_one_kernel<T, S, false>,
+                        grid, dim3(kThreads), 0, st, p);
   }
-  return cudaGetLastError();
+  const uintptr_t all = bc | reinterpret_cast<uintptr_t>(p.x) |
+                        reinterpret_cast<uintptr_t>(p.dt) | reinterpret_cast<uintptr_t>(p.z) |
+                        (uintptr_t)(p.xs | p.dts | p.zs);
+  const int per = p.C_ / p.G, bpg = (per + kChans - 1) / kChans, gx = p.G * bpg;
+  const dim3 grid(gx, row_groups(gx, p.seg.B, 152 * kPerSm));
+  return launch_after(all % 16 == 0 && per % InVec<T>::kElems == 0 ? scan_rows_kernel<T, S, true>
+                                                                    : scan_rows_kernel<T, S, false>,
+                      grid, dim3(kThreads), 0, st, p, bpg);
 }
 
 template <typename T>

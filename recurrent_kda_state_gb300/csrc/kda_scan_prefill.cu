@@ -145,14 +145,19 @@ __global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S, LOCAL))
   constexpr int kBC = (LOCAL ? 1 : 2) * kTile * S;
   float4 *swarp = reinterpret_cast<float4 *>(sbc + 2 * kBC);     // [2][kThreads]
 
+  // The first launch of a call waits for the stream before it lets the second
+  // begin, so that one may read the call's inputs at once and waits only for
+  // the carried states.
+  const bool first = LOCAL || !p.part;
+  if (first) begin_after_stream();
+  if (LOCAL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   const int tid = threadIdx.x;
   const int v = blockIdx.x / nblk, blk = blockIdx.x % nblk;
   Part q;
   SegLoc s;
   if (!find_part(p, v, &q, &s)) return;
   if (LOCAL && q.k + 1 >= q.count) return;
-  // the second launch may begin: it waits before it reads anything of this one
-  if (LOCAL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // the block's channels: kChans of one group
   const int per = p.C_ / p.G, bpg = nblk / p.G, g = blk / bpg;
@@ -272,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S, LOCAL))
   fetch_rows(q.at, 0);
   fetch_bc(q.at);
 
-  // What the first launch wrote is read from here on.
-  if (!LOCAL && p.part) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // What the launch before this one wrote is read from here on.
+  if (!first) begin_after_stream();
 
   // The state at the part's start.  The carry slot of part 0 holds the slot's
   // own state, since the last part replaces that; slot k holds part k - 1's
@@ -429,8 +434,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S, LOCAL))
 template <int S>
 __global__ void __launch_bounds__(kThreads) scan_join_kernel(const ScanParams p, int nblk) {
   constexpr int L = S / kStates, kChans = 2 * kThreads / L, kAhead = 8;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  begin_after_stream();
   const int i = blockIdx.x / nblk, blk = blockIdx.x % nblk, n = blockIdx.y, tid = threadIdx.x;
   SegLoc s;
   if (!locate_segment(p.seg, i, &s) || s.len == 0) return;
@@ -501,23 +505,6 @@ int part_tokens(int N, int B, int C, int S, int G) {
   return (int)part;
 }
 
-// Launches a kernel; behind: its start overlaps the end of the launch before
-// it, whose results it waits for itself.
-cudaError_t launch_behind(void (*kernel)(ScanParams, int), dim3 grid, size_t smem, bool behind,
-                          cudaStream_t st, const ScanParams &p, int nblk) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = grid;
-  c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = smem;
-  c.stream = st;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &at;
-  c.numAttrs = behind ? 1 : 0;
-  return cudaLaunchKernelEx(&c, kernel, p, nblk);
-}
-
 template <typename T, int S, bool VEC, bool LOCAL>
 cudaError_t launch_pass(const ScanParams &p, int nblk, int parts, cudaStream_t st) {
   constexpr size_t smem = smem_bytes<T, S, LOCAL>();
@@ -528,7 +515,7 @@ cudaError_t launch_pass(const ScanParams &p, int nblk, int parts, cudaStream_t s
     if (e != cudaSuccess) return e;
   }
   const dim3 grid((unsigned)((long long)nblk * parts));
-  return launch_behind(kernel, grid, smem, !LOCAL && p.part != 0, st, p, nblk);
+  return launch_after(kernel, grid, dim3(kThreads), smem, st, p, nblk);
 }
 
 template <typename T, int S, bool VEC>
@@ -540,8 +527,8 @@ cudaError_t launch_prefill_v(ScanParams p, cudaStream_t st) {
   p.joined = p.seg.N / p.part > 16 * p.seg.B;
   cudaError_t e = launch_pass<T, S, VEC, true>(p, nblk, parts, st);
   if (e == cudaSuccess && p.joined)
-    e = launch_behind(scan_join_kernel<S>, dim3((unsigned)((long long)nblk * p.seg.B), kStates), 0,
-                      true, st, p, nblk);
+    e = launch_after(scan_join_kernel<S>, dim3((unsigned)((long long)nblk * p.seg.B), kStates),
+                     dim3(kThreads), 0, st, p, nblk);
   return e != cudaSuccess ? e : launch_pass<T, S, VEC, false>(p, nblk, parts, st);
 }
 

@@ -156,14 +156,18 @@ def _ptr(t):
 # The current stream's handle without building a Stream object: a single-token
 # step takes the GPU 2 us, and torch.cuda.current_stream() the host 3 us.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_ready = False  # the first call goes through torch, which sets CUDA up
 
 
 def _stream(stream):
+    global _raw_ready
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is not None and torch.cuda.is_initialized():
+    if _raw_ready:
         return _raw_stream(torch._C._cuda_getDevice())
-    return torch.cuda.current_stream().cuda_stream
+    handle = torch.cuda.current_stream().cuda_stream
+    _raw_ready = _raw_stream is not None
+    return handle
 
 
 def _dtype_code(dt):
@@ -521,9 +525,11 @@ def kda_conv_step(tok, pool, state_slots, commit_len=None, stream=None):
     """Steps of one or a few tokens a row; commit_len [B] int32: how many of a
     row's tokens the stored state takes in (None: all)."""
     B = tok.num_seqs
-    _check(lib().kda_conv_step(
+    st = (_lib or lib()).kda_conv_step(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots"),
-        _table(commit_len, B, "commit_len"), _stream(stream)), "kda_conv_step")
+        None if commit_len is None else _table(commit_len, B, "commit_len"), _stream(stream))
+    if st:
+        _check(st, "kda_conv_step")
 
 
 def kda_scan_workspace_size(num_tokens, num_seqs, channels, state, groups=1):
@@ -554,9 +560,11 @@ def kda_scan_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, star
 def kda_scan_step(tok, pool, state_slots, commit_len=None, stream=None):
     """The scan's steps, commit_len as in kda_conv_step."""
     B = tok.num_seqs
-    _check(lib().kda_scan_step(
+    st = (_lib or lib()).kda_scan_step(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots"),
-        _table(commit_len, B, "commit_len"), _stream(stream)), "kda_scan_step")
+        None if commit_len is None else _table(commit_len, B, "commit_len"), _stream(stream))
+    if st:
+        _check(st, "kda_scan_step")
 
 
 class SlotArrays:
