@@ -425,6 +425,8 @@ int kda_commit_snapshot(const int32_t *accepted_len, const int32_t *state_slots,
  *   - Outputs have the inputs' dtype, rounded once from fp32, and must not
  *     overlap any input.
  *   - The slots of one call must be distinct, checkpoint slots included.
+ *   - At most 65535 segments, 2^20 channels, 2^31 - 2^16 tokens, and 2^31 - 1
+ *     bytes between rows.
  *   - The kernels are launched as programmatic dependents of the previous work
  *     on the stream: they may start while it finishes, but touch no memory
  *     until it has, so stream order holds for every value they read or write.

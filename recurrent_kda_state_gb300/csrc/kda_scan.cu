@@ -359,21 +359,24 @@ __global__ void __launch_bounds__(kThreads, kPerSm) scan_rows_kernel(const ScanP
 }
 
 // Groups that the rows of a batch are dealt to, for gx blocks a group and
-// `room` blocks on the machine: the number that ends first, if a block takes
-// the time of its rows and of two more (its start).  Groups that overflow one
-// wave by a few blocks cost a second one: 256 rows of 4096 channels with 64
-// states took 115 us in 640 blocks where 608 fit, and 89 us by this rule.
+// `room` blocks on the machine: as many as fill one to four waves, whichever
+// ends first if a block takes the time of its rows and of two more (its
+// start).  Groups that overflow a wave by a few blocks cost another one: 256
+// rows of 4096 channels with 64 states took 115 us in 640 blocks where 608 fit,
+// and 89 us by this rule.
 int row_groups(int gx, int B, int room) {
+  const int least = (B + kMaxRows - 1) / kMaxRows;
   long long best = 0;
   int groups = 0;
-  for (int gy = (B + kMaxRows - 1) / kMaxRows; gy <= B; ++gy) {
+  for (int w = 1; w <= 4; ++w) {
+    int gy = w * room / gx;
+    gy = gy < least ? least : gy > B ? B : gy;
     const long long waves = ((long long)gx * gy + room - 1) / room;
     const long long cost = waves * ((B + gy - 1) / gy + 2);
-    if (!groups || cost <= best) {
+    if (!groups || cost < best) {
       best = cost;
       groups = gy;
     }
-    if ((long long)gx * gy >= 4LL * room) break;
   }
   return groups;
 }

@@ -9,6 +9,7 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ECUDA; }
 bool dtype_ok(int dt) { return dt == KDA_F32 || dt == KDA_BF16; }
 size_t elem(int dt) { return dt == KDA_F32 ? 4 : 2; }
 constexpr int kMaxSeqs = 65535;
+constexpr int kMaxTokens = 0x7fff0000;  // tiles may pass the last token
 constexpr int kMaxChannels = 1 << 20;
 constexpr int64_t kMaxStride = 0x7fffffff;  // bytes
 
@@ -27,7 +28,7 @@ int check_param(const void *p, bool needed) {
 int check_batch(int dt, int32_t B, int32_t N, int32_t D) {
   if (!dtype_ok(dt)) return KDA_EDTYPE;
   if (B < 0 || N < 0) return KDA_EINVAL;
-  if (B > kMaxSeqs || D < 1 || D > kMaxChannels) return KDA_ESHAPE;
+  if (B > kMaxSeqs || D < 1 || D > kMaxChannels || N > kMaxTokens) return KDA_ESHAPE;
   return KDA_OK;
 }
 
@@ -219,7 +220,7 @@ int kda_scan_prefill(const kda_scan_tokens *tok, kda_scan_pool *pool,
 
 size_t kda_scan_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t channels,
                                int32_t state, int32_t groups) {
-  if (num_tokens < 0 || num_seqs < 1 || num_seqs > kMaxSeqs || channels < 1 ||
+  if (num_tokens < 0 || num_tokens > kMaxTokens || num_seqs < 1 || num_seqs > kMaxSeqs || channels < 1 ||
       channels > kMaxChannels || !state_ok(state) || groups < 1 || channels % groups != 0)
     return 0;
   return kda::scan_workspace_floats(num_tokens, num_seqs, channels, state, groups) *

@@ -55,6 +55,7 @@ CONV = [(dict(dtype=7), {}, K.KDA_EDTYPE), ({}, dict(dtype=K.KDA_F32), K.KDA_EDT
         (dict(y=0x10000), {}, K.KDA_EINVAL), ({}, dict(base=None), K.KDA_EINVAL),
         (dict(num_seqs=-1), {}, K.KDA_EINVAL), (dict(num_tokens=-1), {}, K.KDA_EINVAL),
         (dict(num_seqs=65536), {}, K.KDA_ESHAPE), ({}, dict(num_slots=0), K.KDA_ESHAPE),
+        (dict(num_tokens=2 ** 31 - 1), {}, K.KDA_ESHAPE), (dict(x_stride=2 ** 30), {}, K.KDA_ESHAPE),
         (dict(cu_seqlens=0x50002), {}, K.KDA_EALIGN)]
 
 
@@ -91,7 +92,8 @@ SCAN = [(dict(dtype=7), {}, K.KDA_EDTYPE), (dict(state=24), dict(state=24), K.KD
         (dict(dt_bias=0x30004), {}, K.KDA_EALIGN), ({}, dict(base=0x60008), K.KDA_EALIGN),
         (dict(A=None), {}, K.KDA_EINVAL), (dict(B=None), {}, K.KDA_EINVAL),
         (dict(dt=None), {}, K.KDA_EINVAL), (dict(y=0x11000), {}, K.KDA_EINVAL),
-        (dict(num_seqs=-1), {}, K.KDA_EINVAL), (dict(num_seqs=65536), {}, K.KDA_ESHAPE)]
+        (dict(num_seqs=-1), {}, K.KDA_EINVAL), (dict(num_seqs=65536), {}, K.KDA_ESHAPE),
+        (dict(num_tokens=2 ** 31 - 1), {}, K.KDA_ESHAPE), (dict(b_stride=2 ** 30), {}, K.KDA_ESHAPE)]
 
 
 @pytest.mark.parametrize("tok,pool,want", SCAN)
@@ -117,6 +119,11 @@ def test_scan_tables_and_workspace(L):
     for bad in ((-1, 1, 64, 16, 1), (8, 0, 64, 16, 1), (8, 1, 0, 16, 1), (8, 1, 64, 24, 1),
                 (8, 1, 64, 16, 3), (8, 65536, 64, 16, 1)):
         assert K.kda_scan_workspace_size(*bad) == 0
+    wide = scan_tok(num_seqs=65535, channels=2 ** 20, state=128, x_stride=2 ** 20, b_stride=128,
+                    dt_stride=2 ** 20, y_stride=2 ** 20, c_stride=128)
+    assert call(by(wide), by(scan_pool(channels=2 ** 20, state=128)), PTR, None, 0, 0, None, None,
+                0, None) == K.KDA_ESHAPE                      # more blocks than a grid has
+    assert K.kda_scan_workspace_size(2 ** 30, 65535, 2 ** 20, 128) == 0
     none = scan_tok(num_seqs=0, num_tokens=0)
     assert call(by(none), by(p), None, None, 0, 0, None, None, 0, None) == K.KDA_OK
 
