@@ -23,13 +23,16 @@
 // segment is cut into parts: a first launch computes each part's end state
 // from a zero start and its sum of delta; the second starts part k from
 // h = exp(A sum_j delta) h + end_j over the parts before it, and does the rest.
-// Where segments have many parts, a launch between the two joins the ends
-// once instead of every part for itself (8192 tokens of 4096 channels in 48
-// parts: 281 us without it, 266 with it).  The first launch repeats the
-// exponentials (two fifths of the time), which is why segments are not cut
-// further than the machine has room for.
-// 266 us for 8192 x 4096 channels x 16 states in bf16 (268 MB: 40 us at the
-// copy bandwidth; the two bare loops alone 163 us).
+// The first launch repeats the exponentials (two fifths of the time of a
+// prompt that is cut everywhere).  Around the two:
+//   - in large ragged batches a launch before them lists the parts, the long
+//     ones first (scan_plan_kernel);
+//   - where segments have many parts, one between them joins the ends once
+//     instead of every part for itself (scan_join_kernel; 8192 tokens of 4096
+//     channels in 48 parts: 281 us without it, 266 with it).
+// 265 us for 8192 x 4096 channels x 16 states in bf16 (268 MB: 40 us at the
+// copy bandwidth; the two bare loops alone 163 us), 427 us for 16384 tokens in
+// 37 prompts of 0 to 2414.
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -91,16 +94,23 @@ __device__ __forceinline__ int part_count(int len, int r, int part) {
   return (int)(((long long)len + r + part - 1) / part);
 }
 
+template <bool LOCAL>
 __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, SegLoc *s) {
   const SegParams &g = p.seg;
-  int i = v;
-  if (p.part) {  // the last segment with cu[i] / part + 2 i <= v (room for its parts)
+  int i = v, k = -1;
+  if (p.table) {
+    const int2 total = p.table[0];
+    if (v >= (LOCAL ? total.y : total.x)) return false;
+    const int2 at = p.table[1 + v];
+    i = at.x;
+    k = at.y;
+  } else if (p.part) {  // the last segment with cu[i] / part + spare i <= v: room for its parts
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = g.B;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32;
       const int j = lo + lane * step;
-      const unsigned m = __ballot_sync(~0u, j < hi && g.cu[j] / p.part + 2 * j <= v);
+      const unsigned m = __ballot_sync(~0u, j < hi && g.cu[j] / p.part + p.spare * j <= v);
       lo += m ? (31 - __clz(m)) * step : 0;
       hi = min(lo + step, hi);
     }
@@ -117,8 +127,8 @@ __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, S
     q->at = -r;
     q->hi = s->len;
   } else {
-    q->v0 = s->begin / p.part + 2 * i;
-    q->k = v - q->v0;
+    q->v0 = s->begin / p.part + p.spare * i;
+    q->k = k >= 0 ? k : v - q->v0;
     q->count = part_count(s->len, r, p.part);
     if (q->k < 0 || q->k >= q->count) return false;
     const long long at = (long long)q->k * p.part - r;
@@ -127,6 +137,62 @@ __device__ __forceinline__ bool find_part(const ScanParams &p, int v, Part *q, S
   }
   q->lo = max(0, q->at);
   return true;
+}
+
+// The parts of all segments in the order they are worked on, as {segment,
+// part}: first all but each segment's last part, which are the longest, then
+// the last ones by falling length.  Long blocks that start last would keep the
+// machine waiting, and blocks with nothing to do, scattered among the others,
+// would leave the work unevenly spread over the SMs.  One block.
+constexpr int kPlanThreads = 1024, kBuckets = 64;
+__global__ void __launch_bounds__(kPlanThreads)
+    scan_plan_kernel(const ScanParams p, int room, int room_local) {
+  __shared__ unsigned long long first[kBuckets];  // parts of a length, then where they go
+  __shared__ bool sound;
+  begin_after_stream();
+  const int tid = threadIdx.x;
+  if (tid < kBuckets) first[tid] = 0;
+  __syncthreads();
+  auto segment = [&](int i, int *count, int *bucket) {
+    SegLoc s;
+    if (!locate_segment(p.seg, i, &s) || s.len == 0) return false;
+    const int r = (int)(first_position(p.seg, i) & (kTile - 1));
+    *count = part_count(s.len, r, p.part);
+    const long long last = s.len + r - (*count - 1LL) * p.part;  // tokens, 1 .. part
+    *bucket = 1 + (int)((p.part - last) * (kBuckets - 2) / p.part);
+    return true;
+  };
+  int n, b;
+  for (int i = tid; i < p.seg.B; i += kPlanThreads) {
+    if (!segment(i, &n, &b)) continue;
+    if (n > 1) atomicAdd(&first[0], (unsigned long long)(n - 1));
+    atomicAdd(&first[b], 1ull);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    const unsigned long long local = first[0];
+    unsigned long long sum = 0;
+    for (int k = 0; k < kBuckets; ++k) {
+      const unsigned long long c = first[k];
+      first[k] = sum;
+      sum += c;
+    }
+    // Segments that overlap can have more parts than the table has room for:
+    // nothing is done then.
+    sound = sum <= (unsigned)room && local <= (unsigned)room_local;
+    p.table[0] = sound ? make_int2((int)sum, (int)local) : make_int2(0, 0);
+    if (!sound) set_error(p.seg.err, KDA_DERR_SEGMENT);
+  }
+  __syncthreads();
+  if (!sound) return;
+  for (int i = tid; i < p.seg.B; i += kPlanThreads) {
+    if (!segment(i, &n, &b)) continue;
+    if (n > 1) {
+      const int at = (int)atomicAdd(&first[0], (unsigned long long)(n - 1));
+      for (int k = 0; k < n - 1; ++k) p.table[1 + at + k] = make_int2(i, k);
+    }
+    p.table[1 + (int)atomicAdd(&first[b], 1ull)] = make_int2(i, n - 1);
+  }
 }
 
 // LOCAL: the first launch (end states of the parts, no outputs).
@@ -145,18 +211,19 @@ __global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S, LOCAL))
   constexpr int kBC = (LOCAL ? 1 : 2) * kTile * S;
   float4 *swarp = reinterpret_cast<float4 *>(sbc + 2 * kBC);     // [2][kThreads]
 
-  // The first launch of a call waits for the stream before it lets the second
+  // The first launch of a call waits for the stream before it lets the next
   // begin, so that one may read the call's inputs at once and waits only for
-  // the carried states.
+  // the carried states.  A large batch waits for the launch to end: blocks that
+  // start into the gaps it leaves are unevenly spread.
   const bool first = LOCAL || !p.part;
   if (first) begin_after_stream();
-  if (LOCAL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (LOCAL && !p.table) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int tid = threadIdx.x;
   const int v = blockIdx.x / nblk, blk = blockIdx.x % nblk;
   Part q;
   SegLoc s;
-  if (!find_part(p, v, &q, &s)) return;
+  if (!find_part<LOCAL>(p, v, &q, &s)) return;
   if (LOCAL && q.k + 1 >= q.count) return;
 
   // the block's channels: kChans of one group
@@ -448,7 +515,7 @@ __global__ void __launch_bounds__(kThreads) scan_join_kernel(const ScanParams p,
   const f2 a = pack2(exponent_scale(p.A[ca * S + st]), exponent_scale(p.A[cb * S + st]));
 
   const long long step = (long long)nblk * kCarry * kThreads;
-  float *w = p.ws + (s.begin / p.part + 2 * i + 1LL) * step +
+  float *w = p.ws + (s.begin / p.part + p.spare * i + 1LL) * step +
              (long long)blk * kCarry * kThreads + tid;  // carry slot 1
   f2 h = pack2(w[(2 * n) * kThreads], w[(2 * n + 1) * kThreads]);
   for (int k = 2; k < count; k += kAhead) {
@@ -485,15 +552,21 @@ int blocks_of_row(int C, int S, int G) {
   return G * ((C / G + chans - 1) / chans);
 }
 
-// Tokens of a part, 0 to walk segments whole.  A part is an equal share of
-// the batch's work for 152 SMs of five blocks and two waves, so a batch that
-// fills them anyway is not cut, and a long segment beside short ones is.  Two
-// waves even out the parts' lengths (16384 tokens in 37 prompts: 495 us, 597 in
-// one wave, 503 in three).
+// Tokens of a part, 0 to walk segments whole.  (Figures: 4096 channels with 16
+// states, bf16.)
 int part_tokens(int N, int B, int C, int S, int G) {
-  const long long nblk = blocks_of_row(C, S, G), room = 152LL * blocks_of(2, S, false) * 2;
+  const long long nblk = blocks_of_row(C, S, G), room = 152LL * blocks_of(2, S, false);
   if (2LL * B * nblk > 0x7fffffffLL) return 0;
-  long long part = ((long long)N * nblk + room - 1) / room;
+  // An equal share of the work for two waves of blocks: a batch that fills the
+  // machine by itself is not cut, a long segment beside short ones is (8192
+  // tokens in one prompt: 266 us; 274 in one wave or in three).
+  long long part = ((long long)N * nblk + 2 * room - 1) / (2 * room);
+  // With two blocks an SM before any cut, not below a quarter over the mean
+  // length: a cut costs the first launch, and gains only what blocks longer
+  // than others waste at the end (37 prompts of 443 tokens: 319 us whole, 517
+  // in halves; 37 prompts of 0 to 2414, 16384 in all: 427 us, 486 at the share).
+  const long long mean = (5LL * N / B + 3) / 4;
+  if (B * nblk >= 2 * 152 && part < mean) part = mean;
   part = (part + kTile - 1) / kTile * kTile;
   // A part walks its tokens and then the parts before it, at about the same
   // time each, so parts below sqrt(N) tokens gain nothing; and 32 tokens are
@@ -503,6 +576,11 @@ int part_tokens(int N, int B, int C, int S, int G) {
   if (part >= N) return 0;
   while (((long long)N / part + 2LL * B) * nblk > 0x7fffffffLL) part *= 2;
   return (int)part;
+}
+
+// Floats of the table of parts at the start of the workspace.
+size_t table_floats(int N, int B, int part) {
+  return (2 * (1 + (size_t)N / part + 2 * (size_t)B) + 63) / 64 * 64;
 }
 
 template <typename T, int S, bool VEC, bool LOCAL>
@@ -523,9 +601,21 @@ cudaError_t launch_prefill_v(ScanParams p, cudaStream_t st) {
   const int nblk = blocks_of_row(p.C_, S, p.G);
   p.part = p.ws ? part_tokens(p.seg.N, p.seg.B, p.C_, S, p.G) : 0;
   if (!p.part) return launch_pass<T, S, VEC, false>(p, nblk, p.seg.B, st);
-  const int parts = p.seg.N / p.part + 2 * p.seg.B;
+  p.spare = p.seg.ckpt_slots && p.seg.start_pos ? 2 : 1;
+  const int parts = p.seg.N / p.part + p.spare * p.seg.B;
   p.joined = p.seg.N / p.part > 16 * p.seg.B;
-  cudaError_t e = launch_pass<T, S, VEC, true>(p, nblk, parts, st);
+  int local = parts;
+  cudaError_t e = cudaSuccess;
+  p.table = nullptr;
+  // The order of the parts is worth its launch where the blocks' tokens come to
+  // some 50 us (16384 tokens in 37 prompts: 427 us with it, 505 without).
+  if (p.seg.B > 1 && (long long)p.seg.N * nblk >= 100000) {
+    p.table = reinterpret_cast<int2 *>(p.ws);
+    local = parts - p.seg.B;
+    e = launch_after(scan_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, parts, local);
+  }
+  p.ws += table_floats(p.seg.N, p.seg.B, p.part);
+  if (e == cudaSuccess && local > 0) e = launch_pass<T, S, VEC, true>(p, nblk, local, st);
   if (e == cudaSuccess && p.joined)
     e = launch_after(scan_join_kernel<S>, dim3((unsigned)((long long)nblk * p.seg.B), kStates),
                      dim3(kThreads), 0, st, p, nblk);
@@ -565,7 +655,8 @@ long long scan_prefill_blocks(int B, int C, int S, int G) {
 size_t scan_workspace_floats(int N, int B, int C, int S, int G) {
   const int part = part_tokens(N, B, C, S, G);
   if (!part) return 0;
-  return ((size_t)N / part + 2 * (size_t)B) * blocks_of_row(C, S, G) * kCarry * kThreads;
+  return table_floats(N, B, part) +
+         ((size_t)N / part + 2 * (size_t)B) * blocks_of_row(C, S, G) * kCarry * kThreads;
 }
 
 }  // namespace kda

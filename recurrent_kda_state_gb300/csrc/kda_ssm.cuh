@@ -44,7 +44,9 @@ struct ScanParams {
   float *ws;  // prompts: carried states of split segments, or NULL
   int C_, S, G, softplus;
   int part;  // prompts: tokens of a part, 0 = segments are not split
+  int spare;   // prompts: part numbers kept for a segment beyond len / part
   int joined;  // prompts: a launch of its own has joined the parts' states
+  int2 *table;  // prompts: {parts, parts but the last ones}, then {segment, part}; or NULL
 };
 
 constexpr int kMaxSlotArrays = 64;

@@ -400,6 +400,22 @@ def test_bad_device_data_is_skipped_and_reported():
     K.kda_get_device_error()
 
 
+def test_overlapping_segments_are_reported():
+    """A segment table that runs over the batch again and again has more parts
+    than a large ragged batch has room for: nothing is done, the bit is set."""
+    D, S, n, B = 384, 128, 8000, 41
+    x = torch.zeros(n, D, device="cuda")
+    b = torch.zeros(n, 1, S, device="cuda")
+    A = -torch.ones(D, S, device="cuda")
+    cu = i32([0 if i % 2 == 0 else n for i in range(B + 1)])
+    pool = K.ScanPool(torch.full((B, D, S), 3.0, device="cuda"))
+    batch = K.ScanBatch(x, x.clone(), A, b, b, cu_seqlens=cu)
+    batch.y.fill_(5.0)
+    K.kda_scan_prefill(batch, pool, i32(np.arange(B)), workspace=K.scan_workspace(batch))
+    assert K.kda_get_device_error() == K.KDA_DERR_SEGMENT
+    assert bool((batch.y == 5.0).all()) and bool((pool.data == 3.0).all())
+
+
 # -------------------------------------------------------------------- moves
 def move_case(seed, P, src, dst, ws=True, shapes=((4, 33), (128, 16), (5000, 2))):
     rng = np.random.default_rng(seed)
@@ -510,3 +526,15 @@ def test_moves_in_columns(seed):
     live = dst[dst >= 0]
     assert len(set(live.tolist())) == len(live)
     move_case(40 + seed, P, src, dst, shapes=((512, 516), (1024, 513), (4, 4)))
+
+
+def test_scan_prefill_ragged_batches_take_their_parts_in_order():
+    """Batches so large that their parts are listed first: split and whole
+    segments, empty ones, checkpoints and starts that are no multiple of 16."""
+    rng = np.random.default_rng(50)
+    lens = np.concatenate([rng.integers(0, 60, 90), [2100, 0, 1300, 1, 16, 900]])
+    rng.shuffle(lens)
+    scan_case(51, "bf16", lens, 16 * 24, 128)
+    scan_case(52, "f32", lens, 16 * 24, 128, every=64, max_ckpt=2,
+              start=rng.integers(0, 100, len(lens)))
+    scan_case(53, "bf16", rng.integers(0, 30, 3000), 48, 128)
