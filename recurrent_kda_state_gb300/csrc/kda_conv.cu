@@ -7,7 +7,7 @@
 // the W - 1 previous rows in registers and eight rows ahead under way, as
 // raw elements: the place of a row that was used takes the row eight on.  Four channels, not the eight of a
 // 16-byte bf16 vector: those took 190 registers, which left eight warps an SM
-// and 165 us where this takes 73, 81 % of the copy bandwidth (8192 x 12288, W = 4).
+// and 165 us where this takes 70, 84 % of the copy bandwidth (8192 x 12288, W = 4).
 // A prompt's segments are cut into tiles of p.tile tokens, each with its own
 // W - 1 rows before it.  Tile 0 alone reads the slot and alone writes it (it
 // fetches the segment's last rows itself), so no other block can see a state

@@ -496,11 +496,11 @@ __global__ void __launch_bounds__(kThreads, blocks_of(sizeof(T), S, LOCAL))
 
 // Joins the parts of each segment: carry slot k, which holds the end of part
 // k - 1 from a zero start, becomes the state that part k starts from.  One
-// thread per two states (blockIdx.y: which of a thread's); the loads of eight
+// thread per two states (blockIdx.y: which of a thread's); the loads of 16
 // parts are under way at a time.
 template <int S>
 __global__ void __launch_bounds__(kThreads) scan_join_kernel(const ScanParams p, int nblk) {
-  constexpr int L = S / kStates, kChans = 2 * kThreads / L, kAhead = 8;
+  constexpr int L = S / kStates, kChans = 2 * kThreads / L, kAhead = 16;
   begin_after_stream();
   const int i = blockIdx.x / nblk, blk = blockIdx.x % nblk, n = blockIdx.y, tid = threadIdx.x;
   SegLoc s;
