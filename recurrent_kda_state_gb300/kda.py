@@ -573,14 +573,14 @@ class SlotArrays:
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
-        if not self.tensors:
-            raise ValueError("no arrays")
+        if not self.tensors or self.tensors[0].shape[0] < 1:
+            raise ValueError("no arrays, or no slots")
         self.num_slots = int(self.tensors[0].shape[0])
         for t in self.tensors:
             if not t.is_contiguous() or t.shape[0] != self.num_slots:
                 raise ValueError("every array is a contiguous [num_slots][...]")
         self.c = (kda_slot_array * len(self.tensors))(
-            *[kda_slot_array(t.data_ptr(), t[0].numel() * t.element_size())
+            *[kda_slot_array(t.data_ptr(), t.numel() // self.num_slots * t.element_size())
               for t in self.tensors])
 
 
