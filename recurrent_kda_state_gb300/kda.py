@@ -598,10 +598,12 @@ def kda_move_slots(arrays, src, dst, workspace=None, stream=None):
     """In every array: slot dst[i] receives slot src[i] (src < 0: zeros, dst < 0:
     nothing).  workspace None: src and dst must be disjoint."""
     n = dst.numel()
-    _check(lib().kda_move_slots(
+    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    st = (_lib or lib()).kda_move_slots(
         arrays.c, len(arrays.tensors), arrays.num_slots, _table(src, n, "src"),
-        _table(dst, n, "dst"), n, None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _stream(stream)), "kda_move_slots")
+        _table(dst, n, "dst"), n, ws, size, _stream(stream))
+    if st:
+        _check(st, "kda_move_slots")
 
 
 def kda_get_device_error(stream=None):

@@ -400,6 +400,24 @@ def test_bad_device_data_is_skipped_and_reported():
     K.kda_get_device_error()
 
 
+@pytest.mark.parametrize("lens", [[2000], [700, 0, 90, 33, 5] * 30])
+def test_the_same_call_gives_the_same_bits(lens):
+    """In whatever order the parts of a batch are worked on."""
+    rng = np.random.default_rng(54)
+    D, S, n, B = 512, 64, sum(lens), len(lens)
+    x, d = (rows(rng, n, (D,), "bf16", False) for _ in range(2))
+    b, c = (rows(rng, n, (1, S), "bf16", False) for _ in range(2))
+    A = torch.from_numpy(-np.exp(rng.uniform(-2, 2, (D, S)))).to("cuda", torch.float32)
+    seen = []
+    for _ in range(4):
+        pool = K.ScanPool.zeros(B, D, S)
+        batch = K.ScanBatch(x, d, A, b, c, cu_seqlens=i32(cumulate(lens)))
+        K.kda_scan_prefill(batch, pool, i32(np.arange(B)), workspace=K.scan_workspace(batch))
+        seen.append((batch.y, pool.data))
+    for y, states in seen[1:]:
+        assert torch.equal(y, seen[0][0]) and torch.equal(states, seen[0][1])
+
+
 def test_overlapping_segments_are_reported():
     """A segment table that runs over the batch again and again has more parts
     than a large ragged batch has room for: nothing is done, the bit is set."""
