@@ -7,7 +7,7 @@
 // the W - 1 previous rows in registers and eight rows ahead under way, as
 // raw elements: the place of a row that was used takes the row eight on.  Four channels, not the eight of a
 // 16-byte bf16 vector: those took 190 registers, which left eight warps an SM
-// and 165 us where this takes 70, 84 % of the copy bandwidth (8192 x 12288, W = 4).
+// and 165 us where this takes 68, 87 % of the copy bandwidth (8192 x 12288, W = 4).
 // A prompt's segments are cut into tiles of p.tile tokens, each with its own
 // W - 1 rows before it.  Tile 0 alone reads the slot and alone writes it (it
 // fetches the segment's last rows itself), so no other block can see a state
@@ -19,7 +19,20 @@ namespace {
 
 constexpr int kBlocks = 6;    // of 128 threads on an SM (registers)
 constexpr int kTileUnit = 8;  // tiles are multiples of this many tokens,
-constexpr int kMaxTile = 32;  // and this long where there are enough of them
+constexpr int kMaxTile = 48;  // and this long where there are enough of them
+
+// V values in fp32, as packed pairs where there are four: one instruction for
+// two channels.
+template <int V>
+struct Vals {
+  using P = typename std::conditional<V == 1, float, f2>::type;
+  static constexpr int N = V == 1 ? 1 : V / 2;
+  P v[N];
+};
+__device__ __forceinline__ float madd(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ f2 madd(f2 a, f2 b, f2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ float silu_of(float v) { return silu_f(v); }
+__device__ __forceinline__ f2 silu_of(f2 v) { return silu2(v); }
 
 // V elements as they are in memory (V = 1, or 4 of them aligned as a whole).
 template <typename T, int V>
@@ -39,32 +52,33 @@ struct Elems {
     if constexpr (V == 1) store(p);
     else __stcs(reinterpret_cast<Raw *>(p), r);
   }
-  __device__ __forceinline__ void get(float *v) const {
+  __device__ __forceinline__ Vals<V> get() const {
+    Vals<V> o;
     if constexpr (V == 1) {
-      v[0] = in_scalar<T>(&r);
+      o.v[0] = in_scalar<T>(&r);
     } else if constexpr (sizeof(T) == 4) {
-      v[0] = __uint_as_float(r.x);
-      v[1] = __uint_as_float(r.y);
-      v[2] = __uint_as_float(r.z);
-      v[3] = __uint_as_float(r.w);
+      o.v[0] = pack2(__uint_as_float(r.x), __uint_as_float(r.y));
+      o.v[1] = pack2(__uint_as_float(r.z), __uint_as_float(r.w));
     } else {
-      v[0] = __uint_as_float(r.x << 16);
-      v[1] = __uint_as_float(r.x & 0xffff0000u);
-      v[2] = __uint_as_float(r.y << 16);
-      v[3] = __uint_as_float(r.y & 0xffff0000u);
+      o.v[0] = pack2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
+      o.v[1] = pack2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
     }
+    return o;
   }
-  __device__ __forceinline__ void set(const float *v) {
+  __device__ __forceinline__ void set(const Vals<V> &o) {
     if constexpr (V == 1) {
-      r = out_scalar<T>(v[0]);
-    } else if constexpr (sizeof(T) == 4) {
-      r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                     __float_as_uint(v[3]));
+      r = out_scalar<T>(o.v[0]);
     } else {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]);
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2], v[3]);
-      r = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
-                     *reinterpret_cast<const uint32_t *>(&b));
+      const float2 a = unpack2(o.v[0]), b = unpack2(o.v[1]);
+      if constexpr (sizeof(T) == 4) {
+        r = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                       __float_as_uint(b.y));
+      } else {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(a.x, a.y);
+        const __nv_bfloat162 q = __floats2bfloat162_rn(b.x, b.y);
+        r = make_uint2(*reinterpret_cast<const uint32_t *>(&p),
+                       *reinterpret_cast<const uint32_t *>(&q));
+      }
     }
   }
 };
@@ -73,21 +87,33 @@ struct Elems {
 // looked up, which they do not depend on.
 template <typename T, int V, int W>
 struct Taps {
-  float w[W][V], bias[V];
+  Vals<V> w[W], bias;
   __device__ __forceinline__ Taps(const ConvParams &p, int c) {
+    const T *wp = static_cast<const T *>(p.weight) + (long long)c * W;
     const T *bp = static_cast<const T *>(p.bias);
-    float flat[V * W];  // [channel][tap]
+    float flat[W][V], b[V];
+    alignas(16) T e[V * W];  // [channel][tap]
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      Elems<T, V> e;
-      e.load(static_cast<const T *>(p.weight) + (long long)c * W + j * V);
-      e.get(flat + j * V);
+      Elems<T, V> q;
+      q.load(wp + j * V);
+      *reinterpret_cast<typename Elems<T, V>::Raw *>(e + j * V) = q.r;
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      bias[e] = bp ? in_scalar<T>(bp + c + e) : 0.0f;
+    for (int u = 0; u < V; ++u) {
+      b[u] = bp ? in_scalar<T>(bp + c + u) : 0.0f;
 #pragma unroll
-      for (int j = 0; j < W; ++j) w[j][e] = flat[e * W + j];
+      for (int j = 0; j < W; ++j) flat[j][u] = in_scalar<T>(&e[u * W + j]);
+    }
+#pragma unroll
+    for (int n = 0; n < Vals<V>::N; ++n) {
+      if constexpr (V == 1) bias.v[n] = b[n];
+      else bias.v[n] = pack2(b[2 * n], b[2 * n + 1]);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        if constexpr (V == 1) w[j].v[n] = flat[j][n];
+        else w[j].v[n] = pack2(flat[j][2 * n], flat[j][2 * n + 1]);
+      }
     }
   }
 };
@@ -143,22 +169,22 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
   }
 
   T *out = row_at(y, t0, p.ys);
+  Vals<V> last[W - 1];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) last[j] = win[j].get();
   auto token = [&](const E &cur) {
-    float acc[V], v[V];
+    const Vals<V> x = cur.get();
+    Vals<V> acc = f.bias;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = f.bias[e];
+    for (int n = 0; n < Vals<V>::N; ++n) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      (j < W - 1 ? win[j] : cur).get(v);
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(f.w[j][e], v[e], acc[e]);
+      for (int j = 0; j < W - 1; ++j) acc.v[n] = madd(f.w[j].v[n], last[j].v[n], acc.v[n]);
+      acc.v[n] = madd(f.w[W - 1].v[n], x.v[n], acc.v[n]);
+      if (p.silu) acc.v[n] = silu_of(acc.v[n]);
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (p.silu) acc[e] = silu_f(acc[e]);
-#pragma unroll
-    for (int j = 0; j + 1 < W - 1; ++j) win[j] = win[j + 1];
-    win[W - 2] = cur;
+    for (int j = 0; j + 1 < W - 1; ++j) last[j] = last[j + 1];
+    last[W - 2] = x;
     E o;
     o.set(acc);
     o.store_once(out);
