@@ -4,10 +4,11 @@
 //
 // Memory bound: x is read and y written once, 2 W + 4 flops a value.  A
 // thread owns four neighbouring channels and walks down a run of tokens with
-// the W - 1 previous rows in registers and eight rows ahead under way, as
-// raw elements: the place of a row that was used takes the row eight on.  Four channels, not the eight of a
-// 16-byte bf16 vector: those took 190 registers, which left eight warps an SM
-// and 165 us where this takes 68, 87 % of the copy bandwidth (8192 x 12288, W = 4).
+// the W - 1 previous rows in registers and eight rows (six in fp32) under way,
+// as raw elements: the place of a row that was used takes a new one.  Four
+// channels, not the eight of a 16-byte bf16 vector: those took 190 registers,
+// which left eight warps an SM and 165 us where this takes 65, 91 % of the copy
+// bandwidth (8192 x 12288, W = 4).
 // A prompt's segments are cut into tiles of p.tile tokens, each with its own
 // W - 1 rows before it.  Tile 0 alone reads the slot and alone writes it (it
 // fetches the segment's last rows itself), so no other block can see a state
@@ -17,7 +18,17 @@
 namespace kda {
 namespace {
 
-constexpr int kBlocks = 6;    // of 128 threads on an SM (registers)
+// Blocks of 128 threads on an SM, and rows of loads in flight of a thread: what
+// registers leave (bf16 68 us with six blocks, 84 with eight; fp32 8.2 us with
+// five blocks and six rows, 8.6 with six and four, 5003 x 1000).
+template <typename T>
+__host__ __device__ constexpr int blocks_of() {
+  return sizeof(T) == 2 ? 7 : 5;
+}
+template <typename T>
+__host__ __device__ constexpr int rows_ahead() {
+  return sizeof(T) == 2 ? 8 : 6;
+}
 constexpr int kTileUnit = 8;  // tiles are multiples of this many tokens,
 constexpr int kMaxTile = 48;  // and this long where there are enough of them
 
@@ -123,7 +134,7 @@ template <typename T, int V, int W>
 __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W> &f,
                                          const SegLoc &s, int i, int c, int t0, int t1) {
   using E = Elems<T, V>;
-  constexpr int kRows = sizeof(T) == 2 ? 8 : 4;  // of loads in flight
+  constexpr int kRows = rows_ahead<T>();
   const long long D = p.D;
   const T *x = row_at(static_cast<const T *>(p.x), s.begin, p.xs) + c;
   T *y = row_at(static_cast<T *>(p.y), s.begin, p.ys) + c;
@@ -211,7 +222,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, const Taps<T, V, W
 
 // One row of threads (threadIdx.y) per tile; blockIdx.x: channels.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(128, kBlocks) conv_step_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(128, blocks_of<T>()) conv_step_kernel(const ConvParams p) {
   begin_after_stream();
   const int i = blockIdx.y * blockDim.y + threadIdx.y;
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V;
@@ -239,7 +250,7 @@ __device__ __forceinline__ int find_segment(const SegParams &p, int g, int tile)
 }
 
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(128, kBlocks) conv_prefill_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(128, blocks_of<T>()) conv_prefill_kernel(const ConvParams p) {
   begin_after_stream();
   const int g = blockIdx.y * blockDim.y + threadIdx.y;
   const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V;
@@ -265,7 +276,7 @@ cudaError_t launch_w(const ConvParams &p, bool step, cudaStream_t st) {
   }
   // Tiles as long as leaves every SM its blocks of 128 threads once.
   ConvParams q = p;
-  const long long want = 152LL * kBlocks * 128;
+  const long long want = 152LL * blocks_of<T>() * 128;
   long long tile = (long long)p.seg.N * nvec / want / kTileUnit * kTileUnit + kTileUnit;
   q.tile = (int)(tile < kTileUnit ? kTileUnit : tile > kMaxTile ? kMaxTile : tile);
   long long tiles = (long long)p.seg.N / q.tile + p.seg.B;
