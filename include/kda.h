@@ -521,8 +521,10 @@ int kda_conv_step(const kda_conv_tokens *tok, kda_conv_pool *pool,
  * workspace: kda_scan_workspace_size(...) bytes, 256-byte aligned, owned by
  * the caller and not used by another call until this one completes; with it
  * long segments are split into parts that run at the same time.  NULL: every
- * segment is walked by itself.  Both meet the same tolerances; they are not
- * bit-identical to each other.
+ * segment is walked by itself, the faster way for prompts of like lengths that
+ * give every SM two or more blocks of 2048 / S channels (the lengths are on
+ * the device, so the call does not know).  Both meet the same tolerances; they
+ * are not bit-identical to each other.
  */
 int kda_scan_prefill(const kda_scan_tokens *tok, kda_scan_pool *pool,
                      const int32_t *state_slots, const int32_t *ckpt_slots,

@@ -31,7 +31,7 @@
 //     instead of every part for itself (scan_join_kernel; 8192 tokens of 4096
 //     channels in 48 parts: 281 us without it, 266 with it).
 // 265 us for 8192 x 4096 channels x 16 states in bf16 (268 MB: 40 us at the
-// copy bandwidth; the two bare loops alone 163 us), 427 us for 16384 tokens in
+// copy bandwidth; the two bare loops alone 163 us), 428 us for 16384 tokens in
 // 37 prompts of 0 to 2414.
 #include "kda_ssm.cuh"
 
@@ -561,12 +561,14 @@ int part_tokens(int N, int B, int C, int S, int G) {
   // machine by itself is not cut, a long segment beside short ones is (8192
   // tokens in one prompt: 266 us; 274 in one wave or in three).
   long long part = ((long long)N * nblk + 2 * room - 1) / (2 * room);
-  // With two blocks an SM before any cut, not below a quarter over the mean
-  // length: a cut costs the first launch, and gains only what blocks longer
-  // than others waste at the end (37 prompts of 443 tokens: 319 us whole, 517
-  // in halves; 37 prompts of 0 to 2414, 16384 in all: 427 us, 486 at the share).
-  const long long mean = (5LL * N / B + 3) / 4;
-  if (B * nblk >= 2 * 152 && part < mean) part = mean;
+  // With three blocks an SM before any cut, not below twice the mean length: a
+  // cut costs the first launch, and gains only what blocks longer than others
+  // waste at the end (32 prompts of 512 tokens: 336 us whole, 452 at the share; 40
+  // of 1 to 900: 435 and 566; 37 of 0 to 2414, 16384 tokens in all: 428 and 422,
+  // and 604 whole).  With fewer blocks the longest prompt would last longer
+  // than the rest (12 of 1 to 3000: 521 us at the share, 709 with this rule).
+  const long long twice = (2LL * N + B - 1) / B;
+  if (B * nblk >= 3 * 152 && part < twice) part = twice;
   part = (part + kTile - 1) / kTile * kTile;
   // A part walks its tokens and then the parts before it, at about the same
   // time each, so parts below sqrt(N) tokens gain nothing; and 32 tokens are
@@ -608,7 +610,7 @@ cudaError_t launch_prefill_v(ScanParams p, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   p.table = nullptr;
   // The order of the parts is worth its launch where the blocks' tokens come to
-  // some 50 us (16384 tokens in 37 prompts: 427 us with it, 505 without).
+  // some 50 us (16384 tokens in 37 prompts: 428 us with it, 505 without).
   if (p.seg.B > 1 && (long long)p.seg.N * nblk >= 100000) {
     p.table = reinterpret_cast<int2 *>(p.ws);
     local = parts - p.seg.B;
