@@ -516,8 +516,9 @@ int kda_conv_step(const kda_conv_tokens *tok, kda_conv_pool *pool,
  *     delta = softplus(dt[d] + dt_bias[d])
  *     h[d][n] = exp(delta * A[d][n]) * h[d][n] + delta * x[d] * B[g][n]
  *     y[d] = (sum_n C[g][n] * h[d][n] + D[d] * x[d]) * z[d] * sigmoid(z[d])
- * The state, the sum over n and delta are fp32.  The slot receives the last
- * state.  Checkpoints as above, with ckpt_every a multiple of 16.
+ * The state, the sum over n and delta are fp32.  A = -inf forgets the state at
+ * every delta > 0 and leaves it at delta = 0 (here and in the steps).  The slot
+ * receives the last state.  Checkpoints as above, with ckpt_every a multiple of 16.
  * workspace: kda_scan_workspace_size(...) bytes, 256-byte aligned, owned by
  * the caller and not used by another call until this one completes; with it
  * long segments are split into parts that run at the same time.  NULL: every

@@ -91,8 +91,9 @@ __device__ __forceinline__ void load_decay(const float *A, int c, int l, f2 (&a)
   for (int j = 0; j < kQuads; ++j) {  // states 4 (l + L j) + {0 .. 3}, as pairs
     const ulonglong2 v =
         *reinterpret_cast<const ulonglong2 *>(A + (long long)c * S + 4 * (l + L * j));
-    a[2 * j] = mul2(v.x, both(kLog2e));
-    a[2 * j + 1] = mul2(v.y, both(kLog2e));
+    const float2 x = unpack2(v.x), y = unpack2(v.y);
+    a[2 * j] = pack2(exponent_scale(x.x), exponent_scale(x.y));
+    a[2 * j + 1] = pack2(exponent_scale(y.x), exponent_scale(y.y));
   }
 }
 

@@ -61,13 +61,6 @@ struct Shape {
   static constexpr int kPitch = kChans * (int)sizeof(T) + (kPad < 16 ? 16 : kPad);
 };
 
-// A log2(e), -inf held at the lowest finite value: a token that pads a tile has
-// delta = 0, and 0 * -inf would be NaN.
-__device__ __forceinline__ float exponent_scale(float a) {
-  const float r = a * kLog2e;
-  return r < -3.4028234e38f ? -3.4028234e38f : r;
-}
-
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }

@@ -148,6 +148,13 @@ __device__ __forceinline__ float rcpf(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
+// A log2(e), -inf held at the lowest finite value: a time step of 0, such as
+// that of a token which pads a tile, leaves the state, and 0 * -inf would be NaN.
+__device__ __forceinline__ float exponent_scale(float a) {
+  const float r = a * kLog2e;
+  return r < -3.4028234e38f ? -3.4028234e38f : r;
+}
+
 // v * sigmoid(v).  Below about -88 the reciprocal of 1 + e^-v is 0, as is the
 // value in fp32; -inf gives NaN, as -inf / (1 + inf) does.
 __device__ __forceinline__ float silu_f(float v) { return v * rcpf(1.0f + ex2f(-kLog2e * v)); }

@@ -556,3 +556,40 @@ def test_scan_prefill_ragged_batches_take_their_parts_in_order():
     scan_case(52, "f32", lens, 16 * 24, 128, every=64, max_ckpt=2,
               start=rng.integers(0, 100, len(lens)))
     scan_case(53, "bf16", rng.integers(0, 30, 3000), 48, 128)
+
+
+@pytest.mark.parametrize("S", [16, 128])
+def test_states_that_forget_all(S):
+    """A = -inf: a token of a time step above 0 forgets what was there, one of a
+    time step of 0 leaves it, in prompts (whole and cut) and in steps alike."""
+    rng = np.random.default_rng(82)
+    D, n = 24, 300
+    x, d = rows(rng, n, (D,), "f32", False), rows(rng, n, (D,), "f32", False).abs()
+    d[torch.from_numpy(rng.random(n) < 0.5).cuda()] = 0.0
+    d[:2], d[-1] = 0.0, 0.0
+    b, c = (rows(rng, n, (1, S), "f32", False) for _ in range(2))
+    A = torch.from_numpy(-np.exp(rng.uniform(-2, 2, (D, S)))).to("cuda", torch.float32)
+    A[::3], A[:, ::5] = -float("inf"), -float("inf")
+    data = torch.from_numpy(rng.standard_normal((n, D, S))).to("cuda", torch.float32)
+    # a decay of exp(-1e30 delta) is 0 or, for a time step of 0, 1
+    finite = np.where(np.isinf(f64(A)), -1e30, f64(A))
+
+    def run(lens, how):
+        cu, slots = cumulate(lens), np.arange(len(lens))
+        want, tol, pool, pool_tol = ssm_ref.scan(
+            f64(x), f64(d), finite, f64(b), f64(c), None, None, None, cu, f64(data[:len(lens)]),
+            slots, softplus_on=False)
+        single = how == "one"
+        batch = K.ScanBatch(x, d, A, b, c, cu_seqlens=None if single else i32(cu), dt_softplus=False)
+        states = K.ScanPool(data[:len(lens)].clone())
+        if how in ("whole", "cut"):
+            ws = K.scan_workspace(batch) if how == "cut" else None
+            K.kda_scan_prefill(batch, states, i32(slots), workspace=ws)
+        else:
+            K.kda_scan_step(batch, states, i32(slots))
+        within(batch.y, want, tol, "y, " + how)
+        within(states.data, pool, pool_tol, "states, " + how)
+    run([n], "whole")
+    run([n], "cut")
+    run([n], "rows")
+    run([1] * n, "one")
