@@ -533,9 +533,11 @@ int kda_scan_prefill(const kda_scan_tokens *tok, kda_scan_pool *pool,
                      const int32_t *start_pos, void *workspace,
                      size_t workspace_bytes, kda_stream_t stream);
 
-/* Bytes of workspace with which kda_scan_prefill splits long segments; 0 when
- * it would not split at these sizes, and on bad arguments (which the prefill
- * call itself rejects). */
+/* Bytes of workspace with which kda_scan_prefill splits long segments.  They
+ * serve every batch of at most num_tokens tokens and num_seqs segments of these
+ * channels, state and groups: a server asks once, for its largest batch.  0 when
+ * no such batch is split, and on bad arguments (which the prefill call itself
+ * rejects). */
 size_t kda_scan_workspace_size(int32_t num_tokens, int32_t num_seqs,
                                int32_t channels, int32_t state, int32_t groups);
 

@@ -33,6 +33,9 @@
 // 265 us for 8192 x 4096 channels x 16 states in bf16 (268 MB: 40 us at the
 // copy bandwidth; the two bare loops alone 163 us), 428 us for 16384 tokens in
 // 37 prompts of 0 to 2414.
+#include <algorithm>
+#include <cmath>
+
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -573,10 +576,8 @@ int part_tokens(int N, int B, int C, int S, int G) {
   return (int)part;
 }
 
-// Floats of the table of parts at the start of the workspace.
-size_t table_floats(int N, int B, int part) {
-  return (2 * (1 + (size_t)N / part + 2 * (size_t)B) + 63) / 64 * 64;
-}
+// Floats of the table of at most `parts` parts at the start of the workspace.
+size_t table_floats(size_t parts) { return (2 * (1 + parts) + 63) / 64 * 64; }
 
 template <typename T, int S, bool VEC, bool LOCAL>
 cudaError_t launch_pass(const ScanParams &p, int nblk, int parts, cudaStream_t st) {
@@ -609,7 +610,7 @@ cudaError_t launch_prefill_v(ScanParams p, cudaStream_t st) {
     local = parts - p.seg.B;
     e = launch_after(scan_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, parts, local);
   }
-  p.ws += table_floats(p.seg.N, p.seg.B, p.part);
+  p.ws += table_floats(parts);
   if (e == cudaSuccess && local > 0) e = launch_pass<T, S, VEC, true>(p, nblk, local, st);
   if (e == cudaSuccess && p.joined)
     e = launch_after(scan_join_kernel<S>, dim3((unsigned)((long long)nblk * p.seg.B), kStates),
@@ -647,11 +648,22 @@ long long scan_prefill_blocks(int B, int C, int S, int G) {
   return (long long)B * blocks_of_row(C, S, G);
 }
 
+bool scan_splits(int N, int B, int C, int S, int G) { return part_tokens(N, B, C, S, G) > 0; }
+
+// A smaller batch may need more than a larger one (5000 tokens of 25 blocks
+// across: 47 carry slots in 19 prompts, 80 in 18), and a server has one
+// workspace for all of them.  So this bounds the need of every batch up to
+// these sizes: part_tokens' least parts, 32 tokens, an equal share for two
+// waves and sqrt(N), allow at most the three counts below, which grow with N.
 size_t scan_workspace_floats(int N, int B, int C, int S, int G) {
-  const int part = part_tokens(N, B, C, S, G);
-  if (!part) return 0;
-  return table_floats(N, B, part) +
-         ((size_t)N / part + 2 * (size_t)B) * blocks_of_row(C, S, G) * kCarry * kThreads;
+  const long long nblk = blocks_of_row(C, S, G), room = 152LL * blocks_of(2, S, false);
+  if (B * nblk > 0x7fffffffLL) return 0;  // refused by the call
+  // one or two segments that give every SM three blocks stay whole
+  if (N <= 32 || (B <= 2 && nblk >= 3 * 152)) return 0;
+  long long parts = std::min<long long>(N / 32, 2 * room / nblk);
+  parts = std::min(parts, (long long)std::sqrt((double)N));
+  const long long slots = std::min(parts + 2LL * B, 0x7fffffffLL / nblk);
+  return table_floats(slots) + (size_t)(slots * nblk) * kCarry * kThreads;
 }
 
 }  // namespace kda

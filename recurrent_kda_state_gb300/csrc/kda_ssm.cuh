@@ -295,7 +295,10 @@ inline long long move_chunks(long long bytes) { return (bytes + kMoveChunk - 1) 
 
 // Blocks of the scan of B whole segments.
 long long scan_prefill_blocks(int B, int C, int S, int G);
-// Workspace floats of the split scan (0: segments are not split).
+// Whether a batch is split when it has a workspace.
+bool scan_splits(int N, int B, int C, int S, int G);
+// Workspace floats of any split batch of at most N tokens and B segments (0:
+// none is split).
 size_t scan_workspace_floats(int N, int B, int C, int S, int G);
 
 }  // namespace kda

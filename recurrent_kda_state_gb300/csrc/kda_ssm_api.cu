@@ -122,13 +122,12 @@ int scan_impl(const kda_scan_tokens *t, kda_scan_pool *pool, const int32_t *slot
   if ((st = check_param(t->dt_bias, false))) return st;
   if (!step && kda::scan_prefill_blocks(t->num_seqs, t->channels, t->state, t->groups) > 0x7fffffffLL)
     return KDA_ESHAPE;
-  size_t need = 0;
-  if (ws) {
-    if (!aligned(ws, 256)) return KDA_EALIGN;
-    need = kda::scan_workspace_floats(t->num_tokens, t->num_seqs, t->channels, t->state,
-                                      t->groups) * sizeof(float);
-    if (ws_bytes < need) return KDA_ENOSPC;
-  }
+  if (!aligned(ws, 256)) return KDA_EALIGN;
+  const bool split = ws && kda::scan_splits(t->num_tokens, t->num_seqs, t->channels, t->state,
+                                            t->groups);
+  if (split && ws_bytes < kda::scan_workspace_floats(t->num_tokens, t->num_seqs, t->channels,
+                                                     t->state, t->groups) * sizeof(float))
+    return KDA_ENOSPC;
   if (kda::device_refused()) return KDA_EDEVICE;
   kda::ScanParams p = {};
   p.seg.err = kda::error_word();
@@ -160,7 +159,7 @@ int scan_impl(const kda_scan_tokens *t, kda_scan_pool *pool, const int32_t *slot
   p.D = t->D;
   p.dtb = t->dt_bias;
   p.pool = pool->base;
-  p.ws = need ? static_cast<float *>(ws) : nullptr;
+  p.ws = split ? static_cast<float *>(ws) : nullptr;
   p.C_ = t->channels;
   p.S = t->state;
   p.G = t->groups;

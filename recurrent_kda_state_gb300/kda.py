@@ -533,13 +533,14 @@ def kda_conv_step(tok, pool, state_slots, commit_len=None, stream=None):
 
 
 def kda_scan_workspace_size(num_tokens, num_seqs, channels, state, groups=1):
-    """Workspace bytes with which kda_scan_prefill splits long segments; 0
-    when it would not split at these sizes."""
+    """Workspace bytes with which kda_scan_prefill splits long segments, enough
+    for every batch of at most these tokens and segments; 0 when none is split."""
     return int(lib().kda_scan_workspace_size(num_tokens, num_seqs, channels, state, groups))
 
 
 def scan_workspace(tok):
-    """A workspace tensor for kda_scan_prefill of this batch (None: not needed)."""
+    """A workspace tensor for kda_scan_prefill of this batch and of smaller ones
+    (None: not needed)."""
     n = kda_scan_workspace_size(tok.c.num_tokens, tok.c.num_seqs, tok.c.channels, tok.c.state,
                                 tok.c.groups)
     return torch.empty(n, dtype=torch.uint8, device=tok.x.device) if n else None

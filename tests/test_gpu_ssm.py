@@ -593,3 +593,27 @@ def test_states_that_forget_all(S):
     run([n], "cut")
     run([n], "rows")
     run([1] * n, "one")
+
+
+def test_one_workspace_serves_smaller_batches():
+    """A workspace of the size for the largest batch of a server, used for batches
+    of fewer tokens and prompts, which may be cut into more parts; the bytes after
+    it stay as they are."""
+    D, S, G, max_tokens, max_seqs = 50, 64, 25, 5000, 19
+    n = K.kda_scan_workspace_size(max_tokens, max_seqs, D, S, G)
+    buf = torch.full((n + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(81)
+    A = torch.from_numpy(-np.exp(rng.uniform(-3.0, 3.0, (D, S)))).to("cuda", torch.float32)
+    for N, B in ((5000, 19), (5000, 18), (4000, 18), (4900, 1), (33, 2), (3000, 3)):
+        lens = rng.multinomial(N, np.full(B, 1.0 / B))
+        x, d = (rows(rng, N, (D,), "f32", False) for _ in range(2))
+        b, c = (rows(rng, N, (G, S), "f32", False) for _ in range(2))
+        data = torch.from_numpy(rng.standard_normal((B, D, S))).to("cuda", torch.float32)
+        cu, slots = cumulate(lens), rng.permutation(B)
+        want, tol, pool, pool_tol = ssm_ref.scan(f64(x), f64(d), f64(A), f64(b), f64(c), None, None,
+                                                 None, cu, f64(data), slots)
+        batch = K.ScanBatch(x, d, A, b, c, cu_seqlens=i32(cu))
+        K.kda_scan_prefill(batch, K.ScanPool(data), i32(slots), workspace=buf[:n])
+        within(batch.y, want, tol, "y")
+        within(data, pool, pool_tol, "states")
+    assert bool((buf[n:] == 0x5a).all())

@@ -4,6 +4,7 @@ import ctypes
 import pytest
 import torch
 
+import ssm_dispatch
 from recurrent_kda_state_gb300 import kda as K
 from recurrent_kda_state_gb300._build import build_library
 
@@ -183,3 +184,29 @@ def test_binding_refuses_tensors_that_do_not_fit():
         K.kda_conv_step(batch, K.ConvPool(torch.zeros(2, 3, 8)), torch.zeros(3, dtype=torch.int32))
     with pytest.raises(ValueError):
         K.kda_conv_step(batch, K.ConvPool(torch.zeros(2, 3, 8)), torch.zeros(4))
+
+
+@pytest.mark.parametrize("D,S,G", [(4096, 16, 1), (4096, 128, 1), (500, 64, 2), (33, 16, 1),
+                                   (50, 64, 25), (2 ** 16, 16, 1), (2 ** 20, 16, 2 ** 10)])
+def test_scan_workspace_of_a_batch_serves_smaller_ones(D, S, G):
+    """More tokens or more segments never need less, and what a batch is cut into
+    fits: a carry slot of 18 x 128 floats for each part and block of channels."""
+    tokens = [1, 32, 33, 100, 1000, 3000, 4096, 8191, 8192, 16384, 100003, 2 ** 24]
+    seqs = [1, 2, 3, 14, 15, 18, 19, 37, 64, 500]
+    size = {(n, b): K.kda_scan_workspace_size(n, b, D, S, G) for n in tokens for b in seqs}
+    for n, m in zip(tokens, tokens[1:]):
+        assert all(size[n, b] <= size[m, b] for b in seqs)
+    for b, c in zip(seqs, seqs[1:]):
+        assert all(size[n, b] <= size[n, c] for n in tokens)
+    nblk = ssm_dispatch.scan_blocks(D, S, G)
+    for (n, b), bytes_ in size.items():
+        part = ssm_dispatch.scan_part(n, b, D, S, G)
+        slots = n // part + 2 * b if part else 0
+        assert bytes_ >= slots * (nblk * 18 * 128 * 4 + 8)
+
+
+def test_scan_workspace_stays_near_the_need():
+    """One more part than two waves hold at most, beside two of every segment."""
+    slot = 32 * 18 * 128 * 4
+    for n, b in ((8192, 1), (16384, 37), (100000, 200)):
+        assert K.kda_scan_workspace_size(n, b, 4096, 16, 1) <= (2 * 760 // 32 + 2 * b + 1) * slot
