@@ -53,11 +53,12 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const MoveParams p) {
   begin_after_stream();
   for (int i = blockIdx.y; i < p.n; i += gridDim.y) {
     const int src = p.src[i], dst = p.dst[i];
-    if (dst < 0 || src == dst) continue;
+    if (dst < 0) continue;
     if (dst >= p.P || src >= p.P) {
       if (!STAGE && blockIdx.x == 0 && threadIdx.x == 0) set_error(p.err, KDA_DERR_SLOT);
       continue;
     }
+    if (src == dst) continue;
     const bool staged = p.ws && src >= 0 && written_by_other(p, src, i);
     if (STAGE && !staged) continue;
     int a = 0;

@@ -617,3 +617,22 @@ def test_one_workspace_serves_smaller_batches():
         within(batch.y, want, tol, "y")
         within(data, pool, pool_tol, "states")
     assert bool((buf[n:] == 0x5a).all())
+
+
+@pytest.mark.parametrize("shape,ws", [((4, 4), False), ((4, 4), True), ((5,), True)])
+def test_moves_out_of_range_alike_on_every_path(shape, ws):
+    """An id that is not below the number of slots sets the bit, also where
+    source and target are the same, whichever way the moves are done."""
+    src, dst = [1, 0, 9, 3, -1], [2, 12, 4, -1, 10]
+    for s, d, bit in ((8, 8, 1), (11, 11, 1), (5, 5, 0), (9, -1, 0)):
+        t = torch.arange(8 * int(np.prod(shape)), device="cuda", dtype=torch.int32).view(8, *shape)
+        was = t.clone()
+        arrays = K.SlotArrays([t])
+        area = K.move_workspace(arrays, 8) if ws else None
+        K.kda_move_slots(arrays, i32([s]), i32([d]), area)
+        assert K.kda_get_device_error() == (K.KDA_DERR_SLOT if bit else 0)
+        assert torch.equal(t, was)
+        K.kda_move_slots(arrays, i32(src + [s]), i32(dst + [d]), area)
+        assert K.kda_get_device_error() == K.KDA_DERR_SLOT
+        was[2] = was[1]
+        assert torch.equal(t, was)
