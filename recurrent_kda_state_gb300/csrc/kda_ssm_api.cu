@@ -193,6 +193,11 @@ int check_arrays(const kda_slot_array *a, int32_t n, kda::MoveParams *p) {
   return KDA_OK;
 }
 
+// Whether the bytes of n moves' staging areas can be counted.
+bool staging_fits(const kda::MoveParams &p, int32_t n) {
+  return n == 0 || (size_t)p.ws_bytes <= SIZE_MAX / (size_t)n;
+}
+
 }  // namespace
 
 extern "C" {
@@ -235,7 +240,7 @@ int kda_scan_step(const kda_scan_tokens *tok, kda_scan_pool *pool, const int32_t
 size_t kda_move_workspace_size(const kda_slot_array *arrays, int32_t num_arrays, int32_t n) {
   kda::MoveParams p = {};
   if (n < 0 || check_arrays(arrays, num_arrays, &p) != KDA_OK) return 0;
-  return (size_t)p.ws_bytes * (size_t)n;
+  return staging_fits(p, n) ? (size_t)p.ws_bytes * (size_t)n : 0;
 }
 
 int kda_move_slots(const kda_slot_array *arrays, int32_t num_arrays, int32_t num_slots,
@@ -251,7 +256,8 @@ int kda_move_slots(const kda_slot_array *arrays, int32_t num_arrays, int32_t num
   if (!aligned(src, 4) || !aligned(dst, 4)) return KDA_EALIGN;
   if (workspace) {
     if (!aligned(workspace, 256)) return KDA_EALIGN;
-    if (workspace_bytes < (size_t)p.ws_bytes * (size_t)n) return KDA_ENOSPC;
+    if (!staging_fits(p, n) || workspace_bytes < (size_t)p.ws_bytes * (size_t)n)
+      return KDA_ENOSPC;
   }
   if (kda::device_refused()) return KDA_EDEVICE;
   p.err = kda::error_word();

@@ -210,3 +210,13 @@ def test_scan_workspace_stays_near_the_need():
     slot = 32 * 18 * 128 * 4
     for n, b in ((8192, 1), (16384, 37), (100000, 200)):
         assert K.kda_scan_workspace_size(n, b, 4096, 16, 1) <= (2 * 760 // 32 + 2 * b + 1) * slot
+
+
+def test_move_workspace_that_cannot_be_counted(L):
+    """2^30 moves of 2^39 bytes are 2^69: no workspace is large enough."""
+    arr = (K.kda_slot_array * 1)(K.kda_slot_array(0x10000, 2 ** 39))
+    for n in (2 ** 30, 2 ** 31 - 1):
+        assert L.kda_move_workspace_size(arr, 1, n) == 0
+        assert L.kda_move_slots(arr, 1, 4, PTR, PTR, n, ctypes.c_void_p(0x70000), 2 ** 20,
+                                None) == K.KDA_ENOSPC
+    assert L.kda_move_workspace_size(arr, 1, 2 ** 20) == 2 ** 59
