@@ -402,6 +402,15 @@ def _param(t, shape, dt, what):
     return None if t is None else t.data_ptr()
 
 
+def _together(home, tensors):
+    """The device index of tensor `home`; all others (None: skipped) are there too."""
+    dev = home.get_device()  # -1: not on a GPU, which the calls refuse
+    for t, what in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("%s is on %s, the others on %s" % (what, t.device, home.device))
+    return dev
+
+
 def _cu(cu_seqlens, N):
     """Pointer and segments of cu_seqlens; None: one token a row (steps)."""
     if cu_seqlens is None:
@@ -411,13 +420,31 @@ def _cu(cu_seqlens, N):
     return cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
 
 
-def _table(t, n, what):
-    """Pointer of an int32 device table of n entries (None: NULL)."""
+def _table(t, n, what, dev):
+    """Pointer of an int32 table of n entries on device dev (None: NULL)."""
     if t is None:
         return None
     if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
         raise ValueError("%s must be contiguous int32 with %d entries" % (what, n))
+    if t.get_device() != dev or dev < 0:
+        raise ValueError("%s is on %s, the call on GPU %d" % (what, t.device, dev))
     return t.data_ptr()
+
+
+def _call_device(tok, pool):
+    if tok.dev != pool.dev or tok.dev < 0:
+        raise ValueError("the batch is on device %d, the pool on %d; both must be on one GPU"
+                         % (tok.dev, pool.dev))
+    return tok.dev
+
+
+def _workspace(ws, dev):
+    """Pointer and bytes of a workspace (None: NULL)."""
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous() or ws.get_device() != dev or dev < 0:
+        raise ValueError("a workspace is a contiguous tensor on the call's GPU")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 class ConvPool:
@@ -427,6 +454,7 @@ class ConvPool:
         if data.dim() != 3 or not data.is_contiguous():
             raise ValueError("a convolution pool is a contiguous [num_slots][W - 1][D]")
         self.data = data
+        self.dev = data.get_device()
         P, taps, D = data.shape
         self.c = kda_conv_pool(data.data_ptr(), _dtype_code(data.dtype), P, D, taps + 1)
         self.ref = ctypes.byref(self.c)
@@ -449,6 +477,8 @@ class ConvBatch:
         self.x, self.weight, self.bias, self.cu_seqlens = x, weight, bias, cu_seqlens
         self.y = y if y is not None else torch.empty(N, D, dtype=dt, device=x.device)
         _same("y", self.y.shape, (N, D))
+        self.dev = _together(x, ((weight, "weight"), (bias, "bias"), (cu_seqlens, "cu_seqlens"),
+                                 (self.y, "y")))
         W = weight.shape[1]
         cu, B = _cu(cu_seqlens, N)
         self.c = kda_conv_tokens(
@@ -464,7 +494,7 @@ class ScanPool:
     def __init__(self, data):
         if data.dtype != torch.float32 or data.dim() != 3 or not data.is_contiguous():
             raise ValueError("a scan pool is a contiguous fp32 [num_slots][D][S]")
-        self.data = data
+        self.data, self.dev = data, data.get_device()
         self.c = kda_scan_pool(data.data_ptr(), *data.shape)
         self.ref = ctypes.byref(self.c)
 
@@ -490,6 +520,8 @@ class ScanBatch:
                                (C, (N, G, S), "C"), (self.y, (N, Dm), "y")):
             if t is not None:
                 _same(what, t.shape, shape)
+        self.dev = _together(x, ((dt, "dt"), (A, "A"), (B, "B"), (C, "C"), (D, "D"), (z, "z"),
+                                 (dt_bias, "dt_bias"), (cu_seqlens, "cu_seqlens"), (self.y, "y")))
         cu, nseq = _cu(cu_seqlens, N)
         self.c = kda_scan_tokens(
             _dtype_code(ty), x.data_ptr(), dt.data_ptr(),
@@ -502,32 +534,32 @@ class ScanBatch:
         self.ref, self.num_seqs = ctypes.byref(self.c), nseq
 
 
-def _ckpt(ckpt_slots, B):
+def _ckpt(ckpt_slots, B, dev):
     if ckpt_slots is None:
         return None, 0
     if ckpt_slots.dim() != 2:
         raise ValueError("ckpt_slots is [B][max_ckpt]")
     n = int(ckpt_slots.shape[1])
-    return _table(ckpt_slots, B * n, "ckpt_slots"), n
+    return _table(ckpt_slots, B * n, "ckpt_slots", dev), n
 
 
 def kda_conv_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, start_pos=None,
                      stream=None):
     """Causal convolution of packed prompts; ckpt_slots [B][max_ckpt] int32."""
-    B = tok.num_seqs
-    ckpt, max_ckpt = _ckpt(ckpt_slots, B)
+    B, dev = tok.num_seqs, _call_device(tok, pool)
+    ckpt, max_ckpt = _ckpt(ckpt_slots, B, dev)
     _check(lib().kda_conv_prefill(
-        tok.ref, pool.ref, _table(state_slots, B, "state_slots"), ckpt, max_ckpt, ckpt_every,
-        _table(start_pos, B, "start_pos"), _stream(stream)), "kda_conv_prefill")
+        tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev), ckpt, max_ckpt, ckpt_every,
+        _table(start_pos, B, "start_pos", dev), _stream(stream)), "kda_conv_prefill")
 
 
 def kda_conv_step(tok, pool, state_slots, commit_len=None, stream=None):
     """Steps of one or a few tokens a row; commit_len [B] int32: how many of a
     row's tokens the stored state takes in (None: all)."""
-    B = tok.num_seqs
+    B, dev = tok.num_seqs, _call_device(tok, pool)
     st = (_lib or lib()).kda_conv_step(
-        tok.ref, pool.ref, _table(state_slots, B, "state_slots"),
-        None if commit_len is None else _table(commit_len, B, "commit_len"), _stream(stream))
+        tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev),
+        None if commit_len is None else _table(commit_len, B, "commit_len", dev), _stream(stream))
     if st:
         _check(st, "kda_conv_step")
 
@@ -550,20 +582,20 @@ def kda_scan_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, star
                      workspace=None, stream=None):
     """Selective scan of packed prompts; workspace: from scan_workspace(tok),
     or None: no segment is split."""
-    B = tok.num_seqs
-    ckpt, max_ckpt = _ckpt(ckpt_slots, B)
+    B, dev = tok.num_seqs, _call_device(tok, pool)
+    ckpt, max_ckpt = _ckpt(ckpt_slots, B, dev)
+    ws, size = _workspace(workspace, dev)
     _check(lib().kda_scan_prefill(
-        tok.ref, pool.ref, _table(state_slots, B, "state_slots"), ckpt, max_ckpt, ckpt_every,
-        _table(start_pos, B, "start_pos"), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _stream(stream)), "kda_scan_prefill")
+        tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev), ckpt, max_ckpt, ckpt_every,
+        _table(start_pos, B, "start_pos", dev), ws, size, _stream(stream)), "kda_scan_prefill")
 
 
 def kda_scan_step(tok, pool, state_slots, commit_len=None, stream=None):
     """The scan's steps, commit_len as in kda_conv_step."""
-    B = tok.num_seqs
+    B, dev = tok.num_seqs, _call_device(tok, pool)
     st = (_lib or lib()).kda_scan_step(
-        tok.ref, pool.ref, _table(state_slots, B, "state_slots"),
-        None if commit_len is None else _table(commit_len, B, "commit_len"), _stream(stream))
+        tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev),
+        None if commit_len is None else _table(commit_len, B, "commit_len", dev), _stream(stream))
     if st:
         _check(st, "kda_scan_step")
 
@@ -577,6 +609,7 @@ class SlotArrays:
         if not self.tensors or self.tensors[0].shape[0] < 1:
             raise ValueError("no arrays, or no slots")
         self.num_slots = int(self.tensors[0].shape[0])
+        self.dev = _together(self.tensors[0], [(t, "an array") for t in self.tensors])
         for t in self.tensors:
             if not t.is_contiguous() or t.shape[0] != self.num_slots:
                 raise ValueError("every array is a contiguous [num_slots][...]")
@@ -598,11 +631,11 @@ def move_workspace(arrays, n):
 def kda_move_slots(arrays, src, dst, workspace=None, stream=None):
     """In every array: slot dst[i] receives slot src[i] (src < 0: zeros, dst < 0:
     nothing).  workspace None: src and dst must be disjoint."""
-    n = dst.numel()
-    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    n, dev = dst.numel(), arrays.dev
+    ws, size = _workspace(workspace, dev)
     st = (_lib or lib()).kda_move_slots(
-        arrays.c, len(arrays.tensors), arrays.num_slots, _table(src, n, "src"),
-        _table(dst, n, "dst"), n, ws, size, _stream(stream))
+        arrays.c, len(arrays.tensors), arrays.num_slots, _table(src, n, "src", dev),
+        _table(dst, n, "dst", dev), n, ws, size, _stream(stream))
     if st:
         _check(st, "kda_move_slots")
 

@@ -220,3 +220,56 @@ def test_move_workspace_that_cannot_be_counted(L):
         assert L.kda_move_slots(arr, 1, 4, PTR, PTR, n, ctypes.c_void_p(0x70000), 2 ** 20,
                                 None) == K.KDA_ENOSPC
     assert L.kda_move_workspace_size(arr, 1, 2 ** 20) == 2 ** 59
+
+
+def test_binding_refuses_tensors_off_the_gpu():
+    """Host memory in a kernel's arguments would fault, so it goes no further."""
+    i32, x = torch.zeros(4, dtype=torch.int32), torch.zeros(4, 8)
+    conv, scan = K.ConvPool(torch.zeros(4, 3, 8)), K.ScanPool(torch.zeros(4, 8, 16))
+    b = torch.zeros(4, 1, 16)
+    cb, sb = K.ConvBatch(x, torch.zeros(8, 4)), K.ScanBatch(x, x.clone(), torch.zeros(8, 16), b, b)
+    arrays = K.SlotArrays([conv.data, scan.data])
+    for call in (lambda: K.kda_conv_step(cb, conv, i32), lambda: K.kda_scan_step(sb, scan, i32),
+                 lambda: K.kda_conv_prefill(cb, conv, i32), lambda: K.kda_scan_prefill(sb, scan, i32),
+                 lambda: K.kda_move_slots(arrays, i32, i32)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+@pytest.mark.gpu
+def test_binding_refuses_tensors_of_several_devices():
+    """One tensor on the host among those on the GPU, at every argument."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    i32, x, w = torch.zeros(4, dtype=torch.int32), torch.zeros(4, 8), torch.zeros(8, 4)
+    b, A, v = torch.zeros(4, 1, 16), torch.zeros(8, 16), torch.zeros(8)
+    conv, scan = torch.zeros(4, 3, 8), torch.zeros(4, 8, 16)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+
+    def refused(call, *args, **kw):
+        """With each argument on the host in turn, the others on the GPU."""
+        on = {k: t.cuda() for k, t in kw.items()}
+        for k in kw:
+            with pytest.raises(ValueError):
+                call(*args, **dict(on, **{k: kw[k]}))
+    cu = torch.tensor([0, 1, 2, 3, 4], dtype=torch.int32)
+    refused(K.ConvBatch, x=x, weight=w, bias=v, cu_seqlens=cu, y=x)
+    refused(K.ScanBatch, x=x, dt=x, A=A, B=b, C=b, D=v, z=x, dt_bias=v, cu_seqlens=cu, y=x)
+    cb = K.ConvBatch(x.cuda(), w.cuda(), cu_seqlens=cu.cuda())
+    sb = K.ScanBatch(x.cuda(), x.cuda(), A.cuda(), b.cuda(), b.cuda(), cu_seqlens=cu.cuda())
+    cp, sp = K.ConvPool(conv.cuda()), K.ScanPool(scan.cuda())
+    ckpt = i32.view(4, 1)
+    refused(K.kda_conv_step, cb, cp, state_slots=i32, commit_len=i32)
+    refused(K.kda_scan_step, sb, sp, state_slots=i32, commit_len=i32)
+    for call, batch, pool, host in ((K.kda_conv_prefill, cb, cp, conv),
+                                    (K.kda_scan_prefill, sb, sp, scan)):
+        refused(lambda **kw: call(batch, pool, ckpt_every=16, **kw), state_slots=i32,
+                ckpt_slots=ckpt, start_pos=i32)
+        with pytest.raises(ValueError):
+            call(batch, type(pool)(host), i32.cuda())
+    with pytest.raises(ValueError):
+        K.kda_scan_prefill(sb, sp, i32.cuda(), workspace=ws)
+    with pytest.raises(ValueError):
+        K.SlotArrays([conv.cuda(), scan])
+    arrays = K.SlotArrays([conv.cuda(), scan.cuda()])
+    refused(lambda **kw: K.kda_move_slots(arrays, **kw), src=i32, dst=i32, workspace=ws)
