@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import ssm_dispatch
 import ssm_ref
 from recurrent_kda_state_gb300 import kda as K
 from recurrent_kda_state_gb300._build import build_library
@@ -636,3 +637,111 @@ def test_moves_out_of_range_alike_on_every_path(shape, ws):
         assert K.kda_get_device_error() == K.KDA_DERR_SLOT
         was[2] = was[1]
         assert torch.equal(t, was)
+
+
+# ------------------------------------------- blocks of many rows, long chains
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("S,D,B", [(16, 2048, 310), (64, 500, 700), (128, 256, 333),
+                                   (128, 4800, 300)])
+def test_scan_step_many_rows_of_one_token(dt, S, D, B):
+    """Decode batches in which a block takes many rows, one token each: the ring
+    of states goes round and each row's token is asked for one row ahead."""
+    assert ssm_dispatch.step_rows(dt, S, B, D, table=False) >= 6
+    g = torch.Generator(device="cuda").manual_seed(60)
+
+    def normal(*shape, to=DT[dt]):
+        return torch.randn(*shape, generator=g, device="cuda").to(to)
+    x, d, z = (normal(B, D) for _ in range(3))
+    b, c = normal(B, 1, S), normal(B, 1, S)
+    A = -torch.exp(torch.rand(D, S, generator=g, device="cuda") * 6.0 - 3.0)
+    skip, bias = normal(D, to=torch.float32), normal(D, to=torch.float32) - 3.0
+    data = normal(B + 5, D, S, to=torch.float32)
+    slots = torch.randperm(B + 5, generator=g, device="cuda")[:B]
+    keep = torch.rand(B, generator=g, device="cuda") < 0.7
+
+    # fp64 on the device, with ssm_ref's bounds of a first token
+    f = lambda t: t.double()  # noqa: E731
+    delta = torch.nn.functional.softplus(f(d) + f(bias), threshold=700.0)
+    decay = torch.exp(delta[..., None] * f(A))
+    add = (delta * f(x))[..., None] * f(b)
+    h0 = f(data)[slots]
+    h = decay * h0 + add
+    mag = decay * h0.abs() + add.abs()
+    del decay, add, h0
+    units = (8 + 64) * ssm_ref.U32
+    o = (f(c) * h).sum(-1) + f(skip) * f(x)
+    err = units * ((f(c).abs() * mag).sum(-1) + (f(skip) * f(x)).abs())
+    gate = f(z) * torch.sigmoid(f(z))
+    err = err * gate.abs() + (f(z).abs() + 8) * ssm_ref.U32 * (o * gate).abs()
+    o = o * gate
+    end, end_tol = f(data), torch.zeros_like(data, dtype=torch.float64)
+    end[slots[keep]], end_tol[slots[keep]] = h[keep], units * mag[keep]
+
+    batch = K.ScanBatch(x, d, A, b, c, D=skip, z=z, dt_bias=bias)
+    K.kda_scan_step(batch, K.ScanPool(data), slots.int(), keep.int())
+    assert bool(((f(batch.y) - o).abs() <= err + ssm_ref.U_OUT[dt] * o.abs()).all())
+    assert bool(((f(data) - end).abs() <= end_tol).all())
+
+
+def drafted(seed, B):
+    """Lengths of a large step, empty rows and long ones among them, and how
+    many tokens of each row the state takes in."""
+    rng = np.random.default_rng(seed)
+    lens = rng.choice([0, 1, 1, 1, 2, 8, 8, 40], B)
+    lens[:2], lens[-1] = 0, 0
+    return lens, rng.integers(0, lens + 1)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("S,D,G,B,view", [(16, 2048, 1, 310, False), (16, 700, 700, 300, False),
+                                          (32, 1000, 1, 300, True), (128, 264, 1, 340, False)])
+def test_scan_step_many_rows_of_several_tokens(dt, S, D, G, B, view):
+    """Blocks of many rows of 0 to 40 tokens: items follow one another across
+    rows, empty rows are passed over, the stages in shared memory go round."""
+    assert ssm_dispatch.step_rows(dt, S, B, D, G) >= 6
+    lens, commit = drafted(61, B)
+    scan_case(62, dt, lens, D, S, G=G, step=True, commit=commit, view=view)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_conv_step_many_rows(dt):
+    lens, commit = drafted(63, 700)
+    conv_case(64, dt, lens, 260, 4, step=True, commit=commit)
+    conv_case(65, dt, [1] * 700, 260, 3, step=True, commit=commit > 0)
+
+
+@pytest.mark.parametrize("dt,lens,D", [("bf16", [4099, 61, 4000], 2800), ("f32", [2099, 61, 2000], 3840)])
+def test_conv_prefill_largest_tiles(dt, lens, D):
+    assert ssm_dispatch.conv_tile(dt, sum(lens), D) == 48
+    conv_case(66, dt, lens, D, 4)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,D,S,G", [([0, 5000], 33, 64, 1), ([4100], 40, 16, 1),
+                                        ([2200, 2100], 24, 32, 3), ([2500, 2500], 20, 128, 1)])
+def test_scan_prefill_joined(dt, lens, D, S, G):
+    """Batches whose parts are joined by a launch of their own."""
+    assert ssm_dispatch.scan_joined(sum(lens), len(lens), D, S, G)
+    assert not ssm_dispatch.scan_listed(sum(lens), len(lens), D, S, G)
+    scan_case(67, dt, lens, D, S, G=G, every=512, max_ckpt=2, start=[9] * len(lens))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,D,S,G", [([1900, 3100], 200, 64, 25), ([5001, 2], 25, 64, 25),
+                                        ([2900, 0, 5100], 250, 32, 25)])
+def test_scan_prefill_listed_and_joined(dt, lens, D, S, G):
+    """A few long prompts: the parts are listed first and joined between."""
+    n, B = sum(lens), len(lens)
+    assert ssm_dispatch.scan_listed(n, B, D, S, G) and ssm_dispatch.scan_joined(n, B, D, S, G)
+    scan_case(68, dt, lens, D, S, G=G)
+    scan_case(69, dt, lens, D, S, G=G, every=512, max_ckpt=2, start=[7, 100, 31][:B])
+
+
+@pytest.mark.parametrize("S,D", [(16, 100), (32, 100), (64, 25)])
+def test_scan_prefill_listed_f32(S, D):
+    rng = np.random.default_rng(70)
+    lens = np.concatenate([rng.integers(0, 60, 40), [1500, 0, 1300, 1, 16, 300]])
+    rng.shuffle(lens)
+    assert ssm_dispatch.scan_listed(int(lens.sum()), len(lens), D, S, 25)
+    scan_case(71, "f32", lens, D, S, G=25, every=64, max_ckpt=2,
+              start=rng.integers(0, 100, len(lens)))
