@@ -505,6 +505,10 @@ int kda_conv_prefill(const kda_conv_tokens *tok, kda_conv_pool *pool,
  * last time and the new drafts in one segment, and the accepted count as
  * commit_len: a rejection needs no stored state.  commit_len outside
  * [0, T_i] sets KDA_DERR_ACCEPT and skips the row.
+ * Before kda_verify, whose rows are the drafts alone: one call on the drafts
+ * with counts of 0, and when the accepted counts are known the same call again
+ * with those.  q, k, v of a KDA layer, contiguous tensors each, come from three
+ * calls on the three parts of a projection's rows (x_stride), with a pool each.
  */
 int kda_conv_step(const kda_conv_tokens *tok, kda_conv_pool *pool,
                   const int32_t *state_slots, const int32_t *commit_len,

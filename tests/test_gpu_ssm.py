@@ -745,3 +745,75 @@ def test_scan_prefill_listed_f32(S, D):
     assert ssm_dispatch.scan_listed(int(lens.sum()), len(lens), D, S, 25)
     scan_case(71, "f32", lens, D, S, G=25, every=64, max_ckpt=2,
               start=rng.integers(0, 100, len(lens)))
+
+
+# ------------------------------------------------- before a layer of KDA heads
+def test_convolution_before_a_kda_layer():
+    """q, k, v of KDA heads from one projection, three convolutions of its parts:
+    the outputs are the layer's packed tensors as they are.  A speculative step
+    runs the drafts with a commit count of 0 before the verify, and again with
+    the accepted counts when they are known."""
+    import oracle
+    rng = np.random.default_rng(80)
+    H, d, W, T, P = 3, 32, 4, 4, 5
+    D, lens, slots = H * d, [70, 33], i32([4, 1])
+    bf16 = torch.bfloat16
+    taps = [torch.from_numpy(rng.standard_normal((D, W)) * 0.5).to("cuda", bf16) for _ in range(3)]
+    convs = [K.ConvPool.zeros(P, W, D, bf16) for _ in range(3)]
+    pool, ring = K.StatePool.zeros(P, H, d), K.ReplayRing(P, H, d, T, bf16)
+    sess = oracle.OracleSession(P, H, d, d)
+
+    def project(n):  # the projection's rows, decay and beta
+        rest = [rng.uniform(0.6, 1.0, (n, H, d)), rng.uniform(0.0, 1.0, (n, H))]
+        return (rows(rng, n, (3 * D,), "bf16", False),
+                *(torch.from_numpy(a).to("cuda", bf16) for a in rest))
+
+    def layer(batches, alpha, beta, cu):
+        q, k, v = (b.y.unflatten(1, (H, d)) for b in batches)
+        k = torch.nn.functional.normalize(k.float(), dim=-1).to(bf16)
+        tok = K.TokenBatch(q, k, v, alpha, beta, i32(cu))
+        return tok, dict(q=f64(q), k=f64(k), v=f64(v), alpha=f64(alpha), beta=f64(beta),
+                         cu_seqlens=cu)
+
+    def batches(x, cu):
+        return [K.ConvBatch(x[:, i * D:(i + 1) * D], taps[i], cu_seqlens=i32(cu)) for i in range(3)]
+
+    def check(bs, x, cu, before, commit):
+        for i, b in enumerate(bs):
+            y, tol, after = ssm_ref.conv(f64(x)[:, i * D:(i + 1) * D], f64(taps[i]), None, cu,
+                                         before[i], [4, 1], True, "bf16", commit)
+            within(b.y, y, tol, "conv")
+            np.testing.assert_array_equal(f64(convs[i].data), after)
+
+    before = [f64(c.data) for c in convs]
+    x, alpha, beta = project(sum(lens))
+    cu = cumulate(lens)
+    bs = batches(x, cu)
+    for b, c in zip(bs, convs):
+        K.kda_conv_prefill(b, c, slots)
+    check(bs, x, cu, before, None)
+    tok, host = layer(bs, alpha, beta, cu)
+    K.kda_prefill_chunked(tok, pool, slots, 16)
+    want, _ = sess.prefill(host, [4, 1])
+    assert np.abs(f64(tok.o) - want).max() <= 2e-3
+    cu = cumulate([T, T])
+    for _ in range(4):
+        before = [f64(c.data) for c in convs]
+        x, alpha, beta = project(2 * T)
+        bs = batches(x, cu)
+        for b, c in zip(bs, convs):
+            K.kda_conv_step(b, c, slots, i32([0, 0]))
+        check(bs, x, cu, before, [0, 0])
+        tok, host = layer(bs, alpha, beta, cu)
+        K.kda_verify(tok, T, pool, slots, ring)
+        assert np.abs(f64(tok.o) - sess.verify(host, [4, 1])).max() <= 2e-3
+        accepted = rng.integers(0, T + 1, 2).astype(np.int32)
+        K.kda_commit(i32(accepted), slots, pool, ring)
+        sess.commit(accepted, [4, 1])
+        for b, c in zip(bs, convs):
+            K.kda_conv_step(b, c, slots, i32(accepted))
+        check(bs, x, cu, before, accepted)
+    K.kda_materialize(slots, pool, ring)
+    for s in (4, 1):
+        got = np.swapaxes(f64(pool.data[s]), -1, -2)
+        assert np.linalg.norm(got - sess.pool[s]) <= 1e-3 * np.linalg.norm(sess.pool[s])
