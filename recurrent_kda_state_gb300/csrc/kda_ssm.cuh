@@ -230,15 +230,6 @@ __device__ __forceinline__ f2 silu2(f2 v) {
   return mul2(v, pack2(rcpf(d.x), rcpf(d.y)));
 }
 
-// A 16-byte vector of elements as pairs.
-template <typename T>
-__device__ __forceinline__ void load_pairs(const void *p, f2 *dst) {
-  float e[InVec<T>::kElems];
-  InVec<T>::load(static_cast<const T *>(p), e);
-#pragma unroll
-  for (int i = 0; i < InVec<T>::kElems / 2; ++i) dst[i] = pack2(e[2 * i], e[2 * i + 1]);
-}
-
 template <typename T>
 __device__ __forceinline__ T out_scalar(float v);
 template <>
@@ -253,29 +244,6 @@ template <typename T>
 __device__ __forceinline__ T *row_at(T *base, int t, int stride) {
   using B = typename std::conditional<std::is_const<T>::value, const char, char>::type;
   return reinterpret_cast<T *>(reinterpret_cast<B *>(base) + (long long)t * stride);
-}
-
-// V consecutive elements (V = 1: plain scalars; else one 16-byte vector).
-template <typename T, int V>
-__device__ __forceinline__ void load_elems(const T *p, float *dst) {
-  if constexpr (V == 1) dst[0] = in_scalar<T>(p);
-  else InVec<T>::load(p, dst);
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_elems(T *p, const float *v) {
-  if constexpr (V == 1) {
-    *p = out_scalar<T>(v[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
 }
 
 template <typename T>
