@@ -72,7 +72,7 @@ enum {
   KDA_EPROTO = -5,  /* ring / commit protocol misuse detectable on host    */
   KDA_ECUDA = -6,   /* a CUDA runtime call failed (launch, copy, sync)     */
   KDA_EDEVICE = -7, /* kda_get_device_error found bits set                 */
-  KDA_ENOSPC = -8   /* workspace smaller than kda_prefill_workspace_size() */
+  KDA_ENOSPC = -8   /* workspace smaller than the call's ..workspace_size() */
 };
 
 /* Bits of the device error word. */
@@ -566,7 +566,10 @@ typedef struct {
  *     src[i] < 0:   slot dst[i] is zeroed             (freed, or made fresh)
  *     dst[i] < 0:   nothing
  * arrays is a HOST array of num_arrays <= 64 entries that all have num_slots
- * slots.  The dst >= 0 must be distinct.  With a workspace of
+ * slots; a model with more of them makes a call for each 64, which is the same,
+ * since no array's moves depend on another's.  A convolution pool of bf16 with
+ * odd (W - 1) * D has slots that are no multiple of 4 bytes, and is refused.  The
+ * dst >= 0 must be distinct.  With a workspace of
  * kda_move_workspace_size(...) bytes, 256-byte aligned, the moves act as if
  * all at once: a slot may be the src of one and the dst of another.  With a
  * NULL workspace src and dst must be disjoint.  An id that is not below

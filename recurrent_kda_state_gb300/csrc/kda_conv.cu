@@ -13,6 +13,8 @@
 // W - 1 rows before it.  Tile 0 alone reads the slot and alone writes it (it
 // fetches the segment's last rows itself), so no other block can see a state
 // that is already replaced.
+// Odd channels, or rows that are not on a multiple of four elements, take one
+// element a thread: 8192 x 12287 101 us, in fp32 147 (12288: 124).
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -53,8 +55,9 @@ struct Elems {
   Raw r;
   __device__ __forceinline__ void load(const T *p) { r = *reinterpret_cast<const Raw *>(p); }
   __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<Raw *>(p) = r; }
-  // Rows pass through once: marked to leave L2 first (5003 x 1000 fp32: 12.3 us
-  // without the marks, 10.3 with them; no difference where the data passes L2).
+  // Rows pass through once: marked to leave L2 first (5003 x 1000 fp32 among
+  // other data of 400 MB: 10.4 us without the marks, 9.9 with them; called again
+  // and again on 80 MB, which L2 holds, 6.9 and 8.4; 8192 x 12288: no difference).
   __device__ __forceinline__ void load_once(const T *p) {
     if constexpr (V == 1) load(p);
     else r = __ldcs(reinterpret_cast<const Raw *>(p));

@@ -12,10 +12,10 @@
 //     from there.  For many moves of little data, where a thread that does
 //     them all would leave most of the machine idle.
 // 64 moves, half of them into places that others leave, and 16 frees: 280 KB
-// slots in 8 layers 66 us the first way (330 MB, 5.0 TB/s) and 80 the second,
-// in 2 layers 27 and 25 us, 70 KB slots in one layer 19 and 10; 8 moves and 2
-// frees of 280 KB in one layer 6 and 8.  So the first way serves up to 16
-// moves, and more of them where it has two blocks a move.
+// slots in 8 layers 63 us the first way (330 MB, 5.2 TB/s) and 76 the second,
+// in 2 layers 22.4 and 20.7 us, 70 KB slots in one layer 15.6 and 7.6; 8 moves
+// and 2 frees of 280 KB in one layer 5.7 and 7.5.  So the first way serves up to
+// 16 moves, and more of them where it has two blocks a move.
 #include "kda_ssm.cuh"
 
 namespace kda {

@@ -3,8 +3,8 @@
 //     h[n] = exp(delta A[n]) h[n] + delta x B[n],   y = C . h + D x  (gated)
 //
 // Memory bound: the states are read and written once, which is nearly all
-// the bytes there are (256 rows of 4096 channels with 64 states: 86 us, 94 % of
-// the copy bandwidth).  A thread owns eight states of one channel (S / 8 lanes
+// the bytes there are (256 rows of 4096 channels with 64 states: 87 us, 93 % of
+// the copy bandwidth; 94 us in fp32).  A thread owns eight states of one channel (S / 8 lanes
 // a channel) and keeps their A in registers while it walks over the rows of
 // its group, so A is read once per block and not once per row.  The states of
 // the next rows are under way by asynchronous copies into a ring in shared
@@ -14,7 +14,9 @@
 // ahead.  Rows that may have several take them from shared memory, up to kTake
 // at a time and two such items ahead: a draft of eight costs its work, not
 // eight latencies (64 rows, eight of them of eight tokens, 4096 channels: 11 us,
-// 13 to 17 with the tokens loaded to registers in chunks).  The sum over
+// 13 to 17 with the tokens loaded to registers in chunks; 64 us with 128 states,
+// 64 % of the copy bandwidth, where 16 lanes of a channel prepare the same time
+// step).  The sum over
 // states is a butterfly over the channel's lanes.
 #include "kda_ssm.cuh"
 
@@ -363,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) scan_rows_kernel(const ScanP
 // Groups that the rows of a batch are dealt to, for gx blocks a group and
 // `room` blocks on the machine: as many as fill one to four waves, whichever
 // ends first if a block takes the time of its rows and of two more (its
-// start).  Groups that overflow a wave by a few blocks cost another one: 256
+// start).  Rows count alike, since their lengths are on the device: with drafts
+// the group that has most of them lasts longest.  Groups that overflow a wave by a few blocks cost another one: 256
 // rows of 4096 channels with 64 states took 115 us in 640 blocks where 608 fit,
 // and 89 us by this rule.
 int row_groups(int gx, int B, int room) {

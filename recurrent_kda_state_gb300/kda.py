@@ -602,7 +602,8 @@ def kda_scan_step(tok, pool, state_slots, commit_len=None, stream=None):
 
 class SlotArrays:
     """The per-slot tensors [num_slots][...] of a model (pools, rings, of all
-    layers) that kda_move_slots moves together."""
+    layers) that kda_move_slots moves together: up to 64, whose slots are each a
+    multiple of 4 bytes.  A model of more takes one SlotArrays for each 64."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
