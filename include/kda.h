@@ -90,6 +90,7 @@ enum {
                             taking work: what it had not finished (outputs,
                             states, rings of those units) is left as it was
                             or unspecified, never half-written silently   */
+  KDA_DERR_POSITION = 256, /* a token's position outside the rotation table  */
   KDA_DERR_UNSAFE = 128  /* after a timeout, the second bounded wait for
                             work still in flight (tensor cores or copies)
                             also gave up before the kernel released its
@@ -583,6 +584,141 @@ int kda_move_slots(const kda_slot_array *arrays, int32_t num_arrays,
 /* Bytes of workspace for kda_move_slots with n moves; 0 on bad arguments. */
 size_t kda_move_workspace_size(const kda_slot_array *arrays, int32_t num_arrays,
                                int32_t n);
+
+/* ------------------------------------------------------------------------
+ * Linear attention layers with a decay for each head, and what stands on both
+ * sides of such a layer and of a KDA layer: the norm of queries and keys with
+ * the position rotation before it, the gated norm of the outputs after it.
+ * (No counterpart on the pages; the conventions of the state space layers
+ * hold: rows with a stride, outputs in the inputs' dtype that overlap no
+ * input unless stated, distinct slots, dependent launches.)
+ */
+
+/* One packed batch of linear attention. */
+typedef struct {
+  kda_dtype dtype;           /* dtype of q, k, v, o                          */
+  const void *q, *k;         /* [N] rows of [Hk][d_k], contiguous in a row   */
+  const void *v;             /* [N] rows of [H][d_v]                         */
+  void *o;                   /* [N] rows of [H][d_v]                         */
+  int64_t q_stride, k_stride, v_stride, o_stride; /* elements between rows   */
+  const float *g;            /* log decays: [N] rows of H                    */
+  int64_t g_stride;          /* elements between rows of g; 0: one row of H
+                                serves every token                           */
+  float scale;               /* of the outputs                               */
+  const int32_t *cu_seqlens; /* [B + 1] device; steps: NULL = one token a row */
+  int32_t num_seqs;          /* B                                            */
+  int32_t num_tokens;        /* N                                            */
+  int32_t num_heads;         /* H, a multiple of Hk                          */
+  int32_t num_qk_heads;      /* Hk: head h reads q, k of head h / (H / Hk)   */
+  int32_t d_k, d_v;          /* each in {16, 32, 64, 128}                    */
+} kda_linear_tokens;
+
+/*
+ * kda_linear_prefill -- linear attention of packed prompts, from the state S
+ * [d_k][d_v] of each (slot, head), stored as in every state pool; for each
+ * token of a segment, in order:
+ *     S = exp(g) * S + k v^T
+ *     o = scale * S^T q                               (post-update state)
+ * States, sums and decays are fp32.  g <= 0 as a rule; g = -inf forgets the
+ * state.  The slot receives the last state; a segment of no tokens leaves its
+ * slot as it is.  Checkpoints as in kda_prefill_chunked, with ckpt_every a
+ * multiple of 64.
+ * In bf16 with d_k and d_v of at least 64 the prompt runs in chunks of 64
+ * tokens on the tensor cores; there a NaN or an infinity in k or v reaches
+ * the outputs of its whole chunk, those of earlier tokens included.
+ * workspace: kda_linear_workspace_size(...) bytes, 256-byte aligned, owned by
+ * the caller and not used by another call until this one completes; with it
+ * long segments are split into parts that run at the same time.  NULL: every
+ * segment is walked by itself.  Both meet the same tolerances; they are not
+ * bit-identical to each other.
+ */
+int kda_linear_prefill(const kda_linear_tokens *tok, kda_state_pool *pool,
+                       const int32_t *state_slots, const int32_t *ckpt_slots,
+                       int32_t max_ckpt, int32_t ckpt_every,
+                       const int32_t *start_pos, void *workspace,
+                       size_t workspace_bytes, kda_stream_t stream);
+
+/* Bytes of workspace with which kda_linear_prefill splits long segments.  They
+ * serve every batch of at most num_tokens tokens and num_seqs segments of these
+ * heads, dims and dtype: a server asks once, for its largest batch.  0 when no
+ * such batch is split, and on bad arguments (which the prefill call itself
+ * rejects). */
+size_t kda_linear_workspace_size(int32_t num_tokens, int32_t num_seqs,
+                                 int32_t num_heads, int32_t d_k, int32_t d_v,
+                                 kda_dtype dtype);
+
+/* kda_linear_step -- the same recurrence for steps of one or a few tokens per
+ * row, commit_len as in kda_conv_step. */
+int kda_linear_step(const kda_linear_tokens *tok, kda_state_pool *pool,
+                    const int32_t *state_slots, const int32_t *commit_len,
+                    kda_stream_t stream);
+
+/* How a head's channels are normalised. */
+typedef enum {
+  KDA_NORM_NONE = 0,
+  KDA_NORM_RMS = 1, /* x / sqrt(mean(x^2) + eps) */
+  KDA_NORM_L2 = 2   /* x / sqrt(sum(x^2) + eps)  */
+} kda_norm;
+
+/* Queries and keys of N tokens. */
+typedef struct {
+  kda_dtype dtype;           /* dtype of q, k, q_out, k_out and the weights  */
+  const void *q, *k;         /* [N] rows of [Hq][d] and [Hk][d]              */
+  void *q_out, *k_out;       /* the same shapes                              */
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride; /* elements        */
+  const void *q_weight, *k_weight; /* [d] or NULL: 1                         */
+  const float *cos_sin;      /* [max_pos] rows of rot_dim / 2 cosines, then
+                                rot_dim / 2 sines; NULL when rot_dim is 0    */
+  const int32_t *positions;  /* [N] device; NULL when rot_dim is 0           */
+  int32_t num_tokens;        /* N                                            */
+  int32_t num_q_heads;       /* Hq, 0: no queries                            */
+  int32_t num_k_heads;       /* Hk, 0: no keys                               */
+  int32_t head_dim;          /* d, even, at most 256                         */
+  int32_t rot_dim;           /* channels that are rotated, even, at most d   */
+  int32_t max_pos;           /* rows of cos_sin                              */
+  int32_t interleaved;       /* 0: channel i turns with i + rot_dim / 2,
+                                else: 2 i with 2 i + 1                       */
+  kda_norm norm;
+  float eps;
+  float q_scale;             /* the queries are multiplied by it at the end  */
+} kda_qk_tokens;
+
+/*
+ * kda_qk_norm -- norm, weight, position rotation and scale of the queries and
+ * keys of each head in one pass.  For each head's x, i < rot_dim / 2 and the
+ * pair (a, b) of channels that turn together:
+ *     y = norm(x) * weight
+ *     y_a, y_b = y_a cos - y_b sin,  y_b cos + y_a sin   (of cos_sin[position])
+ * with sums and products in fp32, rounded once.  Before a KDA layer: keys with
+ * KDA_NORM_L2 and rot_dim 0.  Outputs may be the inputs themselves (the same
+ * pointer and stride); otherwise they overlap no input.  A position outside
+ * [0, max_pos) sets KDA_DERR_POSITION and skips the token.
+ */
+int kda_qk_norm(const kda_qk_tokens *tok, kda_stream_t stream);
+
+/* Outputs of a layer and their gate, N tokens. */
+typedef struct {
+  kda_dtype x_dtype;         /* dtype of x (a KDA layer's o: KDA_F32)        */
+  kda_dtype dtype;           /* dtype of gate, weight, y                     */
+  const void *x;             /* [N] rows of [H][d]                           */
+  const void *gate;          /* [N] rows of [H][d], or NULL: no gate         */
+  const void *weight;        /* [d] or NULL: 1                               */
+  void *y;                   /* [N] rows of [H][d]                           */
+  int64_t x_stride, gate_stride, y_stride; /* elements between rows          */
+  int32_t num_tokens, num_heads;
+  int32_t head_dim;          /* d, at most 256                               */
+  int32_t silu;              /* 0: act = sigmoid, else act(u) = u sigmoid(u) */
+  float eps;
+} kda_gate_tokens;
+
+/*
+ * kda_gated_norm -- y = x / sqrt(mean(x^2) + eps) * weight * act(gate), the
+ * mean over the channels of a head: the way from a KDA or linear attention
+ * layer to the output projection.  Sums and products in fp32, rounded once.
+ * y may be the gate itself, or x where it has y's dtype (the same pointer and
+ * stride); otherwise it overlaps no input.
+ */
+int kda_gated_norm(const kda_gate_tokens *tok, kda_stream_t stream);
 
 /* kda_get_device_error -- synchronize `stream`, read the device error word
  * of the current device into *host_bits (host pointer), clear it, and return

@@ -1,0 +1,203 @@
+// Public calls of linear attention and of the head norms: argument validation
+// on the host, then launches on the caller's stream.  Nothing is allocated here.
+#include "kda_checks.cuh"
+#include "kda_linear.cuh"
+
+namespace {
+
+using namespace kda;
+
+bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+
+// Heads of a row: as many channels as other rows may have.
+bool heads_ok(int heads, int d) { return heads >= 1 && heads <= kMaxChannels / d; }
+
+int linear_impl(const kda_linear_tokens *t, kda_state_pool *pool, const int32_t *slots,
+                const int32_t *ckpt, int32_t max_ckpt, int32_t every, const int32_t *start,
+                const int32_t *commit, void *ws, size_t ws_bytes, bool step, kda_stream_t stream) {
+  if (!pool || !pool->base || !t) return KDA_EINVAL;
+  if (!aligned(pool->base, 16)) return KDA_EALIGN;
+  if (!dtype_ok(t->dtype)) return KDA_EDTYPE;
+  if (t->num_seqs < 0 || t->num_tokens < 0) return KDA_EINVAL;
+  if (t->num_seqs > kMaxSeqs || t->num_tokens > kMaxTokens) return KDA_ESHAPE;
+  if (!dim_ok(t->d_k) || !dim_ok(t->d_v) || pool->num_slots < 1) return KDA_ESHAPE;
+  if (!heads_ok(t->num_heads, t->d_k > t->d_v ? t->d_k : t->d_v)) return KDA_ESHAPE;
+  if (t->num_qk_heads < 1 || t->num_heads % t->num_qk_heads != 0) return KDA_ESHAPE;
+  if (pool->num_heads != t->num_heads || pool->d_k != t->d_k || pool->d_v != t->d_v)
+    return KDA_ESHAPE;
+  int st = check_tables(t->cu_seqlens, step, t->num_seqs, t->num_tokens, slots, ckpt, max_ckpt,
+                        every, 64);
+  if (st) return st;
+  if (!aligned(start, 4) || !aligned(commit, 4)) return KDA_EALIGN;
+  if (t->num_seqs == 0 || t->num_tokens == 0) return KDA_OK;
+  const int qk = t->num_qk_heads * t->d_k, vo = t->num_heads * t->d_v;
+  if ((st = check_view(t->q, t->q_stride, qk, t->dtype))) return st;
+  if ((st = check_view(t->k, t->k_stride, qk, t->dtype))) return st;
+  if ((st = check_view(t->v, t->v_stride, vo, t->dtype))) return st;
+  if ((st = check_view(t->o, t->o_stride, vo, t->dtype))) return st;
+  if ((st = check_view(t->g, t->g_stride ? t->g_stride : t->num_heads, t->num_heads, KDA_F32)))
+    return st;
+  if (t->o == t->q || t->o == t->k || t->o == t->v || t->o == (const void *)t->g) return KDA_EINVAL;
+  if ((long long)t->num_seqs * t->num_heads > 0x7fffffffLL) return KDA_ESHAPE;
+  if (!aligned(ws, 256)) return KDA_EALIGN;
+  (void)ws_bytes;
+  if (device_refused()) return KDA_EDEVICE;
+  LinearParams p = {};
+  p.seg.err = error_word();
+  if (!p.seg.err) return KDA_ECUDA;
+  p.seg.cu = t->cu_seqlens;
+  p.seg.slots = slots;
+  p.seg.commit = commit;
+  p.seg.ckpt_slots = every > 0 && max_ckpt > 0 ? ckpt : nullptr;
+  p.seg.start_pos = start;
+  p.seg.B = t->num_seqs;
+  p.seg.N = t->num_tokens;
+  p.seg.P = pool->num_slots;
+  p.seg.max_ckpt = max_ckpt;
+  p.seg.ckpt_every = every;
+  const int64_t es = (int64_t)elem(t->dtype);
+  p.q = t->q;
+  p.k = t->k;
+  p.v = t->v;
+  p.o = t->o;
+  p.qs = (int)(t->q_stride * es);
+  p.ks = (int)(t->k_stride * es);
+  p.vs = (int)(t->v_stride * es);
+  p.os = (int)(t->o_stride * es);
+  p.g = t->g;
+  p.gs = (int)(t->g_stride * 4);
+  p.H = t->num_heads;
+  p.rep = t->num_heads / t->num_qk_heads;
+  p.DK = t->d_k;
+  p.DV = t->d_v;
+  p.scale = t->scale;
+  p.pool = pool->base;
+  p.vec = aligned(t->q, 16) && aligned(t->k, 16) && aligned(t->v, 16) && p.qs % 16 == 0 &&
+          p.ks % 16 == 0 && p.vs % 16 == 0;
+  return cuda_status(launch_linear_walk(p, t->dtype, step, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Outputs of a view: the input itself, or rows that start elsewhere.
+int check_out(const void *x, int64_t x_stride, const void *y, int64_t y_stride) {
+  return x == y && x_stride != y_stride ? KDA_EINVAL : KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_linear_prefill(const kda_linear_tokens *tok, kda_state_pool *pool,
+                       const int32_t *state_slots, const int32_t *ckpt_slots, int32_t max_ckpt,
+                       int32_t ckpt_every, const int32_t *start_pos, void *workspace,
+                       size_t workspace_bytes, kda_stream_t stream) {
+  return linear_impl(tok, pool, state_slots, ckpt_slots, max_ckpt, ckpt_every, start_pos, nullptr,
+                     workspace, workspace_bytes, false, stream);
+}
+
+size_t kda_linear_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_heads,
+                                 int32_t d_k, int32_t d_v, kda_dtype dtype) {
+  (void)num_tokens, (void)num_seqs, (void)num_heads, (void)d_k, (void)d_v, (void)dtype;
+  return 0;
+}
+
+int kda_linear_step(const kda_linear_tokens *tok, kda_state_pool *pool, const int32_t *state_slots,
+                    const int32_t *commit_len, kda_stream_t stream) {
+  return linear_impl(tok, pool, state_slots, nullptr, 0, 0, nullptr, commit_len, nullptr, 0, true,
+                     stream);
+}
+
+int kda_qk_norm(const kda_qk_tokens *t, kda_stream_t stream) {
+  if (!t) return KDA_EINVAL;
+  if (!dtype_ok(t->dtype)) return KDA_EDTYPE;
+  if (t->num_tokens < 0 || t->norm < KDA_NORM_NONE || t->norm > KDA_NORM_L2) return KDA_EINVAL;
+  if (t->head_dim < 2 || t->head_dim > 256 || t->head_dim % 2 != 0) return KDA_ESHAPE;
+  if (t->rot_dim < 0 || t->rot_dim > t->head_dim || t->rot_dim % 2 != 0) return KDA_ESHAPE;
+  const int heads[2] = {t->num_q_heads, t->num_k_heads};
+  if (heads[0] < 0 || heads[1] < 0) return KDA_EINVAL;
+  if (t->num_tokens > kMaxTokens) return KDA_ESHAPE;
+  if (heads[0] > kMaxChannels / t->head_dim || heads[1] > kMaxChannels / t->head_dim)
+    return KDA_ESHAPE;
+  if (t->rot_dim > 0 && t->max_pos < 1) return KDA_ESHAPE;
+  if (t->num_tokens == 0 || heads[0] + heads[1] == 0) return KDA_OK;
+  int st;
+  QkParams p = {};
+  const void *x[2] = {t->q, t->k};
+  void *y[2] = {t->q_out, t->k_out};
+  const void *w[2] = {t->q_weight, t->k_weight};
+  const int64_t xs[2] = {t->q_stride, t->k_stride}, ys[2] = {t->q_out_stride, t->k_out_stride};
+  const int64_t es = (int64_t)elem(t->dtype);
+  for (int i = 0; i < 2; ++i) {
+    if (!heads[i]) continue;
+    const int row = heads[i] * t->head_dim;
+    if ((st = check_view(x[i], xs[i], row, t->dtype))) return st;
+    if ((st = check_view(y[i], ys[i], row, t->dtype))) return st;
+    if ((st = check_out(x[i], xs[i], y[i], ys[i]))) return st;
+    if ((st = check_param(w[i], false))) return st;
+    p.x[i] = x[i];
+    p.y[i] = y[i];
+    p.w[i] = w[i];
+    p.xs[i] = (int)(xs[i] * es);
+    p.ys[i] = (int)(ys[i] * es);
+    p.heads[i] = heads[i];
+  }
+  if (heads[0] && heads[1] && (y[0] == y[1] || y[0] == x[1] || y[1] == x[0])) return KDA_EINVAL;
+  if (t->rot_dim > 0) {
+    if ((st = check_param(t->cos_sin, true))) return st;
+    if (!t->positions) return KDA_EINVAL;
+    if (!aligned(t->positions, 4)) return KDA_EALIGN;
+  }
+  if (device_refused()) return KDA_EDEVICE;
+  p.err = error_word();
+  if (!p.err) return KDA_ECUDA;
+  p.table = t->cos_sin;
+  p.pos = t->positions;
+  p.N = t->num_tokens;
+  p.d = t->head_dim;
+  p.rot = t->rot_dim;
+  p.max_pos = t->max_pos;
+  p.interleaved = t->interleaved != 0;
+  p.norm = t->norm;
+  p.eps = t->eps;
+  p.q_scale = t->q_scale;
+  return cuda_status(launch_qk_norm(p, t->dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_gated_norm(const kda_gate_tokens *t, kda_stream_t stream) {
+  if (!t) return KDA_EINVAL;
+  if (!dtype_ok(t->dtype) || !dtype_ok(t->x_dtype)) return KDA_EDTYPE;
+  if (t->num_tokens < 0) return KDA_EINVAL;
+  if (t->head_dim < 1 || t->head_dim > 256 || !heads_ok(t->num_heads, t->head_dim))
+    return KDA_ESHAPE;
+  // a block takes one head's row at least
+  if (t->num_tokens > kMaxTokens || (long long)t->num_tokens * t->num_heads > 0x7fffffffLL)
+    return KDA_ESHAPE;
+  if (t->num_tokens == 0) return KDA_OK;
+  const int row = t->num_heads * t->head_dim;
+  int st;
+  if ((st = check_view(t->x, t->x_stride, row, t->x_dtype))) return st;
+  if (t->gate && (st = check_view(t->gate, t->gate_stride, row, t->dtype))) return st;
+  if ((st = check_view(t->y, t->y_stride, row, t->dtype))) return st;
+  if ((st = check_param(t->weight, false))) return st;
+  if (t->x == t->y && t->x_dtype != t->dtype) return KDA_EINVAL;
+  if ((st = check_out(t->x, t->x_stride, t->y, t->y_stride))) return st;
+  if (t->gate && (st = check_out(t->gate, t->gate_stride, t->y, t->y_stride))) return st;
+  if (device_refused()) return KDA_EDEVICE;
+  GateParams p = {};
+  const int64_t es = (int64_t)elem(t->dtype);
+  p.x = t->x;
+  p.gate = t->gate;
+  p.w = t->weight;
+  p.y = t->y;
+  p.xs = (int)(t->x_stride * (int64_t)elem(t->x_dtype));
+  p.gs = t->gate ? (int)(t->gate_stride * es) : 0;
+  p.ys = (int)(t->y_stride * es);
+  p.N = t->num_tokens;
+  p.H = t->num_heads;
+  p.d = t->head_dim;
+  p.silu = t->silu != 0;
+  p.eps = t->eps;
+  return cuda_status(launch_gated_norm(p, t->x_dtype, t->dtype,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -17,8 +17,9 @@ KDA_OK, KDA_EINVAL, KDA_EDTYPE, KDA_ESHAPE, KDA_EALIGN = 0, -1, -2, -3, -4
 KDA_EPROTO, KDA_ECUDA, KDA_EDEVICE, KDA_ENOSPC = -5, -6, -7, -8
 KDA_DERR_SLOT, KDA_DERR_ACCEPT, KDA_DERR_DEPTH = 1, 2, 4
 KDA_DERR_SEGMENT, KDA_DERR_RING, KDA_DERR_RANGE = 8, 16, 32
-KDA_DERR_TIMEOUT, KDA_DERR_UNSAFE = 64, 128
+KDA_DERR_TIMEOUT, KDA_DERR_UNSAFE, KDA_DERR_POSITION = 64, 128, 256
 KDA_F32, KDA_BF16 = 0, 1
+KDA_NORM_NONE, KDA_NORM_RMS, KDA_NORM_L2 = 0, 1, 2
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -72,14 +73,41 @@ class kda_slot_array(ctypes.Structure):
     _fields_ = [("base", _P), ("slot_bytes", ctypes.c_size_t)]
 
 
+class kda_linear_tokens(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("q", _P), ("k", _P), ("v", _P), ("o", _P),
+                ("q_stride", _I64), ("k_stride", _I64), ("v_stride", _I64),
+                ("o_stride", _I64), ("g", _P), ("g_stride", _I64), ("scale", ctypes.c_float),
+                ("cu_seqlens", _P), ("num_seqs", _I32), ("num_tokens", _I32),
+                ("num_heads", _I32), ("num_qk_heads", _I32), ("d_k", _I32), ("d_v", _I32)]
+
+
+class kda_qk_tokens(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("q", _P), ("k", _P), ("q_out", _P), ("k_out", _P),
+                ("q_stride", _I64), ("k_stride", _I64), ("q_out_stride", _I64),
+                ("k_out_stride", _I64), ("q_weight", _P), ("k_weight", _P), ("cos_sin", _P),
+                ("positions", _P), ("num_tokens", _I32), ("num_q_heads", _I32),
+                ("num_k_heads", _I32), ("head_dim", _I32), ("rot_dim", _I32),
+                ("max_pos", _I32), ("interleaved", _I32), ("norm", ctypes.c_int),
+                ("eps", ctypes.c_float), ("q_scale", ctypes.c_float)]
+
+
+class kda_gate_tokens(ctypes.Structure):
+    _fields_ = [("x_dtype", ctypes.c_int), ("dtype", ctypes.c_int), ("x", _P), ("gate", _P),
+                ("weight", _P), ("y", _P), ("x_stride", _I64), ("gate_stride", _I64),
+                ("y_stride", _I64), ("num_tokens", _I32), ("num_heads", _I32),
+                ("head_dim", _I32), ("silu", _I32), ("eps", ctypes.c_float)]
+
+
 EXPORTS = ("kda_prefill_chunked", "kda_prefill_chunked_raw", "kda_prefill_chunked_noalloc",
            "kda_prefill_workspace_size", "kda_verify", "kda_verify_raw",
            "kda_commit", "kda_commit_layers", "kda_materialize", "kda_ring_reset",
            "kda_gather_states", "kda_copy_slots", "kda_verify_snapshot",
            "kda_commit_snapshot", "kda_forward_mixed", "kda_conv_prefill", "kda_conv_step",
            "kda_scan_prefill", "kda_scan_step", "kda_scan_workspace_size",
-           "kda_move_slots", "kda_move_workspace_size", "kda_get_device_error",
-           "kda_set_wait_limit", "kda_status_string", "kda_version")
+           "kda_move_slots", "kda_move_workspace_size", "kda_linear_prefill",
+           "kda_linear_step", "kda_linear_workspace_size", "kda_qk_norm", "kda_gated_norm",
+           "kda_get_device_error", "kda_set_wait_limit",
+           "kda_status_string", "kda_version")
 
 _lib = None
 
@@ -126,6 +154,13 @@ def lib():
         L.kda_move_slots.argtypes = [ap, _I32, _I32, _P, _P, _I32, _P, size, _P]
         L.kda_move_workspace_size.argtypes = [ap, _I32, _I32]
         L.kda_move_workspace_size.restype = size
+        lt = ctypes.POINTER(kda_linear_tokens)
+        L.kda_linear_prefill.argtypes = [lt, pp, _P, _P, _I32, _I32, _P, _P, size, _P]
+        L.kda_linear_step.argtypes = [lt, pp, _P, _P, _P]
+        L.kda_linear_workspace_size.argtypes = [_I32] * 5 + [ctypes.c_int]
+        L.kda_linear_workspace_size.restype = size
+        L.kda_qk_norm.argtypes = [ctypes.POINTER(kda_qk_tokens), _P]
+        L.kda_gated_norm.argtypes = [ctypes.POINTER(kda_gate_tokens), _P]
         L.kda_get_device_error.argtypes = [ctypes.POINTER(_I32), _P]
         L.kda_set_wait_limit.argtypes = [_I32]
         L.kda_status_string.argtypes = [ctypes.c_int]
@@ -184,14 +219,15 @@ class StatePool:
     def __init__(self, data):
         assert data.dtype == torch.float32 and data.dim() == 4
         assert data.is_contiguous()
-        self.data = data
+        self.data, self.dev = data, data.get_device()
         P, H, dv, dk = data.shape
         self.c = kda_state_pool(data.data_ptr(), P, H, dk, dv)
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
-    def zeros(cls, num_slots, H, d, device="cuda"):
-        return cls(torch.zeros(num_slots, H, d, d, dtype=torch.float32,
-                               device=device))
+    def zeros(cls, num_slots, H, d, device="cuda", d_v=None):
+        return cls(torch.zeros(num_slots, H, d if d_v is None else d_v, d,
+                               dtype=torch.float32, device=device))
 
 
 class ReplayRing:
@@ -598,6 +634,176 @@ def kda_scan_step(tok, pool, state_slots, commit_len=None, stream=None):
         None if commit_len is None else _table(commit_len, B, "commit_len", dev), _stream(stream))
     if st:
         _check(st, "kda_scan_step")
+
+
+class LinearBatch:
+    """Packed rows q, k [N][Hk][d_k] and v [N][H][d_v] (row strides are fine), fp32
+    log decays g [N][H] or [H] (every token's), outputs o [N][H][d_v], times scale;
+    cu_seqlens [B + 1] int32, or None for steps of one token a row.  The states
+    are a StatePool's."""
+
+    def __init__(self, q, k, v, g, cu_seqlens=None, scale=1.0, o=None):
+        N, Hk, dk = q.shape
+        _, H, dv = v.shape
+        ty = q.dtype
+        self.q, self.k, self.v, self.g, self.cu_seqlens = q, k, v, g, cu_seqlens
+        self.o = o if o is not None else torch.empty(N, H, dv, dtype=ty, device=q.device)
+        _same("k", k.shape, q.shape)
+        _same("v", v.shape, (N, H, dv))
+        _same("o", self.o.shape, (N, H, dv))
+        _same("g", g.shape, (H,) if g.dim() == 1 else (N, H))
+        if g.dim() == 1:
+            if g.dtype != torch.float32 or not g.is_contiguous():
+                raise ValueError("g must be fp32, and contiguous where it is [H]")
+            g_stride = 0
+        else:
+            g_stride = _row_view(g, torch.float32, "g")
+            if g_stride < H:
+                raise ValueError("g of one row for all tokens is passed as [H]")
+        self.dev = _together(q, ((k, "k"), (v, "v"), (g, "g"), (cu_seqlens, "cu_seqlens"),
+                                 (self.o, "o")))
+        cu, nseq = _cu(cu_seqlens, N)
+        self.c = kda_linear_tokens(
+            _dtype_code(ty), q.data_ptr(), k.data_ptr(), v.data_ptr(), self.o.data_ptr(),
+            _row_view(q, ty, "q"), _row_view(k, ty, "k"), _row_view(v, ty, "v"),
+            _row_view(self.o, ty, "o"), g.data_ptr(), g_stride, scale, cu, nseq, N, H, Hk, dk, dv)
+        self.ref, self.num_seqs = ctypes.byref(self.c), nseq
+
+
+def kda_linear_workspace_size(num_tokens, num_seqs, H, d_k, d_v, dtype):
+    """Workspace bytes with which kda_linear_prefill splits long segments, enough
+    for every batch of at most these tokens and segments (dtype KDA_F32 or
+    KDA_BF16); 0 when none is split."""
+    return int(lib().kda_linear_workspace_size(num_tokens, num_seqs, H, d_k, d_v, dtype))
+
+
+def linear_workspace(tok):
+    """A workspace tensor for kda_linear_prefill of this batch and of smaller ones
+    (None: not needed)."""
+    c = tok.c
+    n = kda_linear_workspace_size(c.num_tokens, c.num_seqs, c.num_heads, c.d_k, c.d_v, c.dtype)
+    return torch.empty(n, dtype=torch.uint8, device=tok.q.device) if n else None
+
+
+def kda_linear_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, start_pos=None,
+                       workspace=None, stream=None):
+    """Linear attention of packed prompts; workspace: from linear_workspace(tok),
+    or None: no segment is split."""
+    B, dev = tok.num_seqs, _call_device(tok, pool)
+    ckpt, max_ckpt = _ckpt(ckpt_slots, B, dev)
+    ws, size = _workspace(workspace, dev)
+    _check(lib().kda_linear_prefill(
+        tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev), ckpt, max_ckpt, ckpt_every,
+        _table(start_pos, B, "start_pos", dev), ws, size, _stream(stream)), "kda_linear_prefill")
+
+
+def kda_linear_step(tok, pool, state_slots, commit_len=None, stream=None):
+    """Steps of one or a few tokens a row, commit_len as in kda_conv_step."""
+    B, dev = tok.num_seqs, _call_device(tok, pool)
+    st = (_lib or lib()).kda_linear_step(
+        tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev),
+        None if commit_len is None else _table(commit_len, B, "commit_len", dev), _stream(stream))
+    if st:
+        _check(st, "kda_linear_step")
+
+
+_NORMS = {None: KDA_NORM_NONE, "rms": KDA_NORM_RMS, "l2": KDA_NORM_L2}
+
+
+class QKBatch:
+    """Queries q [N][Hq][d] and keys k [N][Hk][d] (row strides are fine; either may
+    be None), weights [d] or None, norm "rms", "l2" or None; cos_sin fp32
+    [max_pos][rot_dim] (cosines, then sines) with positions [N] int32, or None: no
+    rotation; interleaved: neighbours turn, else halves; the queries times q_scale.
+    Outputs q_out, k_out may be the inputs."""
+
+    def __init__(self, q, k, q_weight=None, k_weight=None, norm="rms", eps=1e-6, cos_sin=None,
+                 positions=None, interleaved=False, q_scale=1.0, q_out=None, k_out=None):
+        if norm not in _NORMS:
+            raise ValueError("norm must be 'rms', 'l2' or None")
+        if (cos_sin is None) != (positions is None):
+            raise ValueError("cos_sin and positions go together")
+        one = q if q is not None else k
+        N, _, d = one.shape
+        ty = one.dtype
+        if q is not None and k is not None:
+            _same("k", k.shape, (N, k.shape[1], d))
+
+        def rows(x, out, weight, what):
+            if x is None:
+                return None, (None, 0, None, 0, None, 0)
+            if out is None:
+                out = torch.empty(x.shape, dtype=ty, device=x.device)
+            _same(what + "_out", out.shape, x.shape)
+            return out, (x.data_ptr(), _row_view(x, ty, what), out.data_ptr(),
+                         _row_view(out, ty, what + "_out"),
+                         _param(weight, (d,), ty, what + "_weight"), x.shape[1])
+
+        self.q, self.k, self.q_weight, self.k_weight = q, k, q_weight, k_weight
+        self.cos_sin, self.positions = cos_sin, positions
+        self.q_out, a = rows(q, q_out, q_weight, "q")
+        self.k_out, b = rows(k, k_out, k_weight, "k")
+        rot = max_pos = 0
+        if cos_sin is not None:
+            max_pos, rot = cos_sin.shape
+            _param(cos_sin, (max_pos, rot), torch.float32, "cos_sin")
+        self.dev = _together(one, ((q, "q"), (k, "k"), (self.q_out, "q_out"),
+                                   (self.k_out, "k_out"), (q_weight, "q_weight"),
+                                   (k_weight, "k_weight"), (cos_sin, "cos_sin")))
+        self.c = kda_qk_tokens(
+            _dtype_code(ty), a[0], b[0], a[2], b[2], a[1], b[1], a[3], b[3], a[4], b[4],
+            None if cos_sin is None else cos_sin.data_ptr(),
+            _table(positions, N, "positions", self.dev), N, a[5], b[5], d, rot, max_pos,
+            1 if interleaved else 0, _NORMS[norm], eps, q_scale)
+        self.ref = ctypes.byref(self.c)
+
+
+def _on_gpu(tok):
+    if tok.dev < 0:
+        raise ValueError("the batch is not on a GPU")
+
+
+def kda_qk_norm(tok, stream=None):
+    """Norm, rotation and scale of queries and keys: into tok.q_out, tok.k_out."""
+    _on_gpu(tok)
+    st = (_lib or lib()).kda_qk_norm(tok.ref, _stream(stream))
+    if st:
+        _check(st, "kda_qk_norm")
+
+
+class GateBatch:
+    """A layer's outputs x [N][H][d], their gate [N][H][d] or None, weight [d] or
+    None, activation "sigmoid" or "silu", outputs y [N][H][d] in the gate's dtype
+    (without a gate: the weight's, else x's); row strides are fine, and y may be
+    the gate, or x of the same dtype."""
+
+    def __init__(self, x, gate, weight=None, activation="sigmoid", eps=1e-6, y=None):
+        if activation not in ("sigmoid", "silu"):
+            raise ValueError("activation must be 'sigmoid' or 'silu'")
+        N, H, d = x.shape
+        like = next(t for t in (gate, weight, x) if t is not None)
+        ty = like.dtype
+        self.x, self.gate, self.weight = x, gate, weight
+        self.y = y if y is not None else torch.empty(N, H, d, dtype=ty, device=x.device)
+        _same("y", self.y.shape, (N, H, d))
+        if gate is not None:
+            _same("gate", gate.shape, (N, H, d))
+        self.dev = _together(x, ((gate, "gate"), (weight, "weight"), (self.y, "y")))
+        self.c = kda_gate_tokens(
+            _dtype_code(x.dtype), _dtype_code(ty), x.data_ptr(),
+            None if gate is None else gate.data_ptr(), _param(weight, (d,), ty, "weight"),
+            self.y.data_ptr(), _row_view(x, x.dtype, "x"),
+            0 if gate is None else _row_view(gate, ty, "gate"), _row_view(self.y, ty, "y"),
+            N, H, d, 1 if activation == "silu" else 0, eps)
+        self.ref = ctypes.byref(self.c)
+
+
+def kda_gated_norm(tok, stream=None):
+    """Norm of each head's outputs times the gate's activation: into tok.y."""
+    _on_gpu(tok)
+    st = (_lib or lib()).kda_gated_norm(tok.ref, _stream(stream))
+    if st:
+        _check(st, "kda_gated_norm")
 
 
 class SlotArrays:
