@@ -19,15 +19,6 @@ namespace {
 
 constexpr int kTile = 16;  // tokens in shared memory
 
-// e^g = hi + lo.  Near 0 from e^g - 1, whose error is relative to itself.
-__device__ __forceinline__ float2 decay_pair(float g) {
-  if (fabsf(g) < 0.5f) {
-    const float b = expm1f(g), hi = 1.0f + b;
-    return make_float2(hi, b - (hi - 1.0f));
-  }
-  return make_float2(expf(g), 0.0f);
-}
-
 template <int DK>
 struct Walk {
   static constexpr int kKL = DK >= 32 ? 8 : 4;     // lanes along the keys
@@ -113,6 +104,10 @@ __global__ void __launch_bounds__(256) linear_walk_kernel(const LinearParams p) 
       }
   };
   const long long p0 = p.seg.start_pos ? p.seg.start_pos[i] : 0;
+  if (p0 < 0) {
+    set_error(p.seg.err, KDA_DERR_SEGMENT);
+    return;
+  }
   // tokens after which the next checkpoint is due
   long long due = p.seg.ckpt_slots ? p.seg.ckpt_every - p0 % p.seg.ckpt_every : 0x7fffffffffffLL;
   const int hq = h / p.rep;

@@ -19,7 +19,68 @@ struct LinearParams {
   float scale;
   float *pool;
   int vec;  // q, k, v rows start on 16 bytes
+  int o_vec;  // rows of o do
+  // Prompts that are split: chunks of 64 tokens of a part (0: segments are
+  // whole), parts that the grid and the workspace hold, each part's decay and
+  // its state, first what it adds and then the one before it.
+  int part_chunks, max_parts;
+  float2 *part_decay;  // [max_parts][H]
+  float *part_state;   // [max_parts][H][d_v * d_k]
+  int spin_limit;      // polls of a bounded wait before it gives up
 };
+
+// e^g = hi + lo.  Near 0 from e^g - 1, whose error is relative to itself: a
+// state lives through thousands of tokens when g is small, and the 2^-25 by
+// which one fp32 e^g is off is the same every time.
+__device__ __forceinline__ float2 decay_pair(float g) {
+  if (fabsf(g) < 0.5f) {
+    const float b = expm1f(g), hi = 1.0f + b;
+    return make_float2(hi, b - (hi - 1.0f));
+  }
+  return make_float2(expf(g), 0.0f);
+}
+__device__ __forceinline__ float decayed(float s, float2 a, float add) {
+  return fmaf(s, a.x, fmaf(s, a.y, add));
+}
+
+// Parts of segment i, 0 for one without tokens or with a bad table entry.
+__device__ __forceinline__ int segment_parts(const LinearParams &p, int i) {
+  const int b = p.seg.cu[i], e = p.seg.cu[i + 1], p0 = p.seg.start_pos ? p.seg.start_pos[i] : 0;
+  if (b < 0 || e <= b || e > p.seg.N || p0 < 0) return 0;
+  const int chunks = (int)(((p0 & 63) + (long long)(e - b) + 63) >> 6);
+  return (chunks + p.part_chunks - 1) / p.part_chunks;
+}
+struct PartLoc {
+  int seg, part, parts;  // seg < 0: no such part
+};
+// The segment and place of part `target` of all segments' parts in their
+// order; for a whole warp.
+__device__ __forceinline__ PartLoc find_part(const LinearParams &p, int target) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int base = 0; base < p.seg.B; base += 32) {
+    const int n = base + lane < p.seg.B ? segment_parts(p, base + lane) : 0;
+    int upto = n;
+#pragma unroll
+    for (int w = 1; w < 32; w *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, w);
+      if (lane >= w) upto += o;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > target);
+    if (past) {
+      const int l = __ffs(past) - 1, parts = __shfl_sync(0xffffffffu, n, l);
+      return {base + l, target - (before + __shfl_sync(0xffffffffu, upto, l) - parts), parts};
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return {-1, 0, 0};
+}
+// Parts of the segments before segment i; for a whole warp.
+__device__ __forceinline__ int parts_before(const LinearParams &p, int i) {
+  int n = 0;
+  for (int s = threadIdx.x & 31; s < i; s += 32) n += segment_parts(p, s);
+  return __reduce_add_sync(0xffffffffu, n);
+}
 
 struct QkParams {
   const void *x[2];  // queries, keys
@@ -44,6 +105,23 @@ struct GateParams {
 };
 
 cudaError_t launch_linear_walk(const LinearParams &p, kda_dtype dt, bool step, cudaStream_t s);
+// Prompts in bf16 with d_k and d_v of 64 or 128, on the tensor cores.
+cudaError_t launch_linear_tc(const LinearParams &p, cudaStream_t s);
+inline bool linear_uses_tc(int dtype, int d_k, int d_v) {
+  return dtype == KDA_BF16 && d_k >= 64 && d_v >= 64;
+}
+// Chunks of a part of a batch (0: it is not split) and the most parts it can
+// have; the most of any batch of at most N tokens and B segments (0: none is split).
+int linear_part_chunks(int N, int B, int H);
+int linear_max_parts(int N, int B, int H);
+size_t linear_workspace_parts(int N, int B, int H);
+// Bytes of the parts' decays at the start of the workspace.
+inline size_t linear_decay_bytes(size_t parts, int H) {
+  return (parts * H * sizeof(float2) + 255) & ~(size_t)255;
+}
+inline size_t linear_workspace_bytes(size_t parts, int H, int d_k, int d_v) {
+  return parts ? linear_decay_bytes(parts, H) + parts * H * d_k * d_v * sizeof(float) : 0;
+}
 cudaError_t launch_qk_norm(const QkParams &p, kda_dtype dt, cudaStream_t s);
 cudaError_t launch_gated_norm(const GateParams &p, kda_dtype x_dt, kda_dtype dt, cudaStream_t s);
 

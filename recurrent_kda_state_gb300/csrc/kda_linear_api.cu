@@ -40,7 +40,11 @@ int linear_impl(const kda_linear_tokens *t, kda_state_pool *pool, const int32_t 
   if (t->o == t->q || t->o == t->k || t->o == t->v || t->o == (const void *)t->g) return KDA_EINVAL;
   if ((long long)t->num_seqs * t->num_heads > 0x7fffffffLL) return KDA_ESHAPE;
   if (!aligned(ws, 256)) return KDA_EALIGN;
-  (void)ws_bytes;
+  const bool tc = !step && linear_uses_tc(t->dtype, t->d_k, t->d_v);
+  const int part = tc && ws ? linear_part_chunks(t->num_tokens, t->num_seqs, t->num_heads) : 0;
+  const int parts = part ? linear_max_parts(t->num_tokens, t->num_seqs, t->num_heads) : 0;
+  if (ws_bytes < linear_workspace_bytes(parts, t->num_heads, t->d_k, t->d_v)) return KDA_ENOSPC;
+  if ((long long)parts * t->num_heads > 0x7fffffffLL) return KDA_ESHAPE;
   if (device_refused()) return KDA_EDEVICE;
   LinearParams p = {};
   p.seg.err = error_word();
@@ -74,7 +78,16 @@ int linear_impl(const kda_linear_tokens *t, kda_state_pool *pool, const int32_t 
   p.pool = pool->base;
   p.vec = aligned(t->q, 16) && aligned(t->k, 16) && aligned(t->v, 16) && p.qs % 16 == 0 &&
           p.ks % 16 == 0 && p.vs % 16 == 0;
-  return cuda_status(launch_linear_walk(p, t->dtype, step, reinterpret_cast<cudaStream_t>(stream)));
+  p.o_vec = aligned(t->o, 16) && p.os % 16 == 0;
+  p.part_chunks = part;
+  p.max_parts = parts;
+  p.part_decay = part ? static_cast<float2 *>(ws) : nullptr;
+  p.part_state = part ? reinterpret_cast<float *>(static_cast<unsigned char *>(ws) +
+                                                  linear_decay_bytes(parts, p.H))
+                      : nullptr;
+  p.spin_limit = wait_limit_polls();
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(tc ? launch_linear_tc(p, s) : launch_linear_walk(p, t->dtype, step, s));
 }
 
 // Outputs of a view: the input itself, or rows that start elsewhere.
@@ -96,8 +109,12 @@ int kda_linear_prefill(const kda_linear_tokens *tok, kda_state_pool *pool,
 
 size_t kda_linear_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_heads,
                                  int32_t d_k, int32_t d_v, kda_dtype dtype) {
-  (void)num_tokens, (void)num_seqs, (void)num_heads, (void)d_k, (void)d_v, (void)dtype;
-  return 0;
+  if (num_tokens < 0 || num_tokens > kMaxTokens || num_seqs < 1 || num_seqs > kMaxSeqs ||
+      !dim_ok(d_k) || !dim_ok(d_v) || !heads_ok(num_heads, d_k > d_v ? d_k : d_v) ||
+      !dtype_ok(dtype) || !linear_uses_tc(dtype, d_k, d_v))
+    return 0;
+  return linear_workspace_bytes(linear_workspace_parts(num_tokens, num_seqs, num_heads), num_heads,
+                                d_k, d_v);
 }
 
 int kda_linear_step(const kda_linear_tokens *tok, kda_state_pool *pool, const int32_t *state_slots,
