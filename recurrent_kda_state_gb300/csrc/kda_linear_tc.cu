@@ -8,7 +8,7 @@
 // what each part adds to the state (sum_kernel), the states before the parts
 // (join_kernel), the outputs (out_kernel, which alone runs for whole segments).
 //
-// Precision.  Decays are summed in fp64 and kept as hi + lo, so that a token
+// Precision.  Decays are summed in fixed point and kept as hi + lo, so that a token
 // that forgets everything costs the later ones nothing.  K~ is split into three
 // bf16, which hold 24 bits, and V is exact: states are as good as fp32 products
 // and sums make them.  The masked Q K^T is split into two (2^-17).  The state
@@ -25,75 +25,120 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr double kLog2eD = 1.4426950408889634;
 constexpr uint32_t kAccO = 0, kAccU = 128;  // TMEM columns; Q K^T comes before U, in its place
 
 __device__ __forceinline__ uint64_t dadd(uint64_t d, uint32_t off) { return d + (off >> 4); }
 
-// Every thread waits for the tensor cores (bounded); they agree on the outcome.
-__device__ __forceinline__ bool tc_wait(uint64_t *mbar, uint32_t &phase, int limit) {
-  const bool all = __syncthreads_and(umma::mbar_wait(mbar, phase, limit)) != 0;
-  if (all) phase ^= 1u;
+// A warp waits for the tensor cores (bounded); its threads agree on the outcome,
+// and the block's at its next barrier.
+__device__ __forceinline__ bool warp_wait(uint64_t *mbar, uint32_t parity, int limit) {
+  const bool ok = __all_sync(0xffffffffu, umma::mbar_wait(mbar, parity, limit)) != 0;
+  umma::fence_after_sync();
+  return ok;
+}
+// Publish this thread's tiles to the tensor cores and meet the issuing thread;
+// whether every thread is `ok`.
+__device__ __forceinline__ bool tiles_ready(bool ok) {
+  umma::fence_smem_to_async();
+  umma::fence_before_sync();
+  const bool all = __syncthreads_and(ok) != 0;
   umma::fence_after_sync();
   return all;
 }
-// Publish this thread's tiles to the tensor cores and meet the issuing thread.
-__device__ __forceinline__ void tiles_ready() {
-  umma::fence_smem_to_async();
-  umma::fence_before_sync();
-  __syncthreads();
-  umma::fence_after_sync();
-}
 
-__device__ __forceinline__ void copy_wait_but_one() {
-  asm volatile("cp.async.wait_group 1;" ::: "memory");
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// ROWS = 64 rows of D channels into K/64 swizzled blocks of `block` bytes; rows
-// from n on are zeros.
-template <int D>
-__device__ __forceinline__ void load_rows(unsigned char *sm, uint32_t block, const void *base, int tok,
-                                          int stride, int channel, int n, bool vec) {
-  constexpr int kChunks = D / 8;
-#pragma unroll
-  for (int e = 0; e < 64 * kChunks / kThreads; ++e) {
-    const int idx = e * kThreads + threadIdx.x, row = idx / kChunks, c = idx % kChunks;
-    unsigned char *dst = sm + (c >> 3) * block + (row >> 3) * 1024 + (row & 7) * 128 +
-                         (((c & 7) ^ (row & 7)) << 4);
-    const __nv_bfloat16 *src =
-        row_at(static_cast<const __nv_bfloat16 *>(base), tok + (row < n ? row : 0), stride) + channel + c * 8;
+// The tokens of chunk q of a segment (chunks end at absolute multiples of 64).
+struct Chunk {
+  int begin, n;
+  __device__ __forceinline__ Chunk(const SegLoc &s, int skew, int q) {
+    const long long b = (long long)q * 64 - skew, e = b + 64;
+    const int lo = b > 0 ? (int)b : 0, hi = e < s.len ? (int)e : s.len;
+    begin = s.begin + lo;
+    n = hi - lo;
+  }
+};
+
+// 64 rows of D channels, in swizzled blocks of 64 channels, by THREADS threads: a
+// thread has 16 bytes of every kStep-th row, always the same, so that it can
+// change what it loaded itself without meeting the others.
+template <int D, int THREADS>
+struct Rows {
+  static constexpr int kChunks = D / 8, kStep = THREADS / kChunks, kLoads = 64 / kStep;
+  static_assert(kStep % 8 == 0, "rows of one place in the swizzle");
+  int row, chunk;
+  __device__ __forceinline__ explicit Rows(int t) : row(t / kChunks), chunk(t % kChunks) {}
+  // Byte offset of the thread's e-th 16 bytes, and its row.
+  __device__ __forceinline__ uint32_t place(int e, uint32_t block) const {
+    return (chunk >> 3) * block + (row >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4) +
+           e * (kStep / 8) * 1024;
+  }
+  __device__ __forceinline__ int row_of(int e) const { return row + e * kStep; }
+  // The rows of tokens [begin, begin + n) from `channel` on, zeros behind them.
+  __device__ __forceinline__ void load(unsigned char *sm, uint32_t block, const void *base, int stride,
+                                       int channel, const Chunk &c, bool vec) const {
+    const char *first = static_cast<const char *>(base) + (channel + chunk * 8) * 2 + (long long)c.begin * stride;
+    const char *from = first + (long long)row * stride;
+    unsigned char *to = sm + place(0, block);
     if (vec) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                   :: "r"(umma::smem_u32(dst)), "l"(src), "r"(row < n ? 16 : 0) : "memory");
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a = __bfloat16_as_ushort(src[2 * i]), b = __bfloat16_as_ushort(src[2 * i + 1]);
-        w[i] = row < n ? a | b << 16 : 0;
+#pragma unroll 4
+      for (int e = 0; e < kLoads; ++e) {
+        const bool live = row_of(e) < c.n;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     ::"r"(umma::smem_u32(to) + e * (kStep / 8) * 1024), "l"(live ? from : first),
+                     "r"(live ? 16 : 0) : "memory");
+        from += (long long)kStep * stride;
       }
-      *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll 1
+      for (int e = 0; e < kLoads; ++e) {
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (row_of(e) < c.n) {
+          const unsigned short *x = reinterpret_cast<const unsigned short *>(from);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = (uint32_t)x[2 * i] | (uint32_t)x[2 * i + 1] << 16;
+        }
+        *reinterpret_cast<uint4 *>(to + e * (kStep / 8) * 1024) = make_uint4(w[0], w[1], w[2], w[3]);
+        from += (long long)kStep * stride;
+      }
     }
   }
+};
+
+// Two values as bf16 (rounded), and what the rounding left.
+__device__ __forceinline__ uint32_t peel(f2 &x) {
+  const float2 v = unpack2(x);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  const uint32_t r = *reinterpret_cast<const uint32_t *>(&b);
+  x = add2(x, pack2(-__uint_as_float(r << 16), -__uint_as_float(r & 0xffff0000u)));
+  return r;
+}
+__device__ __forceinline__ uint32_t round2(f2 x) {
+  const float2 v = unpack2(x);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// Eight keys times w, in three bf16 parts.
-__device__ __forceinline__ void split3(uint4 k, float w, uint4 *hi, uint4 *mid, uint4 *lo) {
+// Eight keys times w, in three bf16 parts; hi in place.
+__device__ __forceinline__ void split3(unsigned char *hi, unsigned char *mid, unsigned char *lo, float w) {
+  const uint4 k = *reinterpret_cast<const uint4 *>(hi);
   const uint32_t in[4] = {k.x, k.y, k.z, k.w};
   uint32_t h[4], m[4], l[4];
+  const f2 ww = both(w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = __uint_as_float(in[i] << 16) * w, b = __uint_as_float(in[i] & 0xffff0000u) * w;
-    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-    const float2 f = __bfloat1622float2(p);
-    h[i] = *reinterpret_cast<const uint32_t *>(&p);
-    umma::split_bf16x2(a - f.x, b - f.y, m[i], l[i]);
+    f2 x = mul2(pack2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)), ww);
+    h[i] = peel(x);
+    m[i] = peel(x);
+    l[i] = round2(x);
   }
-  *hi = make_uint4(h[0], h[1], h[2], h[3]);
-  *mid = make_uint4(m[0], m[1], m[2], m[3]);
-  *lo = make_uint4(l[0], l[1], l[2], l[3]);
+  *reinterpret_cast<uint4 *>(hi) = make_uint4(h[0], h[1], h[2], h[3]);
+  *reinterpret_cast<uint4 *>(mid) = make_uint4(m[0], m[1], m[2], m[3]);
+  *reinterpret_cast<uint4 *>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 // What a thread holds of the state: a row (value channel) and NS of its columns
@@ -115,51 +160,57 @@ __device__ __forceinline__ int frag_at(int warp, int lane, int f) {
   return (warp * (NS / 4) + f) * 32 + lane;
 }
 
-// A token's log decay in units of log 2; what is below e^-15000 forgets.
-__device__ __forceinline__ double log2_decay(float g) {
-  return (double)(g < -15000.0f ? -15000.0f : g) * kLog2eD;
+// Log decays are summed in fixed point, in units of 2^-44 log 2: exact, and
+// without fp64, which this GPU has little of.  A token's is held within
+// e^{+-210}, beyond fp32 in both directions, so that 64 of them fit.
+constexpr float kFixed = 17592186044416.0f, kUnit = 1.0f / kFixed;
+__device__ __forceinline__ long long fixed_log2(float g) {
+  g = fminf(fmaxf(g, -210.0f), 210.0f);
+  const float hi = g * kLog2e, lo = fmaf(g, kLog2e, -hi) + g * 1.92596299e-8f;  // log2(e) - kLog2e
+  return __float2ll_rn(hi * kFixed) + __float2ll_rn(lo * kFixed);
 }
+__device__ __forceinline__ float unfixed(long long x) { return __ll2float_rn(x) * kUnit; }
 
-// The chunk's decays g of tokens 2 lane and 2 lane + 1, summed from the first.
+// Decays of a chunk, for a warp that has the log decays of tokens 2 lane and 2
+// lane + 1 (0 behind the last token): the sums from the first token on.
 struct ChunkDecay {
-  double g0, g1, total;
+  long long g0, g1, total;
+  float nan0, nan1, nan;  // 0, or NaN from a token on whose decay is NaN
   __device__ __forceinline__ ChunkDecay(float a, float b) {
     const int lane = threadIdx.x & 31;
-    const double x0 = log2_decay(a), x1 = x0 + log2_decay(b);
-    double upto = x1;
+    const long long x0 = fixed_log2(a), x1 = x0 + fixed_log2(b);
+    long long upto = x1;
 #pragma unroll
     for (int w = 1; w < 32; w *= 2) {
-      const double o = __shfl_up_sync(0xffffffffu, upto, w);
+      const long long o = __shfl_up_sync(0xffffffffu, upto, w);
       if (lane >= w) upto += o;
     }
     g0 = upto - x1 + x0;
     g1 = upto;
     total = __shfl_sync(0xffffffffu, upto, 31);
+    nan0 = nan1 = nan = 0.0f;
+    const unsigned bad = __ballot_sync(0xffffffffu, a != a || b != b);
+    if (bad) {
+      nan = __int_as_float(0x7fffffff);
+      const int first = __ffs(bad) - 1;
+      if (lane > first || (lane == first && a != a)) nan0 = nan;
+      if (lane >= first) nan1 = nan;
+    }
   }
 };
-__device__ __forceinline__ float2 halves(double g) {
-  const float hi = (float)g;
-  return make_float2(hi, (float)(g - (double)hi));
-}
-__device__ __forceinline__ float2 total_decay(double log2) { return decay_pair((float)(log2 / kLog2eD)); }
 
-// The tokens of chunk q of a segment (chunks end at absolute multiples of 64).
-struct Chunk {
-  int begin, n;
-  __device__ __forceinline__ Chunk(const SegLoc &s, int skew, int q) {
-    const long long b = (long long)q * 64 - skew, e = b + 64;
-    const int lo = b > 0 ? (int)b : 0, hi = e < s.len ? (int)e : s.len;
-    begin = s.begin + lo;
-    n = hi - lo;
-  }
-};
+// The log decay of the e-th of a lane's two tokens.
+__device__ __forceinline__ float log_decay(const LinearParams &p, const Chunk &c, int h, int e) {
+  const int t = 2 * (threadIdx.x & 31) + e;
+  return t < c.n ? row_at(p.g, c.begin + t, p.gs)[h] : 0.0f;
+}
 
 // ------------------------------------------------------- what a part adds
 template <int DK, int DV>
 struct SumLay {
   static constexpr uint32_t kK = DK * 128, kV = DV * 128;
   static constexpr uint32_t K = 0, V = 2 * kK, MID = V + 2 * kV, LO = MID + kK, MISC = LO + kK;
-  static constexpr uint32_t W = MISC, MBAR = W + 256, TSLOT = MBAR + 8, END = TSLOT + 8;
+  static constexpr uint32_t W = MISC, MBAR = W + 512, TSLOT = MBAR + 8, END = TSLOT + 8;
 };
 
 // U = sum_j e^{G_end - G_j} k_j v_j^T over a part that is not its segment's last,
@@ -176,71 +227,79 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p) 
   if (loc.seg < 0 || loc.part + 1 >= loc.parts) return;
   SegLoc s;
   if (!locate_segment(p.seg, loc.seg, &s)) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int skew = p.seg.start_pos ? p.seg.start_pos[loc.seg] & 63 : 0;
-  const int q0 = loc.part * p.part_chunks, nq = p.part_chunks, hq = h / p.rep;
+  const int nq = p.part_chunks, q1 = loc.part * nq + nq - 1;
   const uint32_t sb = umma::smem_u32(sm);
   float *w = reinterpret_cast<float *>(sm + Lay::W);
   uint64_t *mbar = reinterpret_cast<uint64_t *>(sm + Lay::MBAR);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Lay::TSLOT);
+  const Rows<DK, kThreads> kr(tid);
+  const Rows<DV, kThreads> vr(tid);
 
   auto load = [&](int it) {
     if (it < nq) {
-      const Chunk c(s, skew, q0 + nq - 1 - it);
-      load_rows<DK>(sm + Lay::K + (it & 1) * Lay::kK, 8192, p.k, c.begin, p.ks, hq * DK, c.n, p.vec);
-      load_rows<DV>(sm + Lay::V + (it & 1) * Lay::kV, 8192, p.v, c.begin, p.vs, h * DV, c.n, p.vec);
+      const Chunk c(s, skew, q1 - it);
+      kr.load(sm + Lay::K + (it & 1) * Lay::kK, 8192, p.k, p.ks, h / p.rep * DK, c, p.vec);
+      vr.load(sm + Lay::V + (it & 1) * Lay::kV, 8192, p.v, p.vs, h * DV, c, p.vec);
     }
     copy_commit();
   };
-  double later = 0.0;
-  auto weigh = [&](int it) {  // warp 0
-    const Chunk c(s, skew, q0 + nq - 1 - it);
-    float g[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) g[e] = 2 * lane + e < c.n ? row_at(p.g, c.begin + 2 * lane + e, p.gs)[h] : 0.0f;
-    const ChunkDecay d(g[0], g[1]);
-    w[2 * lane] = ex2f((float)(later + (d.total - d.g0)));
-    w[2 * lane + 1] = ex2f((float)(later + (d.total - d.g1)));
-    later += d.total;
+  long long later = 0;
+  float nan = 0.0f, g[2] = {0.0f, 0.0f};
+  auto ask = [&](int it) {  // warp 0
+    if (it >= nq) return;
+    const Chunk c(s, skew, q1 - it);
+    g[0] = log_decay(p, c, h, 0);
+    g[1] = log_decay(p, c, h, 1);
   };
+  auto weigh = [&](int it) {
+    const ChunkDecay d(g[0], g[1]);
+    float *to = w + (it & 1) * 64 + 2 * lane;
+    nan += d.nan;
+    to[0] = ex2f(unfixed(later + (d.total - d.g0))) + nan;
+    to[1] = ex2f(unfixed(later + (d.total - d.g1))) + nan;
+    later = max(later + d.total, -(1LL << 60));
+    later = min(later, 1LL << 60);
+  };
+  if (warp == 0) ask(0);
   load(0);
   load(1);
   if (warp == 1) umma::tmem_alloc(tslot, 128);
   if (tid == 0) umma::mbar_init(mbar, 1);
-  if (warp == 0) weigh(0);
+  if (warp == 0) {
+    weigh(0);
+    ask(1);
+  }
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = *tslot, tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-  uint32_t phase = 0;
   bool ok = true;
   int it = 0;
   for (; it < nq; ++it) {
     // the chunk's rows are there, and those of the chunk before are done with
-    if (it > 0) {
-      copy_wait();
-      if (!(ok = tc_wait(mbar, phase, p.spin_limit))) break;
-      load(it + 1);
+    if (it == 0) {
+      copy_wait<1>();
     } else {
-      copy_wait_but_one();
-      __syncthreads();
+      copy_wait<0>();
+      ok = warp_wait(mbar, (it - 1) & 1, p.spin_limit);
+      if (ok) load(it + 1);
     }
     const uint32_t kt = Lay::K + (it & 1) * Lay::kK, vt = Lay::V + (it & 1) * Lay::kV;
-    {
-      constexpr int kC = DK / 32;  // 16-byte chunks of a thread
-      const int j = tid >> 2, c0 = (tid & 3) * kC;
-      const float wj = w[j];
+    if (ok) {
 #pragma unroll
-      for (int e = 0; e < kC; ++e) {
-        const int c = c0 + e;
-        const uint32_t off = (c >> 3) * 8192 + (j >> 3) * 1024 + (j & 7) * 128 + (((c & 7) ^ (j & 7)) << 4);
-        uint4 *k = reinterpret_cast<uint4 *>(sm + kt + off);
-        split3(*k, wj, k, reinterpret_cast<uint4 *>(sm + Lay::MID + off),
-               reinterpret_cast<uint4 *>(sm + Lay::LO + off));
+      for (int e = 0; e < kr.kLoads; ++e) {
+        const uint32_t off = kr.place(e, 8192);
+        split3(sm + kt + off, sm + Lay::MID + off, sm + Lay::LO + off, w[(it & 1) * 64 + kr.row_of(e)]);
+      }
+      if (warp == 0 && it + 1 < nq) {
+        weigh(it + 1);
+        ask(it + 2);
       }
     }
-    tiles_ready();
-    if (tid == 0) {
+    if (!(ok = tiles_ready(ok))) break;
+    if (warp == 3 && umma::elect_one()) {
       const uint64_t dv = umma::sdesc_sw128_mn(sb + vt, DV == 128 ? 8192 : 0);
       const uint32_t id = umma::idesc_bf16_abmn(128, DK);
 #pragma unroll
@@ -252,9 +311,8 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p) 
       }
       umma::commit(mbar);
     }
-    if (warp == 0 && it + 1 < nq) weigh(it + 1);
   }
-  if (ok) ok = tc_wait(mbar, phase, p.spin_limit);
+  if (ok) ok = __syncthreads_and(warp_wait(mbar, (nq - 1) & 1, p.spin_limit)) != 0;
   if (ok) {
     const long long at = (long long)target * p.H + h;
     float4 *dst = reinterpret_cast<float4 *>(p.part_state + at * DK * DV);
@@ -267,12 +325,17 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p) 
         dst[frag_at<F::NS>(warp, lane, c / 4 + f)] =
             make_float4(v[4 * f], v[4 * f + 1], v[4 * f + 2], v[4 * f + 3]);
     }
-    if (tid == 0) p.part_decay[at] = total_decay(later);
+    if (tid == 0) {
+      const float2 a = decay_pair(unfixed(later) * kLn2);
+      p.part_decay[at] = make_float2(a.x + nan, a.y);
+    }
   } else if (tid == 0) {
     set_error(p.seg.err, KDA_DERR_TIMEOUT);
-    if (!umma::mbar_wait(mbar, phase, kDrainWaitPolls)) set_error(p.seg.err, KDA_DERR_UNSAFE);
+    // one more bounded chance for the tensor cores before TMEM is freed
+    const int last = min(it, nq) - 1;
+    if (last >= 0 && !umma::mbar_wait(mbar, last & 1, kDrainWaitPolls)) set_error(p.seg.err, KDA_DERR_UNSAFE);
   }
-  copy_wait();
+  copy_wait<0>();
   umma::fence_before_sync();
   __syncthreads();
   if (warp == 1) umma::tmem_dealloc(tmem, 128);
@@ -323,19 +386,28 @@ struct OutLay {
   static constexpr uint32_t kQK = DK * 256, kV = DV * 128;
   static constexpr uint32_t kKt = DK * 128;  // a part of K~
   static constexpr uint32_t kS = DK * DV * 2 > 2 * kKt ? DK * DV * 2 : 2 * kKt;
+  // Rows of outputs on their way out: 16 bytes apart beside their own, so that
+  // lanes with a row each meet no bank twice.
+  static constexpr uint32_t kRow = DV * 2 + 16;
   // The masked Q K^T: hi in Q's first block, lo in its second or behind the state.
   static constexpr uint32_t QK = 0, V = 2 * kQK, S = V + kV, P2 = S + kS;
-  static constexpr uint32_t MISC = P2 + (DK == 64 ? 16384 : 0);
-  static constexpr uint32_t G = MISC, W = G + 512, A = W + 256, MBAR = A + 8, TSLOT = MBAR + 8,
+  static constexpr uint32_t MISC = P2 + (DK == 64 ? 18432 : 0);
+  static_assert(64 * kRow <= (DK == 64 ? 18432 : kQK), "outputs take the place of the weights");
+  static constexpr uint32_t G = MISC, W = G + 512, A = W + 256, MBAR = A + 8, TSLOT = MBAR + 24,
                             END = TSLOT + 8;
 };
 static_assert(2 * (OutLay<128, 128>::END + 1024) <= 228 * 1024, "two blocks an SM");
 
+// Per chunk: products of q (with k, with the state), then the masked weights P by
+// the warps of lanes 0 to 63 of TMEM, which have the tokens' rows, while the others
+// split K~; then what the chunk adds to the state, P V; then the state and its bf16
+// tile by all, while P V runs, and the outputs by the first.  The others do the loads: q and k a
+// chunk ahead, v as soon as P V is done with the last.
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) {
   using Lay = OutLay<DK, DV>;
   using F = Frag<DK, DV>;
-  constexpr int NS = F::NS;
+  constexpr int NS = F::NS, kCols = NS < 32 ? 16 : 32;
   extern __shared__ __align__(1024) unsigned char sm[];
   begin_after_stream();
   const int h = blockIdx.x % p.H, target = blockIdx.x / p.H;
@@ -357,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) 
     set_error(p.seg.err, KDA_DERR_SEGMENT);
     return;
   }
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, half = warp >> 2;
-  const int skew = p0 & 63, hq = h / p.rep;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, quad = warp & 3, half = warp >> 2;
+  const int skew = p0 & 63;
   const int chunks = (int)((skew + (long long)s.len + 63) >> 6);
   int q0 = 0, q1 = chunks;
   if (p.part_chunks) {
@@ -366,97 +438,120 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) 
     q1 = min(chunks, q0 + p.part_chunks);
   }
   const uint32_t sb = umma::smem_u32(sm);
-  float2 *G = reinterpret_cast<float2 *>(sm + Lay::G);
+  float *G = reinterpret_cast<float *>(sm + Lay::G);  // -G_j: 64 hi, 64 lo
   float *w = reinterpret_cast<float *>(sm + Lay::W);
   float2 *whole = reinterpret_cast<float2 *>(sm + Lay::A);
-  uint64_t *mbar = reinterpret_cast<uint64_t *>(sm + Lay::MBAR);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Lay::MBAR);  // products of q, U, P V
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Lay::TSLOT);
+  const bool tokens = quad < 2;                       // the warps of the tokens' rows
+  const int t2 = ((quad & 1) + 2 * half) * 32 + lane;  // thread among the others
+  const Rows<DK, 128> kr(t2);
+  const Rows<DV, 128> vr(t2);
 
   auto load_qk = [&](int q) {
     if (q < q1) {
       const Chunk c(s, skew, q);
       unsigned char *dst = sm + Lay::QK + ((q - q0) & 1) * Lay::kQK;
-      load_rows<DK>(dst, 16384, p.q, c.begin, p.qs, hq * DK, c.n, p.vec);
-      load_rows<DK>(dst + 8192, 16384, p.k, c.begin, p.ks, hq * DK, c.n, p.vec);
+      kr.load(dst, 16384, p.q, p.qs, h / p.rep * DK, c, p.vec);
+      kr.load(dst + 8192, 16384, p.k, p.ks, h / p.rep * DK, c, p.vec);
     }
     copy_commit();
   };
   auto load_v = [&](int q) {
     if (q < q1) {
       const Chunk c(s, skew, q);
-      load_rows<DV>(sm + Lay::V, 8192, p.v, c.begin, p.vs, h * DV, c.n, p.vec);
+      vr.load(sm + Lay::V, 8192, p.v, p.vs, h * DV, c, p.vec);
     }
     copy_commit();
   };
-  auto log_decays = [&](int q, float (&g)[2]) {  // of the lane's tokens
+  // The decays of the next chunk: asked for, summed and published by the warp
+  // whose part of the weights is all zeros.
+  constexpr int kDecayWarp = 4;
+  float g[2] = {0.0f, 0.0f}, gh[2], gl[2], gw[2];
+  float2 ga;
+  auto ask = [&](int q) {
+    if (q >= q1) return;
     const Chunk c(s, skew, q);
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      g[e] = q < q1 && 2 * lane + e < c.n ? row_at(p.g, c.begin + 2 * lane + e, p.gs)[h] : 0.0f;
+    g[0] = log_decay(p, c, h, 0);
+    g[1] = log_decay(p, c, h, 1);
   };
-  auto weigh = [&](const float (&g)[2]) {  // one warp
+  auto weigh = [&]() {
     const ChunkDecay d(g[0], g[1]);
-    G[2 * lane] = halves(d.g0);
-    G[2 * lane + 1] = halves(d.g1);
-    w[2 * lane] = ex2f((float)(d.total - d.g0));
-    w[2 * lane + 1] = ex2f((float)(d.total - d.g1));
-    if (lane == 0) *whole = total_decay(d.total);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long x = -(e ? d.g1 : d.g0);
+      const float hi = __ll2float_rn(x);
+      gh[e] = hi * kUnit + (e ? d.nan1 : d.nan0);
+      gl[e] = unfixed(x - __float2ll_rn(hi));
+      gw[e] = ex2f(unfixed(d.total + x)) + d.nan;
+    }
+    ga = decay_pair(unfixed(d.total) * kLn2);
+    ga.x += d.nan;
   };
-  load_qk(q0);
-  load_v(q0);
-  if (warp == 1) umma::tmem_alloc(tslot, 256);
-  if (tid == 0) umma::mbar_init(mbar, 1);
-  constexpr int kDecayWarp = 2;
-  float g[2];
-  if (warp == kDecayWarp) {
-    log_decays(q0, g);
-    weigh(g);
+  auto publish = [&]() {
+    *reinterpret_cast<float2 *>(G + 2 * lane) = make_float2(gh[0], gh[1]);
+    *reinterpret_cast<float2 *>(G + 64 + 2 * lane) = make_float2(gl[0], gl[1]);
+    *reinterpret_cast<float2 *>(w + 2 * lane) = make_float2(gw[0], gw[1]);
+    if (lane == 0) *whole = ga;
+  };
+  if (warp == kDecayWarp) ask(q0);
+  if (!tokens) {
+    load_qk(q0);
+    load_v(q0);
   }
+  if (warp == 1) umma::tmem_alloc(tslot, 256);
+  if (tid == 0)
+    for (int i = 0; i < 3; ++i) umma::mbar_init(bar + i, 1);
   const int row = F::row(warp, lane), col = F::col(warp);
-  const long long head_at = (long long)h * DK * DV + row * DK + col, slot_size = (long long)p.H * DK * DV;
-  float S[NS];
+  auto slot_at = [&](int slot) { return p.pool + ((long long)slot * p.H + h) * DK * DV + row * DK + col; };
+  f2 S[NS / 2];
   {
     const float4 *src = loc.parts > 1 ? reinterpret_cast<const float4 *>(
                                             p.part_state + ((long long)target * p.H + h) * DK * DV)
-                                      : reinterpret_cast<const float4 *>(p.pool + s.slot * slot_size + head_at);
+                                      : reinterpret_cast<const float4 *>(slot_at(s.slot));
 #pragma unroll
     for (int f = 0; f < NS / 4; ++f) {
       const float4 v = src[loc.parts > 1 ? frag_at<NS>(warp, lane, f) : f];
-      S[4 * f] = v.x;
-      S[4 * f + 1] = v.y;
-      S[4 * f + 2] = v.z;
-      S[4 * f + 3] = v.w;
+      S[2 * f] = pack2(v.x, v.y);
+      S[2 * f + 1] = pack2(v.z, v.w);
     }
   }
   auto store = [&](int slot) {
-    float4 *dst = reinterpret_cast<float4 *>(p.pool + slot * slot_size + head_at);
+    f2 *dst = reinterpret_cast<f2 *>(slot_at(slot));
 #pragma unroll
-    for (int f = 0; f < NS / 4; ++f) dst[f] = make_float4(S[4 * f], S[4 * f + 1], S[4 * f + 2], S[4 * f + 3]);
+    for (int f = 0; f < NS / 2; ++f) dst[f] = S[f];
   };
+  auto tile = [&]() {  // the state in bf16, as [d_v][d_k]
+#pragma unroll
+    for (int e = 0; e < NS; e += 8)
+      *reinterpret_cast<uint4 *>(sm + Lay::S + umma::sw128_off16(row, col + e, DV)) = make_uint4(
+          round2(S[e / 2]), round2(S[e / 2 + 1]), round2(S[e / 2 + 2]), round2(S[e / 2 + 3]));
+  };
+  // the next checkpoint, and the segment's tokens after which it is due
+  unsigned due = 0, ckpt = 0;
+  if (p.seg.ckpt_slots) {
+    const unsigned every = p.seg.ckpt_every, done = Chunk(s, skew, q0).begin - s.begin;
+    ckpt = (p0 + done) / every - p0 / every;
+    due = (ckpt + 1) * every - p0 % every;
+  }
+  tile();
+  if (warp == kDecayWarp) {
+    weigh();
+    publish();
+  }
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = *tslot, tl = tmem + ((uint32_t)(quad * 32) << 16);
-  uint32_t phase = 0;
-  bool ok = true, owed = false;
+  bool ok = true;
+  int first = -1, second = -1;  // chunks whose products of q, and U and P V, were issued last
   for (int q = q0; q < q1; ++q) {
     const Chunk c(s, skew, q);
-    const uint32_t qk = Lay::QK + ((q - q0) & 1) * Lay::kQK, pl = DK == 64 ? Lay::P2 : qk + 16384;
-    if (warp == kDecayWarp) log_decays(q + 1, g);
-#pragma unroll
-    for (int e = 0; e < NS; e += 8) {  // the state as [d_v][d_k]
-      uint32_t b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(S[e + 2 * i], S[e + 2 * i + 1]);
-        b[i] = *reinterpret_cast<const uint32_t *>(&x);
-      }
-      *reinterpret_cast<uint4 *>(sm + Lay::S + umma::sw128_off16(row, col + e, DV)) =
-          make_uint4(b[0], b[1], b[2], b[3]);
-    }
-    copy_wait_but_one();  // q and k of this chunk
-    tiles_ready();
-    if (tid == 0) {
+    const uint32_t par = (q - q0) & 1, qk = Lay::QK + par * Lay::kQK, pl = DK == 64 ? Lay::P2 : qk + 16384;
+    copy_wait<1>();  // q and k of this chunk
+    if (!(ok = tiles_ready(ok))) break;
+    if (warp == kDecayWarp) ask(q + 1);
+    if (warp == kDecayWarp && umma::elect_one()) {
       const uint64_t dq = umma::sdesc_sw128(sb + qk), ds = umma::sdesc_sw128(sb + Lay::S);
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) {
@@ -469,57 +564,74 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) 
         umma::mma_bf16(tmem + kAccO, dadd(dq, (kk >> 2) * 16384 + (kk & 3) * 32),
                        dadd(ds, (kk >> 2) * (DV * 128) + (kk & 3) * 32), umma::idesc_bf16(128, DV),
                        (uint32_t)kk);
-      umma::commit(mbar);
+      umma::commit(bar);
     }
-    owed = true;
-    load_qk(q + 1);
-    if (!(ok = tc_wait(mbar, phase, p.spin_limit))) break;
-    owed = false;
+    first = q - q0;
+    if (!tokens) load_qk(q + 1);
     const float2 a = *whole;
-    if (quad < 2) {  // rows of the chunk's tokens
+    ok = warp_wait(bar, par, p.spin_limit);
+    if (ok && tokens) {
       const int i = 32 * quad + lane;
-      const float2 gi = G[i];
-      float x[32];
-      umma::tmem_ld32(tl + kAccU + 32 * half, x);
+      const float ih = -G[i], il = -G[64 + i];
+      if (quad == 0 && half == 1) {  // later tokens only
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int j = 32 * half + e + u;
-          const float2 gj = G[j];
-          x[e + u] = j <= i ? x[e + u] * ex2f((gi.x - gj.x) + (gi.y - gj.y)) : 0.0f;
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t off = umma::sw128_off16(i, 32 + 8 * e, 64);
+          *reinterpret_cast<uint4 *>(sm + qk + off) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(sm + pl + off) = make_uint4(0, 0, 0, 0);
         }
+        weigh();
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < 32; e += 16) {
+          float x[16];
+          umma::tmem_ld16(tl + kAccU + 32 * half + e, x);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) umma::split_bf16x2(x[e + 2 * u], x[e + 2 * u + 1], hi[u], lo[u]);
-        const uint32_t off = umma::sw128_off16(i, 32 * half + e, 64);
-        *reinterpret_cast<uint4 *>(sm + qk + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(sm + pl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          for (int v = 0; v < 16; v += 8) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int u = 0; u < 8; u += 2) {
+              const int j = 32 * half + e + v + u;
+              const float2 jh = *reinterpret_cast<const float2 *>(G + j);
+              const float2 jl = *reinterpret_cast<const float2 *>(G + 64 + j);
+              const f2 d = add2(add2(both(ih), pack2(jh.x, jh.y)), add2(both(il), pack2(jl.x, jl.y)));
+              float2 y = unpack2(mul2(exp2_2(d), pack2(x[v + u], x[v + u + 1])));
+              y.x = j <= i ? y.x : 0.0f;
+              y.y = j + 1 <= i ? y.y : 0.0f;
+              f2 z = pack2(y.x, y.y);
+              hi[u / 2] = peel(z);
+              lo[u / 2] = round2(z);
+            }
+            const uint32_t off = umma::sw128_off16(i, 32 * half + e + v, 64);
+            *reinterpret_cast<uint4 *>(sm + qk + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(sm + pl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
       }
-      const float eg = ex2f(gi.x + gi.y);
-#pragma unroll
+      const float eg = ex2f(ih + il);
+#pragma unroll 1
       for (int e = 0; e < DV / 2; e += 32) {
         const uint32_t at = tl + kAccO + half * (DV / 2) + e;
+        float x[32];
         umma::tmem_ld32(at, x);
 #pragma unroll
-        for (int u = 0; u < 32; ++u) x[u] *= eg;
+        for (int u = 0; u < 32; u += 2) {
+          const float2 y = unpack2(mul2(pack2(x[u], x[u + 1]), both(eg)));
+          x[u] = y.x;
+          x[u + 1] = y.y;
+        }
         umma::tmem_st32(at, x);
       }
-    } else {  // keys: hi in place, mid and lo where the state was
-      const int t = ((quad - 2) + 2 * half) * 32 + lane, j = t >> 1;
-      const float wj = w[j];
-#pragma unroll
-      for (int e = 0; e < DK / 16; ++e) {
-        const int ch = (t & 1) * (DK / 16) + e;
-        const uint32_t off = (j >> 3) * 1024 + (j & 7) * 128 + (((ch & 7) ^ (j & 7)) << 4);
-        uint4 *k = reinterpret_cast<uint4 *>(sm + qk + 8192 + (ch >> 3) * 16384 + off);
-        unsigned char *m = sm + Lay::S + (ch >> 3) * 8192 + off;
-        split3(*k, wj, k, reinterpret_cast<uint4 *>(m), reinterpret_cast<uint4 *>(m + Lay::kKt));
+    } else if (ok) {  // keys: hi in place, mid and lo where the state was
+#pragma unroll 2
+      for (int e = 0; e < kr.kLoads; ++e) {
+        unsigned char *m = sm + Lay::S + kr.place(e, 8192);
+        split3(sm + qk + 8192 + kr.place(e, 16384), m, m + Lay::kKt, w[kr.row_of(e)]);
       }
     }
-    copy_wait_but_one();  // v of this chunk
-    tiles_ready();
-    if (tid == 0) {
+    copy_wait<1>();  // v of this chunk
+    if (!(ok = tiles_ready(ok))) break;
+    if (warp == 3 && umma::elect_one()) {
       const uint64_t dva = umma::sdesc_sw128_mn(sb + Lay::V, DV == 128 ? 8192 : 0);
       const uint64_t dvb = umma::sdesc_sw128_mn(sb + Lay::V, 8192);
 #pragma unroll
@@ -531,6 +643,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) 
           umma::mma_bf16(tmem + kAccU, dadd(dva, kk * 2048), dadd(dk, kk * 2048),
                          umma::idesc_bf16_abmn(128, DK), (uint32_t)(part | kk));
       }
+      umma::commit(bar + 1);
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
         const uint64_t dp = umma::sdesc_sw128(sb + (part ? pl : qk));
@@ -539,59 +652,88 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) 
           umma::mma_bf16(tmem + kAccO, dadd(dp, kk * 32), dadd(dvb, kk * 2048),
                          umma::idesc_bf16_bmn(128, DV), 1u);
       }
-      umma::commit(mbar);
+      umma::commit(bar + 2);
     }
-    owed = true;
-    if (!(ok = tc_wait(mbar, phase, p.spin_limit))) break;
-    owed = false;
-    load_v(q + 1);
-    if (warp == kDecayWarp) weigh(g);
+    second = q - q0;
+    ok = warp_wait(bar + 1, par, p.spin_limit);
+    if (ok) {
+      if (warp == kDecayWarp) publish();
+      const f2 ah = both(a.x), al = both(a.y);
 #pragma unroll
-    for (int e = 0; e < NS; e += 16) {
-      float u[16];
-      umma::tmem_ld16(tl + kAccU + col + e, u);
+      for (int e = 0; e < NS; e += kCols) {
+        float u[kCols];
+        if constexpr (kCols == 32) umma::tmem_ld32(tl + kAccU + col + e, u);
+        else umma::tmem_ld16(tl + kAccU + col + e, u);
 #pragma unroll
-      for (int x = 0; x < 16; ++x) S[e + x] = decayed(S[e + x], a, u[x]);
-    }
-    if (p.seg.ckpt_slots) {
-      const int slot = checkpoint_slot(p.seg, loc.seg, p0, c.begin - s.begin + c.n);
-      if (slot >= 0) store(slot);
-    }
-    if (quad < 2) {
-      const int i = 32 * quad + lane;
-      __nv_bfloat16 *o = row_at(static_cast<__nv_bfloat16 *>(p.o), c.begin + i, p.os) + h * DV + half * (DV / 2);
-#pragma unroll
-      for (int e = 0; e < DV / 2; e += 16) {
-        float x[16];
-        umma::tmem_ld16(tl + kAccO + half * (DV / 2) + e, x);
-        if (i >= c.n) continue;
-        uint32_t b[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * u] * p.scale, x[2 * u + 1] * p.scale);
-          b[u] = *reinterpret_cast<const uint32_t *>(&y);
+        for (int x = 0; x < kCols; x += 2)
+          S[(e + x) / 2] = fma2(S[(e + x) / 2], ah, fma2(S[(e + x) / 2], al, pack2(u[x], u[x + 1])));
+      }
+      tile();
+      if (c.begin - s.begin + c.n == due) {
+        if (ckpt < p.seg.max_ckpt) {
+          const int slot = p.seg.ckpt_slots[(long long)loc.seg * p.seg.max_ckpt + ckpt];
+          if (slot >= p.seg.P) set_error(p.seg.err, KDA_DERR_SLOT);
+          else if (slot >= 0) store(slot);
         }
-        if (p.o_vec) {
-          *reinterpret_cast<uint4 *>(o + e) = make_uint4(b[0], b[1], b[2], b[3]);
-          *reinterpret_cast<uint4 *>(o + e + 8) = make_uint4(b[4], b[5], b[6], b[7]);
-        } else {
+        due += p.seg.ckpt_every;
+        ++ckpt;
+      }
+      ok = warp_wait(bar + 2, par, p.spin_limit);
+    }
+    if (ok && !tokens) load_v(q + 1);
+    if (ok && tokens) {
+      // a lane has a row; through shared memory the warp stores whole lines
+      unsigned char *stage = sm + (DK == 64 ? Lay::P2 : qk) + 32 * quad * Lay::kRow + half * DV;
+#pragma unroll 1
+      for (int e = 0; e < DV / 2; e += 32) {
+        float x[32];
+        umma::tmem_ld32(tl + kAccO + half * (DV / 2) + e, x);
+        uint32_t b[16];
 #pragma unroll
-          for (int u = 0; u < 16; ++u)
-            o[e + u] = __ushort_as_bfloat16((unsigned short)(b[u / 2] >> (u & 1) * 16));
+        for (int u = 0; u < 16; ++u) b[u] = round2(mul2(pack2(x[2 * u], x[2 * u + 1]), both(p.scale)));
+#pragma unroll
+        for (int u = 0; u < 16; u += 4)
+          *reinterpret_cast<uint4 *>(stage + lane * Lay::kRow + 2 * e + 4 * u) =
+              make_uint4(b[u], b[u + 1], b[u + 2], b[u + 3]);
+      }
+      __syncwarp();
+      constexpr int kLanes = DV / 16;  // that store a row's half
+      const int at = lane % kLanes * 8;
+      int i = 32 * quad + lane / kLanes;
+      const __nv_bfloat16 *from = reinterpret_cast<const __nv_bfloat16 *>(stage + lane / kLanes * Lay::kRow) + at;
+      __nv_bfloat16 *o = row_at(static_cast<__nv_bfloat16 *>(p.o), c.begin + i, p.os) + h * DV + half * (DV / 2) + at;
+#pragma unroll 4
+      for (int e = 0; e < 32 / (32 / kLanes); ++e) {
+        if (i < c.n) {
+          const uint4 b = *reinterpret_cast<const uint4 *>(from);
+          if (p.o_vec) {
+            *reinterpret_cast<uint4 *>(o) = b;
+          } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) o[u] = from[u];
+          }
         }
+        i += 32 / kLanes;
+        from += 32 / kLanes * Lay::kRow / 2;
+        o = row_at(o, 32 / kLanes, p.os);
       }
     }
   }
+  ok = __syncthreads_and(ok) != 0;
   if (!ok) {
     if (tid == 0) {
       set_error(p.seg.err, KDA_DERR_TIMEOUT);
       // one more bounded chance for the tensor cores before TMEM is freed
-      if (owed && !umma::mbar_wait(mbar, phase, kDrainWaitPolls)) set_error(p.seg.err, KDA_DERR_UNSAFE);
+      for (int i = 0; i < 3; ++i) {
+        const int last = i == 0 ? first : second;
+        if (last >= 0 && !umma::mbar_wait(bar + i, last & 1, kDrainWaitPolls))
+          set_error(p.seg.err, KDA_DERR_UNSAFE);
+      }
     }
   } else if (loc.part + 1 == loc.parts) {
     store(s.slot);
   }
-  copy_wait();
+  copy_wait<0>();
   umma::fence_before_sync();
   __syncthreads();
   if (warp == 1) umma::tmem_dealloc(tmem, 256);
@@ -620,25 +762,35 @@ cudaError_t linear_tc(const LinearParams &p, cudaStream_t s) {
 }
 
 constexpr int kBlocks = 2 * 152;  // that the GPU holds
-constexpr int kMinPart = 2;       // chunks of a part
+constexpr int kMinPart = 2, kPartCost = 2;  // chunks of a part
 constexpr int kMaxSplitSeqs = 1024;
 
 }  // namespace
 
-// Parts that fill the machine once where there are few long segments; more
-// segments fill it alone, and searching them costs more.
+// Parts fill whole waves of blocks.  A segment's last part is half a part on
+// average, and a part costs kPartCost chunks beside its own, so the waves that
+// take least are few for few segments; more than kMaxSplitSeqs segments fill the
+// machine alone, and searching them costs more.
 int linear_part_chunks(int N, int B, int H) {
   if (B > kMaxSplitSeqs) return 0;
-  const long long pc = ((long long)N * H + 64 * kBlocks - 1) / (64 * kBlocks);
-  const int part = pc < kMinPart ? kMinPart : (int)pc;
-  return (long long)part * 64 < N ? part : 0;
+  const int room = H < kBlocks ? kBlocks / H : 1, chunks = N / 64 + 1;
+  long long least = 0;
+  int best = 0;
+  for (int waves = 1; waves <= 2 + (B - 1) / room; ++waves) {
+    const int parts = waves * room - (B - 1) / 2;
+    if (parts < 1) continue;
+    int part = (chunks + parts - 1) / parts;
+    if (part < kMinPart) part = kMinPart;
+    const long long cost = (long long)waves * (part + kPartCost);
+    if (!best || cost < least) best = part, least = cost;
+  }
+  return (long long)best * 64 < N ? best : 0;
 }
 int linear_max_parts(int N, int B, int H) { return N / (64 * linear_part_chunks(N, B, H)) + 2 * B; }
 
 size_t linear_workspace_parts(int N, int B, int H) {
-  if (!linear_part_chunks(N, 1, H)) return 0;
-  const int b = B < kMaxSplitSeqs ? B : kMaxSplitSeqs;
-  const int most = N / (64 * kMinPart), fill = kBlocks / H + 1;
+  if (N <= 64 * kMinPart || H >= kBlocks) return 0;
+  const int b = B < kMaxSplitSeqs ? B : kMaxSplitSeqs, most = N / (64 * kMinPart), fill = 2 * (kBlocks / H) + b;
   return (most < fill ? most : fill) + 2 * b;
 }
 

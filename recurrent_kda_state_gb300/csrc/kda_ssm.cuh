@@ -146,7 +146,7 @@ __device__ __forceinline__ float rcpf(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 // A log2(e), -inf held at the lowest finite value: a time step of 0, such as
 // that of a token which pads a tile, leaves the state, and 0 * -inf would be NaN.

@@ -116,6 +116,15 @@ __device__ __forceinline__ void split_bf16(float x, uint16_t &hi, uint16_t &lo) 
   lo = __bfloat16_as_ushort(l);
 }
 
+// One thread of the (converged) warp.  A branch on it lets the compiler issue
+// MMAs back to back, where one on a thread's index costs 46 cycles an MMA.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // Arrive on `mbar` once every tcgen05 op issued so far by this thread is done.
 __device__ __forceinline__ void commit(uint64_t *mbar) {
   asm volatile(
