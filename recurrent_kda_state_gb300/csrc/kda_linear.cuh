@@ -93,6 +93,7 @@ struct QkParams {
   unsigned int *err;
   int N, d, rot, max_pos, interleaved, norm;
   float eps, q_scale;
+  float share;  // of the sum of squares: 1 / d for its mean, else 1
   int per_token, tokens;  // groups of lanes on a token, tokens of a block
 };
 
@@ -102,6 +103,7 @@ struct GateParams {
   int xs, gs, ys;  // row strides in bytes
   int N, H, d, silu;
   float eps;
+  float share;  // 1 / d
 };
 
 cudaError_t launch_linear_walk(const LinearParams &p, kda_dtype dt, bool step, cudaStream_t s);

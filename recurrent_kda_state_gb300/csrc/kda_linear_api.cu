@@ -176,6 +176,7 @@ int kda_qk_norm(const kda_qk_tokens *t, kda_stream_t stream) {
   p.norm = t->norm;
   p.eps = t->eps;
   p.q_scale = t->q_scale;
+  p.share = t->norm == KDA_NORM_RMS ? 1.0f / (float)t->head_dim : 1.0f;
   return cuda_status(launch_qk_norm(p, t->dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -211,7 +212,8 @@ int kda_gated_norm(const kda_gate_tokens *t, kda_stream_t stream) {
   p.N = t->num_tokens;
   p.H = t->num_heads;
   p.d = t->head_dim;
-  p.silu = t->silu != 0;
+  p.silu = t->gate && t->silu;
+  p.share = 1.0f / (float)t->head_dim;
   p.eps = t->eps;
   return cuda_status(launch_gated_norm(p, t->x_dtype, t->dtype,
                                        reinterpret_cast<cudaStream_t>(stream)));

@@ -320,6 +320,34 @@ def test_qk_norm_heads_and_places(dt):
     qk_case(49, dt, 3000, 4, 1, 16, "l2", weights=False)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dt,n,hq,hk,d,rot", [
+    ("bf16", 1301, 31, 5, 128, 128),   # heads that leave sets of four unfull
+    ("bf16", 1800, 13, 0, 256, 64),    # queries alone, wide heads
+    ("bf16", 700, 0, 70, 80, 32),      # keys alone, lanes without channels
+    ("bf16", 200, 201, 9, 128, 32),    # more heads than a block takes
+    ("f32", 1700, 10, 3, 128, 128), ("f32", 3001, 8, 8, 64, 0)])
+def test_qk_norm_walking_down_the_tokens(interleaved, dt, n, hq, hk, d, rot):
+    """Sizes from which a block goes on to further tokens."""
+    qk_case(52, dt, n, hq, hk, d, rot=rot, interleaved=interleaved, view=8, in_place=interleaved)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_qk_norm_skips_tokens_past_the_table_walking(d):
+    rng = np.random.default_rng(53)
+    n, h = 2500, 32
+    q = rows(rng, n, (h, d), "bf16")
+    out = torch.full_like(q, MARK)
+    pos = rng.integers(-3, 8, n)
+    table = torch.cat([torch.ones(5, d // 2), torch.zeros(5, d // 2)], 1).cuda()
+    K.kda_qk_norm(K.QKBatch(q, None, cos_sin=table, positions=i32(pos), q_out=out))
+    assert K.kda_get_device_error() == K.KDA_DERR_POSITION
+    want, tol = linear_ref.qk_norm(f64(q), None, "rms", 1e-6, None, None, False, 1.0, "bf16")
+    live = (pos >= 0) & (pos < 5)
+    within(out[torch.from_numpy(live).cuda()], want[live], tol[live], "q")
+    assert (out[torch.from_numpy(~live).cuda()] == out.new_tensor(MARK)).all()
+
+
 def test_qk_norm_of_one_projection_in_place():
     """q and k are parts of the rows that hold v too, and v stays as it is."""
     rng = np.random.default_rng(50)
@@ -367,6 +395,13 @@ def test_gated_norm(xdt, dt, d):
     gate_case(61, xdt, dt, 1, 32, d, silu=True, view=8)
     gate_case(62, xdt, dt, 33, 3, d, weights=False, view=1)
     gate_case(63, xdt, dt, 9, 2, d, gate=False)
+
+
+def test_gated_norm_walking_down_the_rows():
+    """Sizes from which a block goes on to further rows."""
+    gate_case(67, "f32", "bf16", 3001, 7, 128, view=8)
+    gate_case(68, "bf16", "bf16", 2000, 31, 64, silu=True, place="gate")
+    gate_case(69, "f32", "f32", 5000, 3, 37)
 
 
 def test_gated_norm_in_place():
