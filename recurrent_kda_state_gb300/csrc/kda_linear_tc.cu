@@ -10,22 +10,28 @@
 //
 // Precision.  Decays are summed in fixed point and kept as hi + lo, so that a token
 // that forgets everything costs the later ones nothing.  K~ is split into three
-// bf16, which hold 24 bits, and V is exact: states are as good as fp32 products
-// and sums make them.  The masked Q K^T is split into two (2^-17).  The state
-// enters Q S as bf16: an error of 2^-9 of its products, as the rounding of the
-// outputs has.
+// bf16, which hold 24 bits, and V is exact.  The tensor cores' sums lose up to a
+// unit in each of their steps, always downwards, so theirs are no longer than a
+// chunk (12 steps: states 3.5e-7 off in all, where a part in one accumulator was
+// 2.6e-6); chunks are added in registers.  The masked Q K^T is split into two
+// (2^-17).  The state enters Q S as bf16: an error of 2^-8 of its products, as the
+// rounding of the outputs has.
 //
 // One block of 256 threads walks the chunks of a part, two blocks an SM, so that
-// one's products run beside the other's conversions.  The [Q; K] rows are one
-// operand of 128 rows: with Q alone (64 rows) an MMA takes as long.
+// one's products run beside the other's conversions.  An MMA of 128 x 128 x 16
+// takes 64 cycles, and as long with 64 rows; reading both operands from shared
+// memory is the limit for 128 x 64 x 16 (48 cycles, 32 with one of them in TMEM).
 #include "kda_linear.cuh"
-#include "kda_umma.cuh"
+#include "kda_tma.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kAccO = 0, kAccU = 128;  // TMEM columns; Q K^T comes before U, in its place
+constexpr int kAhead = 2;  // chunks that L2 is ahead of the loads
+// TMEM columns: outputs [d_v][token], the state in bf16 [d_v][d_k / 2], and U
+// [d_v][d_k], before which Q K^T [token][token] has its place.
+constexpr uint32_t kAccO = 0, kState = 64, kAccU = 128;
 
 __device__ __forceinline__ uint64_t dadd(uint64_t d, uint32_t off) { return d + (off >> 4); }
 
@@ -46,11 +52,19 @@ __device__ __forceinline__ bool tiles_ready(bool ok) {
   return all;
 }
 
-template <int PENDING>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+// q, k and v as rows of channels, where they start on 16 bytes.
+struct Maps {
+  CUtensorMap q, k, v;
+};
+// The 64 rows of D channels from `channel` on, in swizzled blocks of 64 channels
+// `block` bytes apart; what lies behind the chunk's tokens comes with them.
+template <int D>
+__device__ __forceinline__ void load_box(uint32_t to, uint32_t block, const CUtensorMap *map, int channel, int row,
+                                         uint64_t *mbar) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+    tma_load2(to + i * block, map, channel + 64 * i, row, umma::smem_u32(mbar));
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // The tokens of chunk q of a segment (chunks end at absolute multiples of 64).
 struct Chunk {
@@ -63,9 +77,14 @@ struct Chunk {
   }
 };
 
-// 64 rows of D channels, in swizzled blocks of 64 channels, by THREADS threads: a
-// thread has 16 bytes of every kStep-th row, always the same, so that it can
-// change what it loaded itself without meeting the others.
+template <int D>
+__device__ __forceinline__ void prefetch_box(const CUtensorMap *map, int channel, int row) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) tma_prefetch2(map, channel + 64 * i, row);
+}
+
+// A thread's share of 64 rows of D channels in such blocks: 16 bytes of every
+// kStep-th row.
 template <int D, int THREADS>
 struct Rows {
   static constexpr int kChunks = D / 8, kStep = THREADS / kChunks, kLoads = 64 / kStep;
@@ -78,87 +97,80 @@ struct Rows {
            e * (kStep / 8) * 1024;
   }
   __device__ __forceinline__ int row_of(int e) const { return row + e * kStep; }
-  // The rows of tokens [begin, begin + n) from `channel` on, zeros behind them.
+  // Rows that the tensor maps do not take, by plain loads; zeros behind the tokens.
   __device__ __forceinline__ void load(unsigned char *sm, uint32_t block, const void *base, int stride,
-                                       int channel, const Chunk &c, bool vec) const {
-    const char *first = static_cast<const char *>(base) + (channel + chunk * 8) * 2 + (long long)c.begin * stride;
-    const char *from = first + (long long)row * stride;
-    unsigned char *to = sm + place(0, block);
-    if (vec) {
-#pragma unroll 4
-      for (int e = 0; e < kLoads; ++e) {
-        const bool live = row_of(e) < c.n;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                     ::"r"(umma::smem_u32(to) + e * (kStep / 8) * 1024), "l"(live ? from : first),
-                     "r"(live ? 16 : 0) : "memory");
-        from += (long long)kStep * stride;
-      }
-    } else {
+                                       int channel, const Chunk &c) const {
 #pragma unroll 1
-      for (int e = 0; e < kLoads; ++e) {
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (row_of(e) < c.n) {
-          const unsigned short *x = reinterpret_cast<const unsigned short *>(from);
+    for (int e = 0; e < kLoads; ++e) {
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (row_of(e) < c.n) {
+        const unsigned short *x =
+            row_at(static_cast<const unsigned short *>(base), c.begin + row_of(e), stride) + channel + chunk * 8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = (uint32_t)x[2 * i] | (uint32_t)x[2 * i + 1] << 16;
-        }
-        *reinterpret_cast<uint4 *>(to + e * (kStep / 8) * 1024) = make_uint4(w[0], w[1], w[2], w[3]);
-        from += (long long)kStep * stride;
+        for (int i = 0; i < 4; ++i) w[i] = (uint32_t)x[2 * i] | (uint32_t)x[2 * i + 1] << 16;
       }
+      *reinterpret_cast<uint4 *>(sm + place(e, block)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+  }
+  // Zeros in the rows from n on.
+  __device__ __forceinline__ void clear(unsigned char *sm, uint32_t block, int n) const {
+#pragma unroll 1
+    for (int e = 0; e < kLoads; ++e)
+      if (row_of(e) >= n) *reinterpret_cast<uint4 *>(sm + place(e, block)) = make_uint4(0, 0, 0, 0);
   }
 };
 
-// Two values as bf16 (rounded), and what the rounding left.
-__device__ __forceinline__ uint32_t peel(f2 &x) {
-  const float2 v = unpack2(x);
-  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
-  const uint32_t r = *reinterpret_cast<const uint32_t *>(&b);
-  x = add2(x, pack2(-__uint_as_float(r << 16), -__uint_as_float(r & 0xffff0000u)));
-  return r;
-}
 __device__ __forceinline__ uint32_t round2(f2 x) {
   const float2 v = unpack2(x);
   const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
   return *reinterpret_cast<const uint32_t *>(&b);
 }
+__device__ __forceinline__ f2 widen2(uint32_t b) {
+  return pack2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+}
+// The first 8 bits of two values as bf16; x keeps the others.
+__device__ __forceinline__ uint32_t peel(f2 &x) {
+  const float2 v = unpack2(x);
+  const uint32_t a = __float_as_uint(v.x), b = __float_as_uint(v.y);
+  x = fma2(pack2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)), both(-1.0f), x);
+  return __byte_perm(a, b, 0x7632);
+}
 
-// Eight keys times w, in three bf16 parts; hi in place.
+// Eight keys times w, in three bf16 parts, which hold its 24 bits; hi in place.
 __device__ __forceinline__ void split3(unsigned char *hi, unsigned char *mid, unsigned char *lo, float w) {
   const uint4 k = *reinterpret_cast<const uint4 *>(hi);
   const uint32_t in[4] = {k.x, k.y, k.z, k.w};
   uint32_t h[4], m[4], l[4];
-  const f2 ww = both(w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f2 x = mul2(pack2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)), ww);
+    f2 x = mul2(widen2(in[i]), both(w));
     h[i] = peel(x);
     m[i] = peel(x);
-    l[i] = round2(x);
+    const float2 v = unpack2(x);
+    l[i] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
   }
   *reinterpret_cast<uint4 *>(hi) = make_uint4(h[0], h[1], h[2], h[3]);
   *reinterpret_cast<uint4 *>(mid) = make_uint4(m[0], m[1], m[2], m[3]);
   *reinterpret_cast<uint4 *>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// What a thread holds of the state: a row (value channel) and NS of its columns
-// (key channels).  d_v = 64: the lanes above 63 repeat the rows and take other
-// columns.
+// What a thread holds of the state: a row (value channel: its lane of TMEM) and
+// half of the columns (key channels).  With d_v = 64 the warps of lanes 64 on hold
+// none.
 template <int DK, int DV>
 struct Frag {
-  static constexpr int NS = DK * DV / kThreads;
-  __device__ __forceinline__ static int row(int warp, int lane) {
-    return DV == 128 ? 32 * (warp & 3) + lane : 32 * (warp & 1) + lane;
+  static constexpr int NS = DK / 2;  // columns
+  __device__ __forceinline__ static bool any(int warp) { return DV == 128 || (warp & 3) < 2; }
+  __device__ __forceinline__ static int row(int warp, int lane) { return 32 * (warp & 3) + lane; }
+  __device__ __forceinline__ static int col(int warp) { return NS * (warp >> 2); }
+  // Float4 f of a thread in a part's state: a warp's are contiguous.
+  __device__ __forceinline__ static int at(int warp, int lane, int f) {
+    const int w = DV == 128 ? warp : (warp & 1) + 2 * (warp >> 2);
+    return (w * (NS / 4) + f) * 32 + lane;
   }
-  __device__ __forceinline__ static int col(int warp) {
-    return NS * (DV == 128 ? warp >> 2 : (warp >> 1 & 1) + 2 * (warp >> 2));
-  }
+  // The warp whose float4s are the w-th.
+  __device__ __forceinline__ static int warp_of(int w) { return DV == 128 ? w : (w & 1) + 4 * (w >> 1); }
 };
-// Float4 f of a thread in a part's state: a warp's are contiguous.
-template <int NS>
-__device__ __forceinline__ int frag_at(int warp, int lane, int f) {
-  return (warp * (NS / 4) + f) * 32 + lane;
-}
 
 // Log decays are summed in fixed point, in units of 2^-44 log 2: exact, and
 // without fp64, which this GPU has little of.  A token's is held within
@@ -210,16 +222,17 @@ template <int DK, int DV>
 struct SumLay {
   static constexpr uint32_t kK = DK * 128, kV = DV * 128;
   static constexpr uint32_t K = 0, V = 2 * kK, MID = V + 2 * kV, LO = MID + kK, MISC = LO + kK;
-  static constexpr uint32_t W = MISC, MBAR = W + 512, TSLOT = MBAR + 8, END = TSLOT + 8;
+  static constexpr uint32_t W = MISC, MBAR = W + 512, TSLOT = MBAR + 24, END = TSLOT + 8;
 };
 
 // U = sum_j e^{G_end - G_j} k_j v_j^T over a part that is not its segment's last,
 // chunk by chunk from the end, so that a chunk's weights need only the decay of
-// those already done; one accumulator, read once.
+// those already done.
 template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, const __grid_constant__ Maps maps) {
   using Lay = SumLay<DK, DV>;
   using F = Frag<DK, DV>;
+  constexpr int NS = F::NS;
   extern __shared__ __align__(1024) unsigned char sm[];
   begin_after_stream();
   const int h = blockIdx.x % p.H, target = blockIdx.x / p.H;
@@ -232,18 +245,34 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p) 
   const int nq = p.part_chunks, q1 = loc.part * nq + nq - 1;
   const uint32_t sb = umma::smem_u32(sm);
   float *w = reinterpret_cast<float *>(sm + Lay::W);
-  uint64_t *mbar = reinterpret_cast<uint64_t *>(sm + Lay::MBAR);
+  uint64_t *mbar = reinterpret_cast<uint64_t *>(sm + Lay::MBAR);  // products, rows of the two stages
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Lay::TSLOT);
   const Rows<DK, kThreads> kr(tid);
   const Rows<DV, kThreads> vr(tid);
 
+  constexpr int kLoadWarp = 7;
+  int asked = -1;  // by the load warp
   auto load = [&](int it) {
-    if (it < nq) {
-      const Chunk c(s, skew, q1 - it);
-      kr.load(sm + Lay::K + (it & 1) * Lay::kK, 8192, p.k, p.ks, h / p.rep * DK, c, p.vec);
-      vr.load(sm + Lay::V + (it & 1) * Lay::kV, 8192, p.v, p.vs, h * DV, c, p.vec);
+    if (it >= nq) return;
+    const Chunk c(s, skew, q1 - it);
+    const uint32_t kt = Lay::K + (it & 1) * Lay::kK, vt = Lay::V + (it & 1) * Lay::kV;
+    if (!p.vec) {
+      kr.load(sm + kt, 8192, p.k, p.ks, h / p.rep * DK, c);
+      vr.load(sm + vt, 8192, p.v, p.vs, h * DV, c);
+    } else if (warp == kLoadWarp) {
+      if (umma::elect_one()) {
+        uint64_t *full = mbar + 1 + (it & 1);
+        mbar_expect_tx(umma::smem_u32(full), Lay::kK + Lay::kV);
+        load_box<DK>(sb + kt, 8192, &maps.k, h / p.rep * DK, c.begin, full);
+        load_box<DV>(sb + vt, 8192, &maps.v, h * DV, c.begin, full);
+        if (it + kAhead < nq) {
+          const int row = Chunk(s, skew, q1 - it - kAhead).begin;
+          prefetch_box<DK>(&maps.k, h / p.rep * DK, row);
+          prefetch_box<DV>(&maps.v, h * DV, row);
+        }
+      }
+      asked = it;
     }
-    copy_commit();
   };
   long long later = 0;
   float nan = 0.0f, g[2] = {0.0f, 0.0f};
@@ -263,10 +292,16 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p) 
     later = min(later, 1LL << 60);
   };
   if (warp == 0) ask(0);
+  if (warp == kLoadWarp) {
+    if (umma::elect_one()) {
+      for (int i = 0; i < 3; ++i) umma::mbar_init(mbar + i, 1);
+      umma::fence_smem_to_async();
+    }
+    __syncwarp();
+  }
   load(0);
   load(1);
   if (warp == 1) umma::tmem_alloc(tslot, 128);
-  if (tid == 0) umma::mbar_init(mbar, 1);
   if (warp == 0) {
     weigh(0);
     ask(1);
@@ -276,26 +311,39 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p) 
   umma::fence_after_sync();
   const uint32_t tmem = *tslot, tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
   bool ok = true;
+  float U[NS];
+#pragma unroll
+  for (int e = 0; e < NS; ++e) U[e] = 0.0f;
+  auto take = [&](int it) {  // the products of chunk it
+    ok = warp_wait(mbar, it & 1, p.spin_limit);
+    if (!ok || !F::any(warp)) return;
+#pragma unroll
+    for (int e = 0; e < NS; e += 32) {
+      float v[32];
+      umma::tmem_ld32(tl + F::col(warp) + e, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) U[e + i] += v[i];
+    }
+  };
   int it = 0;
   for (; it < nq; ++it) {
     // the chunk's rows are there, and those of the chunk before are done with
-    if (it == 0) {
-      copy_wait<1>();
-    } else {
-      copy_wait<0>();
-      ok = warp_wait(mbar, (it - 1) & 1, p.spin_limit);
+    if (it > 0) {
+      take(it - 1);
       if (ok) load(it + 1);
     }
+    if (p.vec) ok = warp_wait(mbar + 1 + (it & 1), (it >> 1) & 1, p.spin_limit) && ok;
+    const int n = Chunk(s, skew, q1 - it).n;
     const uint32_t kt = Lay::K + (it & 1) * Lay::kK, vt = Lay::V + (it & 1) * Lay::kV;
     if (ok) {
+      if (n < 64) {
+        kr.clear(sm + kt, 8192, n);
+        vr.clear(sm + vt, 8192, n);
+      }
 #pragma unroll
       for (int e = 0; e < kr.kLoads; ++e) {
         const uint32_t off = kr.place(e, 8192);
         split3(sm + kt + off, sm + Lay::MID + off, sm + Lay::LO + off, w[(it & 1) * 64 + kr.row_of(e)]);
-      }
-      if (warp == 0 && it + 1 < nq) {
-        weigh(it + 1);
-        ask(it + 2);
       }
     }
     if (!(ok = tiles_ready(ok))) break;
@@ -307,23 +355,26 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p) 
         const uint64_t dk = umma::sdesc_sw128_mn(sb + (part == 0 ? kt : part == 1 ? Lay::MID : Lay::LO), 8192);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma::mma_bf16(tmem, dadd(dv, kk * 2048), dadd(dk, kk * 2048), id, (uint32_t)(it | part | kk));
+          umma::mma_bf16(tmem, dadd(dv, kk * 2048), dadd(dk, kk * 2048), id, (uint32_t)(part | kk));
       }
       umma::commit(mbar);
     }
+    if (warp == 0 && it + 1 < nq) {  // while the products run
+      weigh(it + 1);
+      ask(it + 2);
+    }
   }
-  if (ok) ok = __syncthreads_and(warp_wait(mbar, (nq - 1) & 1, p.spin_limit)) != 0;
+  if (ok) {
+    take(nq - 1);
+    ok = __syncthreads_and(ok) != 0;
+  }
   if (ok) {
     const long long at = (long long)target * p.H + h;
     float4 *dst = reinterpret_cast<float4 *>(p.part_state + at * DK * DV);
+    if (F::any(warp)) {
 #pragma unroll
-    for (int c = 0; c < F::NS; c += 16) {
-      float v[16];
-      umma::tmem_ld16(tl + F::col(warp) + c, v);
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
-        dst[frag_at<F::NS>(warp, lane, c / 4 + f)] =
-            make_float4(v[4 * f], v[4 * f + 1], v[4 * f + 2], v[4 * f + 3]);
+      for (int f = 0; f < NS / 4; ++f)
+        dst[F::at(warp, lane, f)] = make_float4(U[4 * f], U[4 * f + 1], U[4 * f + 2], U[4 * f + 3]);
     }
     if (tid == 0) {
       const float2 a = decay_pair(unfixed(later) * kLn2);
@@ -335,7 +386,9 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p) 
     const int last = min(it, nq) - 1;
     if (last >= 0 && !umma::mbar_wait(mbar, last & 1, kDrainWaitPolls)) set_error(p.seg.err, KDA_DERR_UNSAFE);
   }
-  copy_wait<0>();
+  if (!ok && warp == kLoadWarp)  // and for the loads, before shared memory is
+    for (int i = max(asked - 1, 0); i <= asked; ++i)
+      if (!umma::mbar_wait(mbar + 1 + (i & 1), (i >> 1) & 1, kDrainWaitPolls)) set_error(p.seg.err, KDA_DERR_UNSAFE);
   umma::fence_before_sync();
   __syncthreads();
   if (warp == 1) umma::tmem_dealloc(tmem, 128);
@@ -354,7 +407,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const LinearParams p) {
   SegLoc s;
   if (first + parts > p.max_parts || !locate_segment(p.seg, i, &s)) return;
   const int h = blockIdx.x / (kState4 / kThreads), e = blockIdx.x % (kState4 / kThreads) * kThreads + threadIdx.x;
-  const int lane = e % 32, f = e / 32 % (F::NS / 4), warp = e / 32 / (F::NS / 4);
+  const int lane = e % 32, f = e / 32 % (F::NS / 4), warp = F::warp_of(e / 32 / (F::NS / 4));
   float4 S = *reinterpret_cast<const float4 *>(p.pool + ((long long)s.slot * p.H + h) * DK * DV +
                                                F::row(warp, lane) * DK + F::col(warp) + 4 * f);
   float4 *at = reinterpret_cast<float4 *>(p.part_state) + ((long long)first * p.H + h) * kState4 + e;
@@ -383,31 +436,26 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const LinearParams p) {
 // ----------------------------------------------------------------- outputs
 template <int DK, int DV>
 struct OutLay {
-  static constexpr uint32_t kQK = DK * 256, kV = DV * 128;
-  static constexpr uint32_t kKt = DK * 128;  // a part of K~
-  static constexpr uint32_t kS = DK * DV * 2 > 2 * kKt ? DK * DV * 2 : 2 * kKt;
-  // Rows of outputs on their way out: 16 bytes apart beside their own, so that
-  // lanes with a row each meet no bank twice.
-  static constexpr uint32_t kRow = DV * 2 + 16;
-  // The masked Q K^T: hi in Q's first block, lo in its second or behind the state.
-  static constexpr uint32_t QK = 0, V = 2 * kQK, S = V + kV, P2 = S + kS;
-  static constexpr uint32_t MISC = P2 + (DK == 64 ? 18432 : 0);
-  static_assert(64 * kRow <= (DK == 64 ? 18432 : kQK), "outputs take the place of the weights");
-  static constexpr uint32_t G = MISC, W = G + 512, A = W + 256, MBAR = A + 8, TSLOT = MBAR + 24,
-                            END = TSLOT + 8;
+  static constexpr uint32_t kQK = DK * 256, kV = DV * 128, kKt = DK * 128;  // kKt: a part of K~
+  // The masked Q K^T: hi in Q's first block, lo in its second or in a place of its
+  // own; the outputs come after it, half of the tokens in each.
+  static constexpr uint32_t QK = 0, V = 2 * kQK, MID = V + kV, LO = MID + kKt, P2 = LO + kKt;
+  static constexpr uint32_t MISC = P2 + (DK == 64 ? 8192 : 0);
+  static constexpr uint32_t G = MISC, EG = G + 512, A = EG + 256, MBAR = A + 8, ISSUED = MBAR + 56,
+                            TSLOT = ISSUED + 16, END = TSLOT + 8;
 };
 static_assert(2 * (OutLay<128, 128>::END + 1024) <= 228 * 1024, "two blocks an SM");
 
-// Per chunk: products of q (with k, with the state), then the masked weights P by
-// the warps of lanes 0 to 63 of TMEM, which have the tokens' rows, while the others
-// split K~; then what the chunk adds to the state, P V; then the state and its bf16
-// tile by all, while P V runs, and the outputs by the first.  The others do the loads: q and k a
-// chunk ahead, v as soon as P V is done with the last.
+// Outputs are made as [d_v][token], so that the state, which has a value channel a
+// lane, is an operand from TMEM as soon as it is rounded.  Per chunk: Q K^T and Q S;
+// then the warps of lanes 0 to 63, where Q K^T has the tokens' rows, mask it, the
+// others split K~ and load, all scale Q S; then P V and U, and while U runs the
+// outputs leave; then the state takes U.
 template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) {
+__global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, const __grid_constant__ Maps maps) {
   using Lay = OutLay<DK, DV>;
   using F = Frag<DK, DV>;
-  constexpr int NS = F::NS, kCols = NS < 32 ? 16 : 32;
+  constexpr int NS = F::NS;
   extern __shared__ __align__(1024) unsigned char sm[];
   begin_after_stream();
   const int h = blockIdx.x % p.H, target = blockIdx.x / p.H;
@@ -429,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) 
     set_error(p.seg.err, KDA_DERR_SEGMENT);
     return;
   }
-  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, quad = warp & 3, half = warp >> 2;
-  const int skew = p0 & 63;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int quad = warp & 3, half = warp >> 2, skew = p0 & 63;
   const int chunks = (int)((skew + (long long)s.len + 63) >> 6);
   int q0 = 0, q1 = chunks;
   if (p.part_chunks) {
@@ -439,36 +487,60 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) 
   }
   const uint32_t sb = umma::smem_u32(sm);
   float *G = reinterpret_cast<float *>(sm + Lay::G);  // -G_j: 64 hi, 64 lo
-  float *w = reinterpret_cast<float *>(sm + Lay::W);
+  float *eg = reinterpret_cast<float *>(sm + Lay::EG);
   float2 *whole = reinterpret_cast<float2 *>(sm + Lay::A);
-  uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Lay::MBAR);  // products of q, U, P V
+  uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Lay::MBAR);  // Q K^T, Q S, P V, U
+  uint64_t *full = bar + 4;                                      // q and k (two stages), v
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Lay::TSLOT);
-  const bool tokens = quad < 2;                       // the warps of the tokens' rows
+  const bool tokens = quad < 2;                        // the warps of the tokens' rows
   const int t2 = ((quad & 1) + 2 * half) * 32 + lane;  // thread among the others
   const Rows<DK, 128> kr(t2);
   const Rows<DV, 128> vr(t2);
 
+  constexpr int kLoadWarp = 7;
+  // chunks whose products of q, U and P V, loads of q and k, loads of v were issued last
+  int *issued = reinterpret_cast<int *>(sm + Lay::ISSUED);
   auto load_qk = [&](int q) {
-    if (q < q1) {
-      const Chunk c(s, skew, q);
-      unsigned char *dst = sm + Lay::QK + ((q - q0) & 1) * Lay::kQK;
-      kr.load(dst, 16384, p.q, p.qs, h / p.rep * DK, c, p.vec);
-      kr.load(dst + 8192, 16384, p.k, p.ks, h / p.rep * DK, c, p.vec);
+    if (q >= q1) return;
+    const Chunk c(s, skew, q);
+    const int at = q - q0;
+    const uint32_t to = Lay::QK + (at & 1) * Lay::kQK;
+    if (!p.vec) {
+      if (tokens) return;
+      kr.load(sm + to, 16384, p.q, p.qs, h / p.rep * DK, c);
+      kr.load(sm + to + 8192, 16384, p.k, p.ks, h / p.rep * DK, c);
+    } else if (warp == kLoadWarp) {
+      if (umma::elect_one()) {
+        mbar_expect_tx(umma::smem_u32(full + (at & 1)), Lay::kQK);
+        load_box<DK>(sb + to, 16384, &maps.q, h / p.rep * DK, c.begin, full + (at & 1));
+        load_box<DK>(sb + to + 8192, 16384, &maps.k, h / p.rep * DK, c.begin, full + (at & 1));
+        issued[2] = at;
+        if (q + kAhead < q1) {
+          const int row = Chunk(s, skew, q + kAhead).begin;
+          prefetch_box<DK>(&maps.q, h / p.rep * DK, row);
+          prefetch_box<DK>(&maps.k, h / p.rep * DK, row);
+          prefetch_box<DV>(&maps.v, h * DV, row);
+        }
+      }
     }
-    copy_commit();
   };
   auto load_v = [&](int q) {
-    if (q < q1) {
-      const Chunk c(s, skew, q);
-      vr.load(sm + Lay::V, 8192, p.v, p.vs, h * DV, c, p.vec);
+    if (q >= q1) return;
+    const Chunk c(s, skew, q);
+    if (!p.vec) {
+      if (!tokens) vr.load(sm + Lay::V, 8192, p.v, p.vs, h * DV, c);
+    } else if (warp == kLoadWarp) {
+      if (umma::elect_one()) {
+        mbar_expect_tx(umma::smem_u32(full + 2), Lay::kV);
+        load_box<DV>(sb + Lay::V, 8192, &maps.v, h * DV, c.begin, full + 2);
+        issued[3] = q - q0;
+      }
     }
-    copy_commit();
   };
-  // The decays of the next chunk: asked for, summed and published by the warp
-  // whose part of the weights is all zeros.
+  // The decays of the next chunk: one warp asks for them at the start of a chunk,
+  // sums and publishes them when the chunk's own are done with.
   constexpr int kDecayWarp = 4;
-  float g[2] = {0.0f, 0.0f}, gh[2], gl[2], gw[2];
-  float2 ga;
+  float g[2] = {0.0f, 0.0f};
   auto ask = [&](int q) {
     if (q >= q1) return;
     const Chunk c(s, skew, q);
@@ -479,109 +551,112 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) 
     const ChunkDecay d(g[0], g[1]);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const long long x = -(e ? d.g1 : d.g0);
-      const float hi = __ll2float_rn(x);
-      gh[e] = hi * kUnit + (e ? d.nan1 : d.nan0);
-      gl[e] = unfixed(x - __float2ll_rn(hi));
-      gw[e] = ex2f(unfixed(d.total + x)) + d.nan;
+      const long long x = e ? d.g1 : d.g0;
+      const float hi = __ll2float_rn(-x), nan = e ? d.nan1 : d.nan0;
+      G[2 * lane + e] = hi * kUnit + nan;
+      G[64 + 2 * lane + e] = unfixed(-x - __float2ll_rn(hi));
+      eg[2 * lane + e] = ex2f(unfixed(x)) + nan;
     }
-    ga = decay_pair(unfixed(d.total) * kLn2);
-    ga.x += d.nan;
-  };
-  auto publish = [&]() {
-    *reinterpret_cast<float2 *>(G + 2 * lane) = make_float2(gh[0], gh[1]);
-    *reinterpret_cast<float2 *>(G + 64 + 2 * lane) = make_float2(gl[0], gl[1]);
-    *reinterpret_cast<float2 *>(w + 2 * lane) = make_float2(gw[0], gw[1]);
-    if (lane == 0) *whole = ga;
+    if (lane == 0) {
+      const float2 a = decay_pair(unfixed(d.total) * kLn2);
+      *whole = make_float2(a.x + d.nan, a.y);
+    }
   };
   if (warp == kDecayWarp) ask(q0);
-  if (!tokens) {
-    load_qk(q0);
-    load_v(q0);
+  if (warp == kLoadWarp) {
+    if (umma::elect_one()) {
+      for (int i = 0; i < 7; ++i) umma::mbar_init(bar + i, 1);
+      for (int i = 0; i < 4; ++i) issued[i] = -1;
+      umma::fence_smem_to_async();
+    }
+    __syncwarp();
   }
+  load_qk(q0);
+  load_v(q0);
   if (warp == 1) umma::tmem_alloc(tslot, 256);
-  if (tid == 0)
-    for (int i = 0; i < 3; ++i) umma::mbar_init(bar + i, 1);
   const int row = F::row(warp, lane), col = F::col(warp);
   auto slot_at = [&](int slot) { return p.pool + ((long long)slot * p.H + h) * DK * DV + row * DK + col; };
   f2 S[NS / 2];
-  {
+  if (F::any(warp)) {
     const float4 *src = loc.parts > 1 ? reinterpret_cast<const float4 *>(
                                             p.part_state + ((long long)target * p.H + h) * DK * DV)
                                       : reinterpret_cast<const float4 *>(slot_at(s.slot));
 #pragma unroll
     for (int f = 0; f < NS / 4; ++f) {
-      const float4 v = src[loc.parts > 1 ? frag_at<NS>(warp, lane, f) : f];
+      const float4 v = src[loc.parts > 1 ? F::at(warp, lane, f) : f];
       S[2 * f] = pack2(v.x, v.y);
       S[2 * f + 1] = pack2(v.z, v.w);
     }
   }
   auto store = [&](int slot) {
+    if (!F::any(warp)) return;
     f2 *dst = reinterpret_cast<f2 *>(slot_at(slot));
 #pragma unroll
     for (int f = 0; f < NS / 2; ++f) dst[f] = S[f];
   };
-  auto tile = [&]() {  // the state in bf16, as [d_v][d_k]
-#pragma unroll
-    for (int e = 0; e < NS; e += 8)
-      *reinterpret_cast<uint4 *>(sm + Lay::S + umma::sw128_off16(row, col + e, DV)) = make_uint4(
-          round2(S[e / 2]), round2(S[e / 2 + 1]), round2(S[e / 2 + 2]), round2(S[e / 2 + 3]));
-  };
-  // the next checkpoint, and the segment's tokens after which it is due
-  unsigned due = 0, ckpt = 0;
-  if (p.seg.ckpt_slots) {
-    const unsigned every = p.seg.ckpt_every, done = Chunk(s, skew, q0).begin - s.begin;
-    ckpt = (p0 + done) / every - p0 / every;
-    due = (ckpt + 1) * every - p0 % every;
-  }
-  tile();
-  if (warp == kDecayWarp) {
-    weigh();
-    publish();
-  }
+  if (warp == kDecayWarp) weigh();
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = *tslot, tl = tmem + ((uint32_t)(quad * 32) << 16);
+  auto tile = [&]() {  // the state in bf16
+    if (!F::any(warp)) return;
+    uint32_t b[NS / 2];
+#pragma unroll
+    for (int e = 0; e < NS / 2; ++e) b[e] = round2(S[e]);
+    umma::tmem_st(tl + kState + col / 2, b);
+  };
+  tile();
   bool ok = true;
-  int first = -1, second = -1;  // chunks whose products of q, and U and P V, were issued last
   for (int q = q0; q < q1; ++q) {
     const Chunk c(s, skew, q);
     const uint32_t par = (q - q0) & 1, qk = Lay::QK + par * Lay::kQK, pl = DK == 64 ? Lay::P2 : qk + 16384;
-    copy_wait<1>();  // q and k of this chunk
+    // q and k of this chunk, for those who use them
+    if (p.vec && (!tokens || warp == kDecayWarp))
+      ok = warp_wait(full + par, ((q - q0) >> 1) & 1, p.spin_limit) && ok;
     if (!(ok = tiles_ready(ok))) break;
     if (warp == kDecayWarp) ask(q + 1);
     if (warp == kDecayWarp && umma::elect_one()) {
-      const uint64_t dq = umma::sdesc_sw128(sb + qk), ds = umma::sdesc_sw128(sb + Lay::S);
+      const uint64_t dq = umma::sdesc_sw128(sb + qk);
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) {
         const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
         umma::mma_bf16(tmem + kAccU, dadd(dq, off), dadd(dq, off + 8192), umma::idesc_bf16(128, 64),
                        (uint32_t)kk);
       }
+      umma::commit(bar);
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk)
-        umma::mma_bf16(tmem + kAccO, dadd(dq, (kk >> 2) * 16384 + (kk & 3) * 32),
-                       dadd(ds, (kk >> 2) * (DV * 128) + (kk & 3) * 32), umma::idesc_bf16(128, DV),
-                       (uint32_t)kk);
-      umma::commit(bar);
+        umma::mma_bf16_ts(tmem + kAccO, tmem + kState + kk * 8, dadd(dq, (kk >> 2) * 16384 + (kk & 3) * 32),
+                          umma::idesc_bf16(128, 64), (uint32_t)kk);
+      umma::commit(bar + 1);
+      issued[0] = q - q0;
     }
-    first = q - q0;
-    if (!tokens) load_qk(q + 1);
+    load_qk(q + 1);
     const float2 a = *whole;
     ok = warp_wait(bar, par, p.spin_limit);
-    if (ok && tokens) {
+    if (!tokens && ok) {  // keys: hi in place, mid and lo beside
+      const float th = G[63], tlo = G[127];
+      if (c.n < 64) kr.clear(sm + qk + 8192, 16384, c.n);
+#pragma unroll 2
+      for (int e = 0; e < kr.kLoads; ++e) {
+        const int j = kr.row_of(e);
+        unsigned char *m = sm + Lay::MID + kr.place(e, 8192);
+        split3(sm + qk + 8192 + kr.place(e, 16384), m, m + Lay::kKt, ex2f((G[j] - th) + (G[64 + j] - tlo)));
+      }
+    }
+    ok = warp_wait(bar + 1, par, p.spin_limit) && ok;
+    if (tokens && ok) {
       const int i = 32 * quad + lane;
-      const float ih = -G[i], il = -G[64 + i];
-      if (quad == 0 && half == 1) {  // later tokens only
+      if (warp == kDecayWarp) {  // later tokens only
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t off = umma::sw128_off16(i, 32 + 8 * e, 64);
           *reinterpret_cast<uint4 *>(sm + qk + off) = make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4 *>(sm + pl + off) = make_uint4(0, 0, 0, 0);
         }
-        weigh();
       } else {
+        const float ih = -G[i], il = -G[64 + i];
 #pragma unroll 1
         for (int e = 0; e < 32; e += 16) {
           float x[16];
@@ -608,114 +683,115 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) 
           }
         }
       }
-      const float eg = ex2f(ih + il);
+    }
+    if (ok && F::any(warp)) {  // Q S of 32 tokens, each with its decay
 #pragma unroll 1
-      for (int e = 0; e < DV / 2; e += 32) {
-        const uint32_t at = tl + kAccO + half * (DV / 2) + e;
-        float x[32];
-        umma::tmem_ld32(at, x);
+      for (int e = 32 * half; e < 32 * half + 32; e += 16) {
+        float x[16];
+        umma::tmem_ld16(tl + kAccO + e, x);
+        uint32_t b[16];
 #pragma unroll
-        for (int u = 0; u < 32; u += 2) {
-          const float2 y = unpack2(mul2(pack2(x[u], x[u + 1]), both(eg)));
-          x[u] = y.x;
-          x[u + 1] = y.y;
+        for (int u = 0; u < 16; u += 2) {
+          const float2 d = *reinterpret_cast<const float2 *>(eg + e + u);
+          const float2 v = unpack2(mul2(pack2(x[u], x[u + 1]), pack2(d.x, d.y)));
+          b[u] = __float_as_uint(v.x);
+          b[u + 1] = __float_as_uint(v.y);
         }
-        umma::tmem_st32(at, x);
-      }
-    } else if (ok) {  // keys: hi in place, mid and lo where the state was
-#pragma unroll 2
-      for (int e = 0; e < kr.kLoads; ++e) {
-        unsigned char *m = sm + Lay::S + kr.place(e, 8192);
-        split3(sm + qk + 8192 + kr.place(e, 16384), m, m + Lay::kKt, w[kr.row_of(e)]);
+        umma::tmem_st(tl + kAccO + e, b);
       }
     }
-    copy_wait<1>();  // v of this chunk
+    if (!tokens) {  // v of this chunk
+      if (p.vec) ok = warp_wait(full + 2, par, p.spin_limit) && ok;
+      if (ok && c.n < 64) vr.clear(sm + Lay::V, 8192, c.n);
+    }
     if (!(ok = tiles_ready(ok))) break;
     if (warp == 3 && umma::elect_one()) {
-      const uint64_t dva = umma::sdesc_sw128_mn(sb + Lay::V, DV == 128 ? 8192 : 0);
-      const uint64_t dvb = umma::sdesc_sw128_mn(sb + Lay::V, 8192);
-#pragma unroll
-      for (int part = 0; part < 3; ++part) {
-        const uint64_t dk = part == 0 ? umma::sdesc_sw128_mn(sb + qk + 8192, 16384)
-                                      : umma::sdesc_sw128_mn(sb + Lay::S + (part - 1) * Lay::kKt, 8192);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma::mma_bf16(tmem + kAccU, dadd(dva, kk * 2048), dadd(dk, kk * 2048),
-                         umma::idesc_bf16_abmn(128, DK), (uint32_t)(part | kk));
-      }
-      umma::commit(bar + 1);
+      const uint64_t dv = umma::sdesc_sw128_mn(sb + Lay::V, DV == 128 ? 8192 : 0);
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
         const uint64_t dp = umma::sdesc_sw128(sb + (part ? pl : qk));
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma::mma_bf16(tmem + kAccO, dadd(dp, kk * 32), dadd(dvb, kk * 2048),
-                         umma::idesc_bf16_bmn(128, DV), 1u);
+          umma::mma_bf16(tmem + kAccO, dadd(dv, kk * 2048), dadd(dp, kk * 32), umma::idesc_bf16_amn(128, 64), 1u);
       }
       umma::commit(bar + 2);
-    }
-    second = q - q0;
-    ok = warp_wait(bar + 1, par, p.spin_limit);
-    if (ok) {
-      if (warp == kDecayWarp) publish();
-      const f2 ah = both(a.x), al = both(a.y);
 #pragma unroll
-      for (int e = 0; e < NS; e += kCols) {
-        float u[kCols];
-        if constexpr (kCols == 32) umma::tmem_ld32(tl + kAccU + col + e, u);
-        else umma::tmem_ld16(tl + kAccU + col + e, u);
+      for (int part = 0; part < 3; ++part) {
+        const uint64_t dk = part == 0 ? umma::sdesc_sw128_mn(sb + qk + 8192, 16384)
+                                      : umma::sdesc_sw128_mn(sb + (part == 1 ? Lay::MID : Lay::LO), 8192);
 #pragma unroll
-        for (int x = 0; x < kCols; x += 2)
-          S[(e + x) / 2] = fma2(S[(e + x) / 2], ah, fma2(S[(e + x) / 2], al, pack2(u[x], u[x + 1])));
+        for (int kk = 0; kk < 4; ++kk)
+          umma::mma_bf16(tmem + kAccU, dadd(dv, kk * 2048), dadd(dk, kk * 2048),
+                         umma::idesc_bf16_abmn(128, DK), (uint32_t)(part | kk));
       }
-      tile();
-      if (c.begin - s.begin + c.n == due) {
-        if (ckpt < p.seg.max_ckpt) {
-          const int slot = p.seg.ckpt_slots[(long long)loc.seg * p.seg.max_ckpt + ckpt];
-          if (slot >= p.seg.P) set_error(p.seg.err, KDA_DERR_SLOT);
-          else if (slot >= 0) store(slot);
-        }
-        due += p.seg.ckpt_every;
-        ++ckpt;
-      }
-      ok = warp_wait(bar + 2, par, p.spin_limit);
+      umma::commit(bar + 3);
+      issued[1] = q - q0;
     }
-    if (ok && !tokens) load_v(q + 1);
-    if (ok && tokens) {
-      // a lane has a row; through shared memory the warp stores whole lines
-      unsigned char *stage = sm + (DK == 64 ? Lay::P2 : qk) + 32 * quad * Lay::kRow + half * DV;
+    if (warp == kDecayWarp) weigh();
+    ok = warp_wait(bar + 2, par, p.spin_limit);
+    // the outputs of 32 tokens, gathered by the four warps that have their channels
+    unsigned char *stage = sm + (half ? pl : qk);
+    if (ok && F::any(warp)) {
 #pragma unroll 1
-      for (int e = 0; e < DV / 2; e += 32) {
-        float x[32];
-        umma::tmem_ld32(tl + kAccO + half * (DV / 2) + e, x);
-        uint32_t b[16];
+      for (int e = 0; e < 32; e += 16) {
+        float x[16];
+        umma::tmem_ld16(tl + kAccO + 32 * half + e, x);
+        unsigned char *to = stage + e * (DV * 2) + row * 2;
 #pragma unroll
-        for (int u = 0; u < 16; ++u) b[u] = round2(mul2(pack2(x[2 * u], x[2 * u + 1]), both(p.scale)));
-#pragma unroll
-        for (int u = 0; u < 16; u += 4)
-          *reinterpret_cast<uint4 *>(stage + lane * Lay::kRow + 2 * e + 4 * u) =
-              make_uint4(b[u], b[u + 1], b[u + 2], b[u + 3]);
+        for (int u = 0; u < 16; u += 2) {
+          const uint32_t b = round2(mul2(pack2(x[u], x[u + 1]), both(p.scale)));
+          *reinterpret_cast<unsigned short *>(to + u * (DV * 2)) = (unsigned short)b;
+          *reinterpret_cast<unsigned short *>(to + (u + 1) * (DV * 2)) = (unsigned short)(b >> 16);
+        }
       }
-      __syncwarp();
-      constexpr int kLanes = DV / 16;  // that store a row's half
-      const int at = lane % kLanes * 8;
-      int i = 32 * quad + lane / kLanes;
-      const __nv_bfloat16 *from = reinterpret_cast<const __nv_bfloat16 *>(stage + lane / kLanes * Lay::kRow) + at;
-      __nv_bfloat16 *o = row_at(static_cast<__nv_bfloat16 *>(p.o), c.begin + i, p.os) + h * DV + half * (DV / 2) + at;
-#pragma unroll 4
-      for (int e = 0; e < 32 / (32 / kLanes); ++e) {
-        if (i < c.n) {
+    }
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+    if (ok) {
+      constexpr int kLanes = DV / 8, kStep = 128 / kLanes;  // threads of a row, rows at a time
+      const int t = quad * 32 + lane, at = t % kLanes * 8;
+      int i = t / kLanes;
+      const __nv_bfloat16 *from = reinterpret_cast<const __nv_bfloat16 *>(stage) + i * DV + at;
+      __nv_bfloat16 *o =
+          row_at(static_cast<__nv_bfloat16 *>(p.o), c.begin + 32 * half + i, p.os) + h * DV + at;
+#pragma unroll
+      for (int e = 0; e < 32 / kStep; ++e) {
+        if (32 * half + i < c.n) {
           const uint4 b = *reinterpret_cast<const uint4 *>(from);
           if (p.o_vec) {
             *reinterpret_cast<uint4 *>(o) = b;
           } else {
-#pragma unroll
+#pragma unroll 1
             for (int u = 0; u < 8; ++u) o[u] = from[u];
           }
         }
-        i += 32 / kLanes;
-        from += 32 / kLanes * Lay::kRow / 2;
-        o = row_at(o, 32 / kLanes, p.os);
+        i += kStep;
+        from += kStep * DV;
+        o = row_at(o, kStep, p.os);
+      }
+    }
+    ok = warp_wait(bar + 3, par, p.spin_limit) && ok;
+    if (ok) {
+      load_v(q + 1);
+      if (F::any(warp)) {
+        const f2 ah = both(a.x), al = both(a.y);
+#pragma unroll
+        for (int e = 0; e < NS; e += 16) {
+          float u[16];
+          umma::tmem_ld16(tl + kAccU + col + e, u);
+#pragma unroll
+          for (int x = 0; x < 16; x += 2)
+            S[(e + x) / 2] = fma2(S[(e + x) / 2], ah, fma2(S[(e + x) / 2], al, pack2(u[x], u[x + 1])));
+        }
+      }
+      tile();
+      if (p.seg.ckpt_slots) {  // positions fit 32 bits without a sign
+        const unsigned every = p.seg.ckpt_every, pos = p0 + (c.begin - s.begin) + c.n;
+        const unsigned m = pos / every - p0 / every - 1;
+        if (pos % every == 0 && m < (unsigned)p.seg.max_ckpt) {
+          const int slot = p.seg.ckpt_slots[(long long)loc.seg * p.seg.max_ckpt + m];
+          if (slot >= p.seg.P) set_error(p.seg.err, KDA_DERR_SLOT);
+          else if (slot >= 0) store(slot);
+        }
       }
     }
   }
@@ -724,16 +800,20 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p) 
     if (tid == 0) {
       set_error(p.seg.err, KDA_DERR_TIMEOUT);
       // one more bounded chance for the tensor cores before TMEM is freed
-      for (int i = 0; i < 3; ++i) {
-        const int last = i == 0 ? first : second;
+      for (int i = 0; i < 4; ++i) {
+        const int last = issued[i / 2];
         if (last >= 0 && !umma::mbar_wait(bar + i, last & 1, kDrainWaitPolls))
           set_error(p.seg.err, KDA_DERR_UNSAFE);
       }
+      // and for the loads, before shared memory is
+      for (int i = max(issued[2] - 1, 0); i <= issued[2]; ++i)
+        if (!umma::mbar_wait(full + (i & 1), (i >> 1) & 1, kDrainWaitPolls)) set_error(p.seg.err, KDA_DERR_UNSAFE);
+      if (issued[3] >= 0 && !umma::mbar_wait(full + 2, issued[3] & 1, kDrainWaitPolls))
+        set_error(p.seg.err, KDA_DERR_UNSAFE);
     }
   } else if (loc.part + 1 == loc.parts) {
     store(s.slot);
   }
-  copy_wait<0>();
   umma::fence_before_sync();
   __syncthreads();
   if (warp == 1) umma::tmem_dealloc(tmem, 256);
@@ -747,18 +827,26 @@ cudaError_t allow(K *kernel, size_t bytes) {
 template <int DK, int DV>
 cudaError_t linear_tc(const LinearParams &p, cudaStream_t s) {
   constexpr size_t sum_bytes = SumLay<DK, DV>::END, out_bytes = OutLay<DK, DV>::END;
+  Maps maps = {};
+  cudaError_t e = cudaSuccess;
+  if (p.vec) {
+    const int qk = p.H / p.rep * DK;
+    e = rows_map(&maps.q, p.q, p.seg.N, qk, p.qs);
+    if (e == cudaSuccess) e = rows_map(&maps.k, p.k, p.seg.N, qk, p.ks);
+    if (e == cudaSuccess) e = rows_map(&maps.v, p.v, p.seg.N, p.H * DV, p.vs);
+  }
   // per device, and cheap beside a launch
-  cudaError_t e = allow(out_kernel<DK, DV>, out_bytes);
+  if (e == cudaSuccess) e = allow(out_kernel<DK, DV>, out_bytes);
   if (e != cudaSuccess) return e;
   if (!p.part_chunks)
-    return launch_after(out_kernel<DK, DV>, dim3(p.seg.B * p.H), dim3(kThreads), out_bytes, s, p);
+    return launch_after(out_kernel<DK, DV>, dim3(p.seg.B * p.H), dim3(kThreads), out_bytes, s, p, maps);
   if ((e = allow(sum_kernel<DK, DV>, sum_bytes)) != cudaSuccess) return e;
   const dim3 grid(p.max_parts * p.H);
-  if ((e = launch_after(sum_kernel<DK, DV>, grid, dim3(kThreads), sum_bytes, s, p)) != cudaSuccess) return e;
+  if ((e = launch_after(sum_kernel<DK, DV>, grid, dim3(kThreads), sum_bytes, s, p, maps)) != cudaSuccess) return e;
   if ((e = launch_after(join_kernel<DK, DV>, dim3(p.H * (DK * DV / 4 / kThreads), p.seg.B), dim3(kThreads), 0, s,
                         p)) != cudaSuccess)
     return e;
-  return launch_after(out_kernel<DK, DV>, grid, dim3(kThreads), out_bytes, s, p);
+  return launch_after(out_kernel<DK, DV>, grid, dim3(kThreads), out_bytes, s, p, maps);
 }
 
 constexpr int kBlocks = 2 * 152;  // that the GPU holds

@@ -38,13 +38,10 @@
 // Shared-memory operand tiles are 128-byte swizzled, K-major or, where the
 // same bytes serve a second product transposed, read MN-major (see
 // kda_umma.cuh); the TMEM accumulators sit at fixed columns.
-#include <cuda.h>
-
 #include <cstddef>
-#include <mutex>
 
 #include "kda_internal.cuh"
-#include "kda_umma.cuh"
+#include "kda_tma.cuh"
 
 namespace kda {
 
@@ -343,17 +340,6 @@ __device__ __forceinline__ void prefetch_input_maps(const InputMaps &maps, int t
                  :: "l"(reinterpret_cast<uint64_t>(&maps.q + (tid - 32))) : "memory");
 }
 
-// One TMA load of a 2-D box of `tm` at (x, token) into shared memory,
-// completing its bytes on the mbarrier's transaction count.
-__device__ __forceinline__ void tma_load2(uint32_t dst, const CUtensorMap *tm, int x,
-                                          int tok, uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];"
-      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(tok), "r"(mbar)
-      : "memory");
-}
-
 // One TMA load of a box of `tm` at (x, head, token) into shared memory,
 // completing its bytes on the mbarrier's transaction count.
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *tm, int x,
@@ -364,12 +350,6 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *tm, i
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(head), "r"(tok),
          "r"(mbar) : "memory");
 }
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t mbar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-               :: "r"(mbar), "r"(bytes) : "memory");
-}
-
 
 template <bool RAW>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -1569,27 +1549,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_pass_kernel(const Pref
 }  // namespace
 
 namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
-                                  void *, const cuuint64_t *, const cuuint64_t *,
-                                  const cuuint32_t *, const cuuint32_t *,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled from the driver, looked up once.
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  });
-  return fn;
-}
 
 // [N][H][D] bf16 as a 3-D tensor map with boxes of `box_x` channels x 1 head
 // x 64 tokens, zero fill past N; no swizzle, or (box_x = 64) the 128-byte

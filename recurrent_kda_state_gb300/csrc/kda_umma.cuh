@@ -78,10 +78,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
-// The same with B MN-major (bit 16: B transposed), and with A and B MN-major
-// (bit 15: A transposed).
+// The same with B MN-major (bit 16: B transposed), with A MN-major (bit 15: A
+// transposed), and with both.
 __host__ __device__ constexpr uint32_t idesc_bf16_bmn(int M, int N) {
   return idesc_bf16(M, N) | (1u << 16);
+}
+__host__ __device__ constexpr uint32_t idesc_bf16_amn(int M, int N) {
+  return idesc_bf16(M, N) | (1u << 15);
 }
 __host__ __device__ constexpr uint32_t idesc_bf16_abmn(int M, int N) {
   return idesc_bf16(M, N) | (1u << 15) | (1u << 16);
@@ -95,6 +98,16 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t da,
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
       :: "r"(d_tmem), "l"(da), "l"(db), "r"(idesc), "r"(accumulate));
+}
+
+// The same with A in TMEM: a lane holds a row of A, a column two values of K,
+// the first in the low half.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t db,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_tmem), "l"(db), "r"(idesc), "r"(accumulate));
 }
 
 // Two fp32 values as bf16 pairs hi + lo with hi = rn(x), lo = rn(x - hi):
@@ -310,12 +323,19 @@ __device__ __forceinline__ void tmem_ld16_pair_sum2(uint32_t ta, uint32_t tb, ui
   }
 }
 
-// Registers -> 32 consecutive TMEM columns of this thread's lane, complete on
-// return.
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+// Registers -> 16 or 32 consecutive TMEM columns of this thread's lane, complete
+// on return.
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+         "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+         "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
