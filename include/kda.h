@@ -640,9 +640,9 @@ int kda_linear_prefill(const kda_linear_tokens *tok, kda_state_pool *pool,
 
 /* Bytes of workspace with which kda_linear_prefill splits long segments.  They
  * serve every batch of at most num_tokens tokens and num_seqs segments of these
- * heads, dims and dtype: a server asks once, for its largest batch.  0 when no
- * such batch is split, and on bad arguments (which the prefill call itself
- * rejects). */
+ * heads, dims and dtype: a server asks once, for its largest batch.  0 for
+ * batches too short to split, and on bad arguments (which the prefill call
+ * itself rejects). */
 size_t kda_linear_workspace_size(int32_t num_tokens, int32_t num_seqs,
                                  int32_t num_heads, int32_t d_k, int32_t d_v,
                                  kda_dtype dtype);

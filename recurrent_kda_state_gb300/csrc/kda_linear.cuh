@@ -43,12 +43,32 @@ __device__ __forceinline__ float decayed(float s, float2 a, float add) {
   return fmaf(s, a.x, fmaf(s, a.y, add));
 }
 
+// Log decays are summed in fixed point, in units of 2^-44 log 2: exact, and
+// without fp64, which this GPU has little of.  A token's is held within
+// e^{+-210}, beyond fp32 in both directions, so that 64 of them fit.
+constexpr float kFixed = 17592186044416.0f, kUnit = 1.0f / kFixed;
+__device__ __forceinline__ long long fixed_log2(float g) {
+  g = fminf(fmaxf(g, -210.0f), 210.0f);
+  const float hi = g * kLog2e, lo = fmaf(g, kLog2e, -hi) + g * 1.92596299e-8f;  // log2(e) - kLog2e
+  return __float2ll_rn(hi * kFixed) + __float2ll_rn(lo * kFixed);
+}
+__device__ __forceinline__ float unfixed(long long x) { return __ll2float_rn(x) * kUnit; }
+constexpr long long kMostFixed = 1LL << 60;  // of a part's sum, which is held within it
+
 // Parts of segment i, 0 for one without tokens or with a bad table entry.
 __device__ __forceinline__ int segment_parts(const LinearParams &p, int i) {
   const int b = p.seg.cu[i], e = p.seg.cu[i + 1], p0 = p.seg.start_pos ? p.seg.start_pos[i] : 0;
   if (b < 0 || e <= b || e > p.seg.N || p0 < 0) return 0;
   const int chunks = (int)(((p0 & 63) + (long long)(e - b) + 63) >> 6);
   return (chunks + p.part_chunks - 1) / p.part_chunks;
+}
+// Segments that no part stands for, reported by one block.
+__device__ __forceinline__ void report_segments(const LinearParams &p) {
+  for (int i = threadIdx.x; i < p.seg.B; i += blockDim.x) {
+    const int b = p.seg.cu[i], e = p.seg.cu[i + 1];
+    if (b < 0 || e < b || e > p.seg.N || (p.seg.start_pos && p.seg.start_pos[i] < 0))
+      set_error(p.seg.err, KDA_DERR_SEGMENT);
+  }
 }
 struct PartLoc {
   int seg, part, parts;  // seg < 0: no such part
@@ -106,6 +126,53 @@ struct GateParams {
   float share;  // 1 / d
 };
 
+// The states before the parts of every cut segment, in the place of what the parts
+// add: a thread follows four states of one head, F::plain of them in the pool.
+template <typename F>
+__global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p) {
+  constexpr int kAhead = 8;
+  begin_after_stream();
+  const int state4 = p.DK * p.DV / 4, idx = blockIdx.x * 256 + threadIdx.x, h = idx / state4, e = idx % state4;
+  const int i = blockIdx.y, parts = segment_parts(p, i), first = parts_before(p, i);
+  SegLoc s;
+  if (parts < 2 || first + parts > p.max_parts || !locate_segment(p.seg, i, &s) || h >= p.H) return;
+  float4 S = *reinterpret_cast<const float4 *>(p.pool + ((long long)s.slot * p.H + h) * p.DK * p.DV + F::plain(e));
+  float4 *at = reinterpret_cast<float4 *>(p.part_state) + ((long long)first * p.H + h) * state4 + e;
+  const float2 *decay = p.part_decay + (long long)first * p.H + h;
+  const long long step = (long long)p.H * state4;
+  for (int q = 0; q < parts; q += kAhead) {
+    float4 add[kAhead];
+    float2 a[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (q + u + 1 < parts) {
+        add[u] = at[(q + u) * step];
+        a[u] = decay[(long long)(q + u) * p.H];
+      }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (q + u >= parts) break;
+      at[(q + u) * step] = S;
+      if (q + u + 1 < parts)
+        S = make_float4(decayed(S.x, a[u], add[u].x), decayed(S.y, a[u], add[u].y),
+                        decayed(S.z, a[u], add[u].z), decayed(S.w, a[u], add[u].w));
+    }
+  }
+}
+template <typename F>
+cudaError_t launch_linear_join(const LinearParams &p, cudaStream_t s) {
+  const long long threads = (long long)p.H * p.DK * p.DV / 4;
+  return launch_after(linear_join_kernel<F>, dim3((unsigned)((threads + 255) / 256), p.seg.B), dim3(256), 0, s, p);
+}
+
+// Where chunks run, and how the parts of a batch are chosen: see linear_part_chunks.
+struct LinearCut {
+  int room;   // parts of all heads' that the GPU holds at once
+  int least;  // chunks of a part at least
+  int cost;   // chunks that a part costs beside its own
+};
+LinearCut linear_cut(int dtype, int H, int d_k, int d_v);
+
 cudaError_t launch_linear_walk(const LinearParams &p, kda_dtype dt, bool step, cudaStream_t s);
 // Prompts in bf16 with d_k and d_v of 64 or 128, on the tensor cores.
 cudaError_t launch_linear_tc(const LinearParams &p, cudaStream_t s);
@@ -114,9 +181,9 @@ inline bool linear_uses_tc(int dtype, int d_k, int d_v) {
 }
 // Chunks of a part of a batch (0: it is not split) and the most parts it can
 // have; the most of any batch of at most N tokens and B segments (0: none is split).
-int linear_part_chunks(int N, int B, int H);
-int linear_max_parts(int N, int B, int H);
-size_t linear_workspace_parts(int N, int B, int H);
+int linear_part_chunks(int N, int B, const LinearCut &c);
+int linear_max_parts(int N, int B, const LinearCut &c);
+size_t linear_workspace_parts(int N, int B, const LinearCut &c);
 // Bytes of the parts' decays at the start of the workspace.
 inline size_t linear_decay_bytes(size_t parts, int H) {
   return (parts * H * sizeof(float2) + 255) & ~(size_t)255;

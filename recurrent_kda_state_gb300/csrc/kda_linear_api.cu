@@ -41,8 +41,9 @@ int linear_impl(const kda_linear_tokens *t, kda_state_pool *pool, const int32_t 
   if ((long long)t->num_seqs * t->num_heads > 0x7fffffffLL) return KDA_ESHAPE;
   if (!aligned(ws, 256)) return KDA_EALIGN;
   const bool tc = !step && linear_uses_tc(t->dtype, t->d_k, t->d_v);
-  const int part = tc && ws ? linear_part_chunks(t->num_tokens, t->num_seqs, t->num_heads) : 0;
-  const int parts = part ? linear_max_parts(t->num_tokens, t->num_seqs, t->num_heads) : 0;
+  const LinearCut cut = linear_cut(t->dtype, t->num_heads, t->d_k, t->d_v);
+  const int part = !step && ws ? linear_part_chunks(t->num_tokens, t->num_seqs, cut) : 0;
+  const int parts = part ? linear_max_parts(t->num_tokens, t->num_seqs, cut) : 0;
   if (ws_bytes < linear_workspace_bytes(parts, t->num_heads, t->d_k, t->d_v)) return KDA_ENOSPC;
   if ((long long)parts * t->num_heads > 0x7fffffffLL) return KDA_ESHAPE;
   if (device_refused()) return KDA_EDEVICE;
@@ -97,6 +98,50 @@ int check_out(const void *x, int64_t x_stride, const void *y, int64_t y_stride) 
 
 }  // namespace
 
+namespace kda {
+
+// Two blocks of the tensor cores' kernel on an SM; of the walking one's four to
+// eight, with half of 128 value channels each.
+LinearCut linear_cut(int dtype, int H, int d_k, int d_v) {
+  if (linear_uses_tc(dtype, d_k, d_v)) return {H < 2 * 152 ? 2 * 152 / H : 1, 2, 2};
+  const int blocks = 152 * (d_k == 128 ? 4 : d_k == 64 ? 6 : 8), of_part = H * (d_v > 64 ? 2 : 1);
+  return {of_part < blocks ? blocks / of_part : 1, 1, 1};
+}
+
+constexpr int kMaxSplitSeqs = 1024;
+
+// Parts fill whole waves of blocks.  A segment's last part is half a part on
+// average, and a part has a cost of its own, so the waves that take least are few
+// for few segments; more than kMaxSplitSeqs segments fill the machine alone, and
+// searching them costs more.
+int linear_part_chunks(int N, int B, const LinearCut &c) {
+  if (B > kMaxSplitSeqs) return 0;
+  const int chunks = N / 64 + 1;
+  long long least = 0;
+  int best = 0;
+  for (int waves = 1; waves <= 2 + (B - 1) / c.room; ++waves) {
+    const int parts = waves * c.room - (B - 1) / 2;
+    if (parts < 1) continue;
+    int part = (chunks + parts - 1) / parts;
+    if (part < c.least) part = c.least;
+    const long long cost = (long long)waves * (part + c.cost);
+    if (!best || cost < least) best = part, least = cost;
+  }
+  return (long long)best * 64 < N ? best : 0;
+}
+int linear_max_parts(int N, int B, const LinearCut &c) {
+  return N / (64 * linear_part_chunks(N, B, c)) + 2 * B;
+}
+// At most two waves more than the segments need: parts * 64 * part <= N + 64.
+size_t linear_workspace_parts(int N, int B, const LinearCut &c) {
+  if (N <= 64 * c.least) return 0;
+  const int b = B < kMaxSplitSeqs ? B : kMaxSplitSeqs, most = N / (64 * c.least);
+  const int fill = 2 * c.room + b;
+  return (most < fill ? most : fill) + 2 * b;
+}
+
+}  // namespace kda
+
 extern "C" {
 
 int kda_linear_prefill(const kda_linear_tokens *tok, kda_state_pool *pool,
@@ -111,10 +156,11 @@ size_t kda_linear_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t n
                                  int32_t d_k, int32_t d_v, kda_dtype dtype) {
   if (num_tokens < 0 || num_tokens > kMaxTokens || num_seqs < 1 || num_seqs > kMaxSeqs ||
       !dim_ok(d_k) || !dim_ok(d_v) || !heads_ok(num_heads, d_k > d_v ? d_k : d_v) ||
-      !dtype_ok(dtype) || !linear_uses_tc(dtype, d_k, d_v))
+      !dtype_ok(dtype))
     return 0;
-  return linear_workspace_bytes(linear_workspace_parts(num_tokens, num_seqs, num_heads), num_heads,
-                                d_k, d_v);
+  return linear_workspace_bytes(
+      linear_workspace_parts(num_tokens, num_seqs, linear_cut(dtype, num_heads, d_k, d_v)), num_heads,
+      d_k, d_v);
 }
 
 int kda_linear_step(const kda_linear_tokens *tok, kda_state_pool *pool, const int32_t *state_slots,

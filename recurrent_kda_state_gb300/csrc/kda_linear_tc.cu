@@ -6,7 +6,7 @@
 //
 // Long segments are cut into parts that run at the same time, in three launches:
 // what each part adds to the state (sum_kernel), the states before the parts
-// (join_kernel), the outputs (out_kernel, which alone runs for whole segments).
+// (linear_join_kernel), the outputs (out_kernel, which alone runs for whole segments).
 //
 // Precision.  Decays are summed in fixed point and kept as hi + lo, so that a token
 // that forgets everything costs the later ones nothing.  K~ is split into three
@@ -168,20 +168,12 @@ struct Frag {
     const int w = DV == 128 ? warp : (warp & 1) + 2 * (warp >> 2);
     return (w * (NS / 4) + f) * 32 + lane;
   }
-  // The warp whose float4s are the w-th.
-  __device__ __forceinline__ static int warp_of(int w) { return DV == 128 ? w : (w & 1) + 4 * (w >> 1); }
+  // The place of a part's e-th float4 in a state of the pool.
+  __device__ __forceinline__ static int plain(int e) {
+    const int w = e / 32 / (NS / 4), warp = DV == 128 ? w : (w & 1) + 4 * (w >> 1);
+    return row(warp, e % 32) * DK + col(warp) + 4 * (e / 32 % (NS / 4));
+  }
 };
-
-// Log decays are summed in fixed point, in units of 2^-44 log 2: exact, and
-// without fp64, which this GPU has little of.  A token's is held within
-// e^{+-210}, beyond fp32 in both directions, so that 64 of them fit.
-constexpr float kFixed = 17592186044416.0f, kUnit = 1.0f / kFixed;
-__device__ __forceinline__ long long fixed_log2(float g) {
-  g = fminf(fmaxf(g, -210.0f), 210.0f);
-  const float hi = g * kLog2e, lo = fmaf(g, kLog2e, -hi) + g * 1.92596299e-8f;  // log2(e) - kLog2e
-  return __float2ll_rn(hi * kFixed) + __float2ll_rn(lo * kFixed);
-}
-__device__ __forceinline__ float unfixed(long long x) { return __ll2float_rn(x) * kUnit; }
 
 // Decays of a chunk, for a warp that has the log decays of tokens 2 lane and 2
 // lane + 1 (0 behind the last token): the sums from the first token on.
@@ -288,8 +280,7 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
     nan += d.nan;
     to[0] = ex2f(unfixed(later + (d.total - d.g0))) + nan;
     to[1] = ex2f(unfixed(later + (d.total - d.g1))) + nan;
-    later = max(later + d.total, -(1LL << 60));
-    later = min(later, 1LL << 60);
+    later = min(max(later + d.total, -kMostFixed), kMostFixed);
   };
   if (warp == 0) ask(0);
   if (warp == kLoadWarp) {
@@ -304,7 +295,11 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
   if (warp == 1) umma::tmem_alloc(tslot, 128);
   if (warp == 0) {
     weigh(0);
-    ask(1);
+    if (nq > 1) {
+      ask(1);
+      weigh(1);
+      ask(2);
+    }
   }
   umma::fence_before_sync();
   __syncthreads();
@@ -359,9 +354,11 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
       }
       umma::commit(mbar);
     }
-    if (warp == 0 && it + 1 < nq) {  // while the products run
-      weigh(it + 1);
-      ask(it + 2);
+    // while the products run, the weights in the place of this chunk's, which the
+    // next barrier publishes
+    if (warp == 0 && it + 2 < nq) {
+      weigh(it + 2);
+      ask(it + 3);
     }
   }
   if (ok) {
@@ -394,45 +391,6 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
   if (warp == 1) umma::tmem_dealloc(tmem, 128);
 }
 
-// ------------------------------------------------ states before the parts
-// A thread follows four states of one (segment, head) through the parts.
-template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads) join_kernel(const LinearParams p) {
-  using F = Frag<DK, DV>;
-  constexpr int kState4 = DK * DV / 4, kAhead = 8;
-  begin_after_stream();
-  const int i = blockIdx.y, parts = segment_parts(p, i);
-  if (parts < 2) return;
-  const int first = parts_before(p, i);
-  SegLoc s;
-  if (first + parts > p.max_parts || !locate_segment(p.seg, i, &s)) return;
-  const int h = blockIdx.x / (kState4 / kThreads), e = blockIdx.x % (kState4 / kThreads) * kThreads + threadIdx.x;
-  const int lane = e % 32, f = e / 32 % (F::NS / 4), warp = F::warp_of(e / 32 / (F::NS / 4));
-  float4 S = *reinterpret_cast<const float4 *>(p.pool + ((long long)s.slot * p.H + h) * DK * DV +
-                                               F::row(warp, lane) * DK + F::col(warp) + 4 * f);
-  float4 *at = reinterpret_cast<float4 *>(p.part_state) + ((long long)first * p.H + h) * kState4 + e;
-  const float2 *decay = p.part_decay + (long long)first * p.H + h;
-  const long long step = (long long)p.H * kState4;
-  for (int q = 0; q < parts; q += kAhead) {
-    float4 add[kAhead];
-    float2 a[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (q + u + 1 < parts) {
-        add[u] = at[(q + u) * step];
-        a[u] = decay[(long long)(q + u) * p.H];
-      }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (q + u >= parts) break;
-      at[(q + u) * step] = S;
-      if (q + u + 1 < parts)
-        S = make_float4(decayed(S.x, a[u], add[u].x), decayed(S.y, a[u], add[u].y),
-                        decayed(S.z, a[u], add[u].z), decayed(S.w, a[u], add[u].w));
-    }
-  }
-}
-
 // ----------------------------------------------------------------- outputs
 template <int DK, int DV>
 struct OutLay {
@@ -461,12 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
   const int h = blockIdx.x % p.H, target = blockIdx.x / p.H;
   PartLoc loc = {target, 0, 1};
   if (p.part_chunks) {
-    if (blockIdx.x == 0)  // segments that no part stands for
-      for (int i = threadIdx.x; i < p.seg.B; i += kThreads) {
-        const int b = p.seg.cu[i], e = p.seg.cu[i + 1];
-        if (b < 0 || e < b || e > p.seg.N || (p.seg.start_pos && p.seg.start_pos[i] < 0))
-          set_error(p.seg.err, KDA_DERR_SEGMENT);
-      }
+    if (blockIdx.x == 0) report_segments(p);
     loc = find_part(p, target);
     if (loc.seg < 0) return;
   }
@@ -843,44 +796,11 @@ cudaError_t linear_tc(const LinearParams &p, cudaStream_t s) {
   if ((e = allow(sum_kernel<DK, DV>, sum_bytes)) != cudaSuccess) return e;
   const dim3 grid(p.max_parts * p.H);
   if ((e = launch_after(sum_kernel<DK, DV>, grid, dim3(kThreads), sum_bytes, s, p, maps)) != cudaSuccess) return e;
-  if ((e = launch_after(join_kernel<DK, DV>, dim3(p.H * (DK * DV / 4 / kThreads), p.seg.B), dim3(kThreads), 0, s,
-                        p)) != cudaSuccess)
-    return e;
+  if ((e = launch_linear_join<Frag<DK, DV>>(p, s)) != cudaSuccess) return e;
   return launch_after(out_kernel<DK, DV>, grid, dim3(kThreads), out_bytes, s, p, maps);
 }
 
-constexpr int kBlocks = 2 * 152;  // that the GPU holds
-constexpr int kMinPart = 2, kPartCost = 2;  // chunks of a part
-constexpr int kMaxSplitSeqs = 1024;
-
 }  // namespace
-
-// Parts fill whole waves of blocks.  A segment's last part is half a part on
-// average, and a part costs kPartCost chunks beside its own, so the waves that
-// take least are few for few segments; more than kMaxSplitSeqs segments fill the
-// machine alone, and searching them costs more.
-int linear_part_chunks(int N, int B, int H) {
-  if (B > kMaxSplitSeqs) return 0;
-  const int room = H < kBlocks ? kBlocks / H : 1, chunks = N / 64 + 1;
-  long long least = 0;
-  int best = 0;
-  for (int waves = 1; waves <= 2 + (B - 1) / room; ++waves) {
-    const int parts = waves * room - (B - 1) / 2;
-    if (parts < 1) continue;
-    int part = (chunks + parts - 1) / parts;
-    if (part < kMinPart) part = kMinPart;
-    const long long cost = (long long)waves * (part + kPartCost);
-    if (!best || cost < least) best = part, least = cost;
-  }
-  return (long long)best * 64 < N ? best : 0;
-}
-int linear_max_parts(int N, int B, int H) { return N / (64 * linear_part_chunks(N, B, H)) + 2 * B; }
-
-size_t linear_workspace_parts(int N, int B, int H) {
-  if (N <= 64 * kMinPart || H >= kBlocks) return 0;
-  const int b = B < kMaxSplitSeqs ? B : kMaxSplitSeqs, most = N / (64 * kMinPart), fill = 2 * (kBlocks / H) + b;
-  return (most < fill ? most : fill) + 2 * b;
-}
 
 cudaError_t launch_linear_tc(const LinearParams &p, cudaStream_t s) {
   if (p.DK == 128) return p.DV == 128 ? linear_tc<128, 128>(p, s) : linear_tc<128, 64>(p, s);

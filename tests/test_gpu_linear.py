@@ -118,6 +118,16 @@ def test_prefill_long(dt, workspace):
     linear_case(11, dt, [7, 1900, 0, 450, 64], 2, 128, 128, workspace=workspace)
 
 
+@pytest.mark.parametrize("dt,lens,H,d", [("bf16", [2048], 32, 64), ("bf16", [1500, 1100], 16, 128),
+                                         ("bf16", [700, 9, 400, 300, 64, 500], 24, 64), ("f32", [1500], 16, 32)])
+def test_prefill_fills_the_machine(dt, lens, H, d):
+    """Parts of all heads on every SM at once, the results the same each time."""
+    a, sa = linear_case(19, dt, lens, H, d, d)
+    for _ in range(3):
+        b, sb = linear_case(19, dt, lens, H, d, d)
+        assert torch.equal(a.o, b.o) and torch.equal(sa.data, sb.data)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["strong", "forget", "none"])
 def test_prefill_decays(dt, kind):
