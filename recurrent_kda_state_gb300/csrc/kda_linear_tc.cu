@@ -163,10 +163,13 @@ struct Frag {
   __device__ __forceinline__ static bool any(int warp) { return DV == 128 || (warp & 3) < 2; }
   __device__ __forceinline__ static int row(int warp, int lane) { return 32 * (warp & 3) + lane; }
   __device__ __forceinline__ static int col(int warp) { return NS * (warp >> 2); }
+  // The warp's place among those that hold any.
+  __device__ __forceinline__ static int place(int warp) {
+    return DV == 128 ? warp : (warp & 1) + 2 * (warp >> 2);
+  }
   // Float4 f of a thread in a part's state: a warp's are contiguous.
   __device__ __forceinline__ static int at(int warp, int lane, int f) {
-    const int w = DV == 128 ? warp : (warp & 1) + 2 * (warp >> 2);
-    return (w * (NS / 4) + f) * 32 + lane;
+    return (place(warp) * (NS / 4) + f) * 32 + lane;
   }
   // The place of a part's e-th float4 in a state of the pool.
   __device__ __forceinline__ static int plain(int e) {
@@ -398,7 +401,9 @@ struct OutLay {
   // The masked Q K^T: hi in Q's first block, lo in its second or in a place of its
   // own; the outputs come after it, half of the tokens in each.
   static constexpr uint32_t QK = 0, V = 2 * kQK, MID = V + kV, LO = MID + kKt, P2 = LO + kKt;
-  static constexpr uint32_t MISC = P2 + (DK == 64 ? 8192 : 0);
+  // States on their way between rows in registers and lines in memory: 4 KB a warp,
+  // in the place of K~ where that is large enough.
+  static constexpr uint32_t TURN = DK == 64 ? P2 + 8192 : MID, MISC = DK == 64 ? TURN + 32768 : P2;
   static constexpr uint32_t G = MISC, EG = G + 512, A = EG + 256, MBAR = A + 8, ISSUED = MBAR + 56,
                             TSLOT = ISSUED + 16, END = TSLOT + 8;
 };
@@ -528,25 +533,58 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
   load_v(q0);
   if (warp == 1) umma::tmem_alloc(tslot, 256);
   const int row = F::row(warp, lane), col = F::col(warp);
-  auto slot_at = [&](int slot) { return p.pool + ((long long)slot * p.H + h) * DK * DV + row * DK + col; };
   f2 S[NS / 2];
-  if (F::any(warp)) {
-    const float4 *src = loc.parts > 1 ? reinterpret_cast<const float4 *>(
-                                            p.part_state + ((long long)target * p.H + h) * DK * DV)
-                                      : reinterpret_cast<const float4 *>(slot_at(s.slot));
+  // A state's rows of 32 floats between memory (lines of 128 bytes, four an
+  // instruction) and registers (a row a lane).
+  unsigned char *turn = sm + Lay::TURN + F::place(warp) * 4096;
+  auto line = [&](int r, int c) { return reinterpret_cast<float4 *>(turn + r * 128 + ((c ^ (r & 7)) << 4)); };
+  auto head_at = [&](int slot) {
+    return p.pool + ((long long)slot * p.H + h) * DK * DV + (32 * quad + lane / 8) * DK + col + lane % 8 * 4;
+  };
+  auto store = [&](int slot) {
+    if (!F::any(warp)) return;
+    float *to = head_at(slot);
+#pragma unroll
+    for (int e = 0; e < NS; e += 32) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float2 x = unpack2(S[e / 2 + 2 * c]), y = unpack2(S[e / 2 + 2 * c + 1]);
+        *line(lane, c) = make_float4(x.x, x.y, y.x, y.y);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4 *>(to + 4 * j * DK + e) = *line(4 * j + lane / 8, lane % 8);
+      __syncwarp();
+    }
+  };
+  if (F::any(warp) && loc.parts > 1) {
+    const float4 *src = reinterpret_cast<const float4 *>(p.part_state + ((long long)target * p.H + h) * DK * DV);
 #pragma unroll
     for (int f = 0; f < NS / 4; ++f) {
-      const float4 v = src[loc.parts > 1 ? F::at(warp, lane, f) : f];
+      const float4 v = src[F::at(warp, lane, f)];
       S[2 * f] = pack2(v.x, v.y);
       S[2 * f + 1] = pack2(v.z, v.w);
     }
-  }
-  auto store = [&](int slot) {
-    if (!F::any(warp)) return;
-    f2 *dst = reinterpret_cast<f2 *>(slot_at(slot));
+  } else if (F::any(warp)) {
+    const float *from = head_at(s.slot);
 #pragma unroll
-    for (int f = 0; f < NS / 2; ++f) dst[f] = S[f];
-  };
+    for (int e = 0; e < NS; e += 32) {
+      float4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const float4 *>(from + 4 * j * DK + e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *line(4 * j + lane / 8, lane % 8) = v[j];
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float4 x = *line(lane, c);
+        S[e / 2 + 2 * c] = pack2(x.x, x.y);
+        S[e / 2 + 2 * c + 1] = pack2(x.z, x.w);
+      }
+      __syncwarp();
+    }
+  }
   if (warp == kDecayWarp) weigh();
   umma::fence_before_sync();
   __syncthreads();
