@@ -89,11 +89,11 @@ __global__ void __launch_bounds__(128) linear_walk_kernel(const LinearParams p) 
   begin_after_stream();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % p.H, target = blockIdx.x / p.H;
-  PartLoc loc = {target, 0, 1};
+  PartLoc loc = {target, 0, 1, 0};
   if (KIND != kStep && p.part_chunks) {
     if (KIND == kPrompt && blockIdx.x == 0 && blockIdx.y == 0) report_segments(p);
-    loc = find_part(p, target);
-    if (loc.seg < 0 || (KIND == kSum && loc.part + 1 == loc.parts)) return;
+    loc = find_part<KIND == kPrompt>(p, target);
+    if (loc.seg < 0 || loc.index >= p.max_parts) return;
   }
   const int i = loc.seg;
   SegLoc s;
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(128) linear_walk_kernel(const LinearParams p) 
   f2 S[R][2 * K4];
   {
     const bool ws = KIND != kStep && loc.parts > 1;
-    const float *src = (ws ? p.part_state + ((long long)target * p.H + h) * head_size
+    const float *src = (ws ? p.part_state + ((long long)loc.index * p.H + h) * head_size
                            : p.pool + ((long long)s.slot * p.H + h) * head_size) + at;
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(128) linear_walk_kernel(const LinearParams p) 
     }
   }
   if constexpr (KIND == kSum) {
-    const long long place = (long long)target * p.H + h;
+    const long long place = (long long)loc.index * p.H + h;
     store(p.part_state + place * head_size);
     if (tid == 0 && blockIdx.y == 0) {
       const float2 a = decay_pair(unfixed(sum_g) * kLn2);
@@ -278,7 +278,7 @@ cudaError_t walk(const LinearParams &p, bool step, cudaStream_t s) {
   if (step) return launch_after(linear_walk_kernel<T, DK, kStep>, dim3(p.seg.B * p.H, slices), block, 0, s, p);
   const dim3 grid((p.part_chunks ? p.max_parts : p.seg.B) * p.H, slices);
   if (p.part_chunks) {
-    cudaError_t e = launch_after(linear_walk_kernel<T, DK, kSum>, grid, block, 0, s, p);
+    cudaError_t e = launch_after(linear_walk_kernel<T, DK, kSum>, dim3(p.max_cut * p.H, slices), block, 0, s, p);
     if (e == cudaSuccess) e = launch_linear_join<Plain>(p, s);
     if (e != cudaSuccess) return e;
   }

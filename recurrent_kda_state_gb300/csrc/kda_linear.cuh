@@ -24,6 +24,7 @@ struct LinearParams {
   // whole), parts that the grid and the workspace hold, each part's decay and
   // its state, first what it adds and then the one before it.
   int part_chunks, max_parts;
+  int max_cut;         // the most parts that are not their segment's last
   float2 *part_decay;  // [max_parts][H]
   float *part_state;   // [max_parts][H][d_v * d_k]
   int spin_limit;      // polls of a bounded wait before it gives up
@@ -72,34 +73,33 @@ __device__ __forceinline__ void report_segments(const LinearParams &p) {
 }
 struct PartLoc {
   int seg, part, parts;  // seg < 0: no such part
+  int index;             // among the parts of all segments
 };
-// The segment and place of part `target` of all segments' parts in their
-// order; for a whole warp.
+// The segment and place of part `target` of all segments' parts in their order, or
+// of those that are not their segment's last; for a whole warp.
+template <bool LAST = true>
 __device__ __forceinline__ PartLoc find_part(const LinearParams &p, int target) {
   const int lane = threadIdx.x & 31;
-  int before = 0;
+  int before = 0, index = 0;  // counted parts of the segments before, and all their parts
   for (int base = 0; base < p.seg.B; base += 32) {
-    const int n = base + lane < p.seg.B ? segment_parts(p, base + lane) : 0;
-    int upto = n;
+    const int parts = base + lane < p.seg.B ? segment_parts(p, base + lane) : 0;
+    const int n = LAST ? parts : max(parts - 1, 0);
+    int upto = n, all = parts;
 #pragma unroll
     for (int w = 1; w < 32; w *= 2) {
-      const int o = __shfl_up_sync(0xffffffffu, upto, w);
-      if (lane >= w) upto += o;
+      const int o = __shfl_up_sync(0xffffffffu, upto, w), r = __shfl_up_sync(0xffffffffu, all, w);
+      if (lane >= w) upto += o, all += r;
     }
     const unsigned past = __ballot_sync(0xffffffffu, before + upto > target);
     if (past) {
-      const int l = __ffs(past) - 1, parts = __shfl_sync(0xffffffffu, n, l);
-      return {base + l, target - (before + __shfl_sync(0xffffffffu, upto, l) - parts), parts};
+      const int l = __ffs(past) - 1, its = __shfl_sync(0xffffffffu, parts, l);
+      const int part = target - (before + __shfl_sync(0xffffffffu, upto - n, l));
+      return {base + l, part, its, index + __shfl_sync(0xffffffffu, all, l) - its + part};
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
+    index += __shfl_sync(0xffffffffu, all, 31);
   }
-  return {-1, 0, 0};
-}
-// Parts of the segments before segment i; for a whole warp.
-__device__ __forceinline__ int parts_before(const LinearParams &p, int i) {
-  int n = 0;
-  for (int s = threadIdx.x & 31; s < i; s += 32) n += segment_parts(p, s);
-  return __reduce_add_sync(0xffffffffu, n);
+  return {-1, 0, 0, 0};
 }
 
 struct QkParams {
@@ -127,49 +127,70 @@ struct GateParams {
 };
 
 // The states before the parts of every cut segment, in the place of what the parts
-// add: a thread follows four states of one head, F::plain of them in the pool.
+// add: a thread follows four states of one head, F::plain of them in the pool, for
+// every gridDim.y-th of the cut segments.
 template <typename F>
 __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p) {
   constexpr int kAhead = 8;
   begin_after_stream();
   const int state4 = p.DK * p.DV / 4, idx = blockIdx.x * 256 + threadIdx.x, h = idx / state4, e = idx % state4;
-  const int i = blockIdx.y, parts = segment_parts(p, i), first = parts_before(p, i);
-  SegLoc s;
-  if (parts < 2 || first + parts > p.max_parts || !locate_segment(p.seg, i, &s) || h >= p.H) return;
-  float4 S = *reinterpret_cast<const float4 *>(p.pool + ((long long)s.slot * p.H + h) * p.DK * p.DV + F::plain(e));
-  float4 *at = reinterpret_cast<float4 *>(p.part_state) + ((long long)first * p.H + h) * state4 + e;
-  const float2 *decay = p.part_decay + (long long)first * p.H + h;
+  const int lane = threadIdx.x & 31;
   const long long step = (long long)p.H * state4;
-  for (int q = 0; q < parts; q += kAhead) {
-    float4 add[kAhead];
-    float2 a[kAhead];
+  int index = 0, turn = 0;  // parts of the segments before, cut segments so far
+  for (int base = 0; base < p.seg.B; base += 32) {
+    const int n = base + lane < p.seg.B ? segment_parts(p, base + lane) : 0;
+    int upto = n;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (q + u + 1 < parts) {
-        add[u] = at[(q + u) * step];
-        a[u] = decay[(long long)(q + u) * p.H];
-      }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (q + u >= parts) break;
-      at[(q + u) * step] = S;
-      if (q + u + 1 < parts)
-        S = make_float4(decayed(S.x, a[u], add[u].x), decayed(S.y, a[u], add[u].y),
-                        decayed(S.z, a[u], add[u].z), decayed(S.w, a[u], add[u].w));
+    for (int w = 1; w < 32; w *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, w);
+      if (lane >= w) upto += o;
     }
+    for (unsigned cut = __ballot_sync(0xffffffffu, n > 1); cut; cut &= cut - 1) {
+      const int l = __ffs(cut) - 1, parts = __shfl_sync(0xffffffffu, n, l);
+      const int first = index + __shfl_sync(0xffffffffu, upto, l) - parts;
+      if (turn++ % gridDim.y != blockIdx.y) continue;
+      SegLoc s;
+      if (first + parts > p.max_parts || h >= p.H || !locate_segment(p.seg, base + l, &s)) continue;
+      float4 S =
+          *reinterpret_cast<const float4 *>(p.pool + ((long long)s.slot * p.H + h) * p.DK * p.DV + F::plain(e));
+      float4 *at = reinterpret_cast<float4 *>(p.part_state) + ((long long)first * p.H + h) * state4 + e;
+      const float2 *decay = p.part_decay + (long long)first * p.H + h;
+      for (int q = 0; q < parts; q += kAhead) {
+        float4 add[kAhead];
+        float2 a[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (q + u + 1 < parts) {
+            add[u] = at[(q + u) * step];
+            a[u] = decay[(long long)(q + u) * p.H];
+          }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (q + u >= parts) break;
+          at[(q + u) * step] = S;
+          if (q + u + 1 < parts)
+            S = make_float4(decayed(S.x, a[u], add[u].x), decayed(S.y, a[u], add[u].y),
+                            decayed(S.z, a[u], add[u].z), decayed(S.w, a[u], add[u].w));
+        }
+      }
+      __syncwarp();
+    }
+    index += __shfl_sync(0xffffffffu, upto, 31);
   }
 }
 template <typename F>
 cudaError_t launch_linear_join(const LinearParams &p, cudaStream_t s) {
-  const long long threads = (long long)p.H * p.DK * p.DV / 4;
-  return launch_after(linear_join_kernel<F>, dim3((unsigned)((threads + 255) / 256), p.seg.B), dim3(256), 0, s, p);
+  const long long blocks = ((long long)p.H * p.DK * p.DV / 4 + 255) / 256;
+  const long long rows = 152 * 8 / blocks + 1;  // the machine once, if segments are cut
+  return launch_after(linear_join_kernel<F>, dim3((unsigned)blocks, p.seg.B < rows ? p.seg.B : (int)rows), dim3(256),
+                      0, s, p);
 }
 
-// Where chunks run, and how the parts of a batch are chosen: see linear_part_chunks.
+// Where the chunks of a batch run, for the choice of its parts.
 struct LinearCut {
-  int room;   // parts of all heads' that the GPU holds at once
-  int least;  // chunks of a part at least
-  int cost;   // chunks that a part costs beside its own
+  int blocks, of_part;  // that the GPU holds; that a part takes, with all heads
+  int least;            // chunks of a part at least
+  int room() const { return of_part < blocks ? blocks / of_part : 1; }
 };
 LinearCut linear_cut(int dtype, int H, int d_k, int d_v);
 
@@ -182,7 +203,8 @@ inline bool linear_uses_tc(int dtype, int d_k, int d_v) {
 // Chunks of a part of a batch (0: it is not split) and the most parts it can
 // have; the most of any batch of at most N tokens and B segments (0: none is split).
 int linear_part_chunks(int N, int B, const LinearCut &c);
-int linear_max_parts(int N, int B, const LinearCut &c);
+int linear_max_parts(int N, int B, int part);
+int linear_max_cut(int N, int B, int part);
 size_t linear_workspace_parts(int N, int B, const LinearCut &c);
 // Bytes of the parts' decays at the start of the workspace.
 inline size_t linear_decay_bytes(size_t parts, int H) {

@@ -2,6 +2,7 @@
 // on the host, then launches on the caller's stream.  Nothing is allocated here.
 #include "kda_checks.cuh"
 #include "kda_linear.cuh"
+#include <cmath>
 
 namespace {
 
@@ -43,7 +44,7 @@ int linear_impl(const kda_linear_tokens *t, kda_state_pool *pool, const int32_t 
   const bool tc = !step && linear_uses_tc(t->dtype, t->d_k, t->d_v);
   const LinearCut cut = linear_cut(t->dtype, t->num_heads, t->d_k, t->d_v);
   const int part = !step && ws ? linear_part_chunks(t->num_tokens, t->num_seqs, cut) : 0;
-  const int parts = part ? linear_max_parts(t->num_tokens, t->num_seqs, cut) : 0;
+  const int parts = part ? linear_max_parts(t->num_tokens, t->num_seqs, part) : 0;
   if (ws_bytes < linear_workspace_bytes(parts, t->num_heads, t->d_k, t->d_v)) return KDA_ENOSPC;
   if ((long long)parts * t->num_heads > 0x7fffffffLL) return KDA_ESHAPE;
   if (device_refused()) return KDA_EDEVICE;
@@ -82,6 +83,7 @@ int linear_impl(const kda_linear_tokens *t, kda_state_pool *pool, const int32_t 
   p.o_vec = aligned(t->o, 16) && p.os % 16 == 0;
   p.part_chunks = part;
   p.max_parts = parts;
+  p.max_cut = part ? linear_max_cut(t->num_tokens, t->num_seqs, part) : 0;
   p.part_decay = part ? static_cast<float2 *>(ws) : nullptr;
   p.part_state = part ? reinterpret_cast<float *>(static_cast<unsigned char *>(ws) +
                                                   linear_decay_bytes(parts, p.H))
@@ -103,40 +105,59 @@ namespace kda {
 // Two blocks of the tensor cores' kernel on an SM; of the walking one's four to
 // eight, with half of 128 value channels each.
 LinearCut linear_cut(int dtype, int H, int d_k, int d_v) {
-  if (linear_uses_tc(dtype, d_k, d_v)) return {H < 2 * 152 ? 2 * 152 / H : 1, 2, 2};
-  const int blocks = 152 * (d_k == 128 ? 4 : d_k == 64 ? 6 : 8), of_part = H * (d_v > 64 ? 2 : 1);
-  return {of_part < blocks ? blocks / of_part : 1, 1, 1};
+  if (linear_uses_tc(dtype, d_k, d_v)) return {2 * 152, H, 2};
+  return {152 * (d_k == 128 ? 4 : d_k == 64 ? 6 : 8), H * (d_v > 64 ? 2 : 1), 1};
 }
 
 constexpr int kMaxSplitSeqs = 1024;
 
-// Parts fill whole waves of blocks.  A segment's last part is half a part on
-// average, and a part has a cost of its own, so the waves that take least are few
-// for few segments; more than kMaxSplitSeqs segments fill the machine alone, and
-// searching them costs more.
+// Parts of a batch of B segments, by what it would take in units of a chunk's time.
+// A segment's last part is half a part on average; a part costs kPart beside its
+// chunks; parts that do not fill the machine take as long as one; those that are
+// not a segment's last are gone over before, at kSum a chunk, and joined.  Whole,
+// the longest segment counts, which grows beside the mean with their number (the
+// lengths are on the device: of four whole prompts of 4096 tokens in all, 64 heads
+// of 128 x 64, the longest took 120 us where parts take 145; one that long alone,
+// 32 heads of 128 x 128, 262 and 70).  More than kMaxSplitSeqs segments fill the
+// machine alone, and searching them costs more.
 int linear_part_chunks(int N, int B, const LinearCut &c) {
-  if (B > kMaxSplitSeqs) return 0;
-  const int chunks = N / 64 + 1;
-  long long least = 0;
+  constexpr double kPart = 1.5, kSum = 0.5, kLaunch = 1.0, kLarge = 12.0;
+  if (B > kMaxSplitSeqs || B < 1 || N <= 64 * c.least) return 0;
+  const double chunks = N / 64.0 + 0.5 * B, share = (double)c.of_part / c.blocks;
+  auto time = [&](double parts, double of_part) {
+    const double waves = parts * share;
+    return (waves <= 1.0 ? 1.0 : waves + 0.5) * of_part;
+  };
+  const double longest = std::fmin(chunks, (1.0 + 0.45 * std::log2(B)) * chunks / B);
+  const double even = B * share * (chunks / B + kPart);
+  double least = longest + kPart > even ? longest + kPart : even;
   int best = 0;
-  for (int waves = 1; waves <= 2 + (B - 1) / c.room; ++waves) {
-    const int parts = waves * c.room - (B - 1) / 2;
-    if (parts < 1) continue;
-    int part = (chunks + parts - 1) / parts;
+  const int most = 2 * c.room() + B;  // which the workspace is sized for
+  for (int k = 2; k <= most; k += k / 16 + 1) {
+    int part = (int)(chunks / k) + 1;
     if (part < c.least) part = c.least;
-    const long long cost = (long long)waves * (part + c.cost);
-    if (!best || cost < least) best = part, least = cost;
+    const double cut = chunks / part - 0.5 * B;
+    if (cut > 0.0) {
+      const double t = time(cut + B, part + kPart) + time(cut, kSum * part + 1.0) + kLaunch;
+      if (t < least) best = part, least = t;
+    }
+    if (part == c.least) break;
   }
+  // Better whole: but in a large batch a segment that is far longer than expected is
+  // cut, which costs two nearly empty launches where there is none (37 prompts of
+  // 16384 tokens in six draws: 214 to 403 us whole, 222 to 335 so).
+  if (!best && B > 1 && even >= kLarge) best = (int)(1.2 * std::fmax(longest, even)) + 4;
   return (long long)best * 64 < N ? best : 0;
 }
-int linear_max_parts(int N, int B, const LinearCut &c) {
-  return N / (64 * linear_part_chunks(N, B, c)) + 2 * B;
-}
-// At most two waves more than the segments need: parts * 64 * part <= N + 64.
+// A segment of n tokens that begins inside a chunk touches at most n / 64 + 2 of
+// them, and one more than its first part's are needed for a cut.
+int linear_max_parts(int N, int B, int part) { return N / (64 * part) + 2 * B; }
+int linear_max_cut(int N, int B, int part) { return (N / 64 + B) / part + 1; }
+// linear_part_chunks makes at most 2 room + B parts of a batch's chunks.
 size_t linear_workspace_parts(int N, int B, const LinearCut &c) {
   if (N <= 64 * c.least) return 0;
   const int b = B < kMaxSplitSeqs ? B : kMaxSplitSeqs, most = N / (64 * c.least);
-  const int fill = 2 * c.room + b;
+  const int fill = 2 * c.room() + b;
   return (most < fill ? most : fill) + 2 * b;
 }
 

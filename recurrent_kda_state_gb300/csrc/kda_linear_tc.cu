@@ -230,9 +230,9 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
   constexpr int NS = F::NS;
   extern __shared__ __align__(1024) unsigned char sm[];
   begin_after_stream();
-  const int h = blockIdx.x % p.H, target = blockIdx.x / p.H;
-  const PartLoc loc = find_part(p, target);
-  if (loc.seg < 0 || loc.part + 1 >= loc.parts) return;
+  const int h = blockIdx.x % p.H;
+  const PartLoc loc = find_part<false>(p, blockIdx.x / p.H);
+  if (loc.seg < 0 || loc.index >= p.max_parts) return;
   SegLoc s;
   if (!locate_segment(p.seg, loc.seg, &s)) return;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
     ok = __syncthreads_and(ok) != 0;
   }
   if (ok) {
-    const long long at = (long long)target * p.H + h;
+    const long long at = (long long)loc.index * p.H + h;
     float4 *dst = reinterpret_cast<float4 *>(p.part_state + at * DK * DV);
     if (F::any(warp)) {
 #pragma unroll
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
   extern __shared__ __align__(1024) unsigned char sm[];
   begin_after_stream();
   const int h = blockIdx.x % p.H, target = blockIdx.x / p.H;
-  PartLoc loc = {target, 0, 1};
+  PartLoc loc = {target, 0, 1, 0};
   if (p.part_chunks) {
     if (blockIdx.x == 0) report_segments(p);
     loc = find_part(p, target);
@@ -832,10 +832,9 @@ cudaError_t linear_tc(const LinearParams &p, cudaStream_t s) {
   if (!p.part_chunks)
     return launch_after(out_kernel<DK, DV>, dim3(p.seg.B * p.H), dim3(kThreads), out_bytes, s, p, maps);
   if ((e = allow(sum_kernel<DK, DV>, sum_bytes)) != cudaSuccess) return e;
-  const dim3 grid(p.max_parts * p.H);
-  if ((e = launch_after(sum_kernel<DK, DV>, grid, dim3(kThreads), sum_bytes, s, p, maps)) != cudaSuccess) return e;
+  if ((e = launch_after(sum_kernel<DK, DV>, dim3(p.max_cut * p.H), dim3(kThreads), sum_bytes, s, p, maps)) != cudaSuccess) return e;
   if ((e = launch_linear_join<Frag<DK, DV>>(p, s)) != cudaSuccess) return e;
-  return launch_after(out_kernel<DK, DV>, grid, dim3(kThreads), out_bytes, s, p, maps);
+  return launch_after(out_kernel<DK, DV>, dim3(p.max_parts * p.H), dim3(kThreads), out_bytes, s, p, maps);
 }
 
 }  // namespace

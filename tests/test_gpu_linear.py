@@ -71,7 +71,11 @@ def linear_case(seed, dt, lens, H, dk, dv, Hk=None, kind="mild", fixed=False, vi
     k = rows(rng, n + 3, (Hk, dk), dt, view, dk ** -0.5)[:n]
     v = rows(rng, n + 3, (H, dv), dt, view)[:n]
     g = decays(rng, 1 if fixed else n, H, kind)
-    g = torch.from_numpy(g[0] if fixed else g).float().cuda()
+    if fixed:
+        g = torch.from_numpy(g[0]).float().cuda()
+    else:  # rows with a stride where the others have one
+        g = torch.from_numpy(np.concatenate([g, g], 1)).float().cuda()[:, H:] if view else (
+            torch.from_numpy(g).float().cuda())
     data = torch.from_numpy(rng.standard_normal((P, H, dv, dk))).float().cuda()
     ids = rng.permutation(P)
     slots = ids[:B]
@@ -85,8 +89,9 @@ def linear_case(seed, dt, lens, H, dk, dv, Hk=None, kind="mild", fixed=False, vi
         f64(q), f64(k), f64(v), np.broadcast_to(f64(g), (n, H)), cu, f64(data), slots, scale, dt, tensor,
         commit, ckpt, every, start)
     single = step and (lens == 1).all()
-    wide = torch.full((n + 2, H, dv + 0), 7.0, dtype=DT[dt], device="cuda")
-    batch = K.LinearBatch(q, k, v, g, None if single else i32(cu), scale, wide[:n])
+    wide = torch.full((n + 2, H * dv + view), 7.0, dtype=DT[dt], device="cuda")
+    batch = K.LinearBatch(q, k, v, g, None if single else i32(cu), scale,
+                          wide[:n, view:].unflatten(1, (H, dv)))
     states = K.StatePool(data)
     if step:
         K.kda_linear_step(batch, states, i32(slots), None if commit is None else i32(commit))
@@ -96,7 +101,7 @@ def linear_case(seed, dt, lens, H, dk, dv, Hk=None, kind="mild", fixed=False, vi
                              K.linear_workspace(batch) if workspace else None)
     within(batch.o, want, tol, "o")
     within(states.data, pool, pool_tol, "states")
-    assert (wide[n:] == 7).all()
+    assert (wide[n:] == 7).all() and (wide[:, :view] == 7).all()
     return batch, states
 
 
@@ -276,6 +281,95 @@ def test_same_bits_on_any_stream_and_in_a_graph(dt, n):
         batch.o.zero_()
         graph.replay()
         assert torch.equal(o, batch.o) and torch.equal(s, states.data)
+
+
+def test_two_streams_at_once():
+    """Batches with pools and workspaces of their own, on two streams together."""
+    rng = np.random.default_rng(34)
+    H, d, n = 8, 128, 1500
+    work = []
+    for _ in range(2):
+        q, k, v = (rows(rng, n, (H, d), "bf16") for _ in range(3))
+        g = torch.from_numpy(decays(rng, n, H, "mild")).float().cuda()
+        b = K.LinearBatch(q, k, v, g, i32([0, 1000, n]))
+        work.append((b, K.StatePool.zeros(2, H, d), K.linear_workspace(b)))
+    slots, streams = i32([1, 0]), [torch.cuda.Stream() for _ in range(2)]
+    want = []
+    for b, pool, ws in work:
+        K.kda_linear_prefill(b, pool, slots, workspace=ws)
+        want.append((b.o.clone(), pool.data.clone()))
+    for _ in range(5):
+        for b, pool, ws in work:
+            b.o.zero_()
+            pool.data.zero_()
+        torch.cuda.synchronize()
+        for (b, pool, ws), st in zip(work, streams):
+            K.kda_linear_prefill(b, pool, slots, workspace=ws, stream=st)
+        torch.cuda.synchronize()
+        for (b, pool, ws), (o, states) in zip(work, want):
+            assert torch.equal(b.o, o) and torch.equal(pool.data, states)
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+def test_bounded_waits(workspace):
+    """A wait that gives up is reported, slots stay as they are, and the next call is
+    right."""
+    rng = np.random.default_rng(35)
+    H, d, n = 2, 64, 900
+    q, k, v = (rows(rng, n, (H, d), "bf16") for _ in range(3))
+    batch = K.LinearBatch(q, k, v, torch.full((H,), -0.01, device="cuda"), i32([0, n]))
+    states = K.StatePool(torch.full((2, H, d, d), 0.5, device="cuda"))
+    ws = K.linear_workspace(batch) if workspace else None
+    K.kda_set_wait_limit(0)
+    try:
+        K.kda_linear_prefill(batch, states, i32([1]), workspace=ws)
+        assert K.kda_get_device_error() == K.KDA_DERR_TIMEOUT
+    finally:
+        K.kda_set_wait_limit(-1)
+    assert (states.data == 0.5).all()
+    K.kda_linear_prefill(batch, states, i32([1]), workspace=ws)
+    o, states_1 = batch.o.clone(), states.data.clone()
+    states.data.fill_(0.5)
+    K.kda_linear_prefill(batch, states, i32([1]), workspace=ws)
+    assert torch.equal(o, batch.o) and torch.equal(states.data, states_1)
+
+
+def test_other_sequences_values_stay_out():
+    """A chunk's rows behind a segment's end are its neighbour's: NaN there, and in
+    tokens of no segment, reach nothing."""
+    rng = np.random.default_rng(36)
+    H, d, n = 2, 64, 300
+    for dt in ("bf16", "f32"):
+        q, k, v = (rows(rng, n, (H, d), dt) for _ in range(3))
+        g = torch.from_numpy(decays(rng, n, H, "mild")).float().cuda()
+        cu = [0, 70, 200]
+        clean = K.LinearBatch(q.clone(), k.clone(), v.clone(), g.clone(), i32(cu))
+        for t in (q, k, v, g):
+            t[70:] = float("nan")
+        dirty = K.LinearBatch(q, k, v, g, i32(cu))
+        got = []
+        for b in (clean, dirty):
+            pool = K.StatePool.zeros(2, H, d)
+            K.kda_linear_prefill(b, pool, i32([1, 0]))
+            got.append((b.o[:70].clone(), pool.data[1].clone()))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        assert got[0][0].isfinite().all()
+
+
+def test_a_nan_reaches_what_follows_it():
+    """A decay that is NaN: the tokens from it on, and the state."""
+    rng = np.random.default_rng(37)
+    H, d, n = 2, 64, 200
+    for dt in ("bf16", "f32"):
+        q, k, v = (rows(rng, n, (H, d), dt) for _ in range(3))
+        g = torch.full((n, H), -0.1, device="cuda")
+        g[100, 1] = float("nan")
+        for ws in (True, False):
+            b = K.LinearBatch(q, k, v, g, i32([0, n]))
+            pool = K.StatePool.zeros(1, H, d)
+            K.kda_linear_prefill(b, pool, i32([0]), workspace=K.linear_workspace(b) if ws else None)
+            assert b.o[:, 0].isfinite().all() and b.o[:100].isfinite().all() and b.o[100:, 1].isnan().all()
+            assert pool.data[0, 0].isfinite().all() and pool.data[0, 1].isnan().all()
 
 
 # ------------------------------------------------------------- head norms

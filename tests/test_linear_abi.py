@@ -5,6 +5,7 @@ import ctypes
 import pytest
 import torch
 
+import linear_dispatch
 from recurrent_kda_state_gb300 import kda as K
 from recurrent_kda_state_gb300._build import build_library
 
@@ -75,6 +76,38 @@ def test_linear_tables(L):
     for empty in (tok(num_seqs=0, num_tokens=0), tok(num_tokens=0, q=None, k=None, v=None, o=None)):
         assert call(by(empty), by(p), PTR, None, 0, 0, None, None, 0, None) == K.KDA_OK
         assert L.kda_linear_step(by(empty), by(p), PTR, None, None) == K.KDA_OK
+
+
+@pytest.mark.parametrize("dt,H,dk,dv", [("bf16", 32, 128, 128), ("bf16", 1, 64, 64), ("bf16", 64, 128, 64),
+                                        ("bf16", 500, 64, 64), ("f32", 6, 64, 32), ("f32", 32, 128, 128),
+                                        ("bf16", 3, 16, 16), ("f32", 4000, 16, 128)])
+def test_workspace_of_a_batch_serves_smaller_ones(L, dt, H, dk, dv):
+    """More tokens or more segments never need less, and what a batch is cut into
+    fits."""
+    tokens = [1, 64, 65, 128, 129, 200, 333, 1000, 3000, 4096, 8191, 8192, 16384, 100003, 2 ** 24]
+    seqs = [1, 2, 3, 4, 7, 16, 37, 64, 500, 1024, 1025, 65535]
+    code = {"f32": K.KDA_F32, "bf16": K.KDA_BF16}[dt]
+    size = {(n, b): K.kda_linear_workspace_size(n, b, H, dk, dv, code) for n in tokens for b in seqs}
+    for n, m in zip(tokens, tokens[1:]):
+        assert all(size[n, b] <= size[m, b] for b in seqs)
+    for b, c in zip(seqs, seqs[1:]):
+        assert all(size[n, b] <= size[n, c] for n in tokens)
+    for (n, b), bytes_ in size.items():
+        assert bytes_ >= linear_dispatch.workspace(n, b, dt, H, dk, dv)
+
+
+def test_workspace_too_small(L):
+    n = 8192
+    big = dict(num_tokens=n, num_seqs=1, num_heads=32, num_qk_heads=32, d_k=128, d_v=128, q_stride=4096,
+               k_stride=4096, v_stride=4096, o_stride=4096, g_stride=32)
+    need = linear_dispatch.workspace(n, 1, "bf16", 32, 128, 128)
+    assert need and linear_dispatch.part_chunks(n, 1, "bf16", 32, 128, 128) == 15
+    t, p = tok(**big), pool(num_heads=32, d_k=128, d_v=128)
+    assert L.kda_linear_prefill(by(t), by(p), PTR, None, 0, 0, None, ctypes.c_void_p(0x70000), need - 1,
+                                None) == K.KDA_ENOSPC
+    for bad in ((-1, 1, 4, 64, 64, 1), (8192, 0, 4, 64, 64, 1), (8192, 65536, 4, 64, 64, 1), (8192, 1, 0, 64, 64, 1),
+                (8192, 1, 4, 48, 64, 1), (8192, 1, 4, 64, 256, 1), (8192, 1, 4, 64, 64, 2), (64, 1, 4, 64, 64, 0)):
+        assert K.kda_linear_workspace_size(*bad) == 0
 
 
 def qk(**kw):
