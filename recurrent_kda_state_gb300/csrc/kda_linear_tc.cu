@@ -112,10 +112,10 @@ struct Rows {
       *reinterpret_cast<uint4 *>(sm + place(e, block)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  // Zeros in the rows from n on.
-  __device__ __forceinline__ void clear(unsigned char *sm, uint32_t block, int n) const {
+  // Zeros in the rows from n on, of the thread's first `loads`.
+  __device__ __forceinline__ void clear(unsigned char *sm, uint32_t block, int n, int loads = kLoads) const {
 #pragma unroll 1
-    for (int e = 0; e < kLoads; ++e)
+    for (int e = 0; e < loads; ++e)
       if (row_of(e) >= n) *reinterpret_cast<uint4 *>(sm + place(e, block)) = make_uint4(0, 0, 0, 0);
   }
 };
@@ -222,7 +222,8 @@ struct SumLay {
 
 // U = sum_j e^{G_end - G_j} k_j v_j^T over a part that is not its segment's last,
 // chunk by chunk from the end, so that a chunk's weights need only the decay of
-// those already done.
+// those already done.  Two accumulators: one is read while the next chunk's
+// products run.
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, const __grid_constant__ Maps maps) {
   using Lay = SumLay<DK, DV>;
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
   }
   load(0);
   load(1);
-  if (warp == 1) umma::tmem_alloc(tslot, 128);
+  if (warp == 1) umma::tmem_alloc(tslot, 256);
   if (warp == 0) {
     weigh(0);
     if (nq > 1) {
@@ -312,13 +313,12 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
   float U[NS];
 #pragma unroll
   for (int e = 0; e < NS; ++e) U[e] = 0.0f;
-  auto take = [&](int it) {  // the products of chunk it
-    ok = warp_wait(mbar, it & 1, p.spin_limit);
-    if (!ok || !F::any(warp)) return;
+  auto take = [&](int it) {  // the products of chunk it, which are done
+    if (!F::any(warp)) return;
 #pragma unroll
     for (int e = 0; e < NS; e += 32) {
       float v[32];
-      umma::tmem_ld32(tl + F::col(warp) + e, v);
+      umma::tmem_ld32(tl + (it & 1) * 128 + F::col(warp) + e, v);
 #pragma unroll
       for (int i = 0; i < 32; ++i) U[e + i] += v[i];
     }
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
   for (; it < nq; ++it) {
     // the chunk's rows are there, and those of the chunk before are done with
     if (it > 0) {
-      take(it - 1);
+      ok = warp_wait(mbar, (it - 1) & 1, p.spin_limit);
       if (ok) load(it + 1);
     }
     if (p.vec) ok = warp_wait(mbar + 1 + (it & 1), (it >> 1) & 1, p.spin_limit) && ok;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
         const uint64_t dk = umma::sdesc_sw128_mn(sb + (part == 0 ? kt : part == 1 ? Lay::MID : Lay::LO), 8192);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma::mma_bf16(tmem, dadd(dv, kk * 2048), dadd(dk, kk * 2048), id, (uint32_t)(part | kk));
+          umma::mma_bf16(tmem + (it & 1) * 128, dadd(dv, kk * 2048), dadd(dk, kk * 2048), id, (uint32_t)(part | kk));
       }
       umma::commit(mbar);
     }
@@ -363,9 +363,11 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
       weigh(it + 2);
       ask(it + 3);
     }
+    if (it > 0) take(it - 1);
   }
   if (ok) {
-    take(nq - 1);
+    ok = warp_wait(mbar, (nq - 1) & 1, p.spin_limit);
+    if (ok) take(nq - 1);
     ok = __syncthreads_and(ok) != 0;
   }
   if (ok) {
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
       if (!umma::mbar_wait(mbar + 1 + (i & 1), (i >> 1) & 1, kDrainWaitPolls)) set_error(p.seg.err, KDA_DERR_UNSAFE);
   umma::fence_before_sync();
   __syncthreads();
-  if (warp == 1) umma::tmem_dealloc(tmem, 128);
+  if (warp == 1) umma::tmem_dealloc(tmem, 256);
 }
 
 // ----------------------------------------------------------------- outputs
@@ -626,27 +628,30 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
     load_qk(q + 1);
     const float2 a = *whole;
     ok = warp_wait(bar, par, p.spin_limit);
-    if (!tokens && ok) {  // keys: hi in place, mid and lo beside
-      const float th = G[63], tlo = G[127];
-      if (c.n < 64) kr.clear(sm + qk + 8192, 16384, c.n);
+    // keys: hi in place, mid and lo beside; the last kLoads-th of them by kDecayWarp
+    auto split = [&](int j, uint32_t at, uint32_t block_at) {
+      unsigned char *m = sm + Lay::MID + at;
+      split3(sm + qk + 8192 + block_at, m, m + Lay::kKt, ex2f((G[j] - G[63]) + (G[64 + j] - G[127])));
+    };
+    if (!tokens && ok) {
+      if (c.n < 64) kr.clear(sm + qk + 8192, 16384, c.n, kr.kLoads - 1);
 #pragma unroll 2
-      for (int e = 0; e < kr.kLoads; ++e) {
-        const int j = kr.row_of(e);
-        unsigned char *m = sm + Lay::MID + kr.place(e, 8192);
-        split3(sm + qk + 8192 + kr.place(e, 16384), m, m + Lay::kKt, ex2f((G[j] - th) + (G[64 + j] - tlo)));
+      for (int e = 0; e < kr.kLoads - 1; ++e) split(kr.row_of(e), kr.place(e, 8192), kr.place(e, 16384));
+    }
+    if (warp == kDecayWarp && ok) {
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) {
+        const Rows<DK, 128> r(32 * e + lane);
+        const int last = r.kLoads - 1;
+        if (r.row_of(last) >= c.n)
+          *reinterpret_cast<uint4 *>(sm + qk + 8192 + r.place(last, 16384)) = make_uint4(0, 0, 0, 0);
+        split(r.row_of(last), r.place(last, 8192), r.place(last, 16384));
       }
     }
     ok = warp_wait(bar + 1, par, p.spin_limit) && ok;
     if (tokens && ok) {
       const int i = 32 * quad + lane;
-      if (warp == kDecayWarp) {  // later tokens only
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t off = umma::sw128_off16(i, 32 + 8 * e, 64);
-          *reinterpret_cast<uint4 *>(sm + qk + off) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4 *>(sm + pl + off) = make_uint4(0, 0, 0, 0);
-        }
-      } else {
+      if (warp != kDecayWarp) {  // whose part is zero, and skipped
         const float ih = -G[i], il = -G[64 + i];
 #pragma unroll 1
         for (int e = 0; e < 32; e += 16) {
@@ -702,8 +707,12 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
       for (int part = 0; part < 2; ++part) {
         const uint64_t dp = umma::sdesc_sw128(sb + (part ? pl : qk));
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
+        for (int kk = 0; kk < 2; ++kk)
           umma::mma_bf16(tmem + kAccO, dadd(dv, kk * 2048), dadd(dp, kk * 32), umma::idesc_bf16_amn(128, 64), 1u);
+#pragma unroll
+        for (int kk = 2; kk < 4; ++kk)  // the later half of the tokens, for its own alone
+          umma::mma_bf16(tmem + kAccO + 32, dadd(dv, kk * 2048), dadd(dp, 4096 + kk * 32),
+                         umma::idesc_bf16_amn(128, 32), 1u);
       }
       umma::commit(bar + 2);
 #pragma unroll
@@ -721,19 +730,20 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
     if (warp == kDecayWarp) weigh();
     ok = warp_wait(bar + 2, par, p.spin_limit);
     // the outputs of 32 tokens, gathered by the four warps that have their channels
+    // (16 bytes at a time in places swizzled by the token)
     unsigned char *stage = sm + (half ? pl : qk);
     if (ok && F::any(warp)) {
-#pragma unroll 1
+#pragma unroll
       for (int e = 0; e < 32; e += 16) {
         float x[16];
-        umma::tmem_ld16(tl + kAccO + 32 * half + e, x);
-        unsigned char *to = stage + e * (DV * 2) + row * 2;
+        umma::tmem_ld_rows16(tl + (e << 16) + kAccO + 32 * half, x);
+        uint32_t b[8];
 #pragma unroll
-        for (int u = 0; u < 16; u += 2) {
-          const uint32_t b = round2(mul2(pack2(x[u], x[u + 1]), both(p.scale)));
-          *reinterpret_cast<unsigned short *>(to + u * (DV * 2)) = (unsigned short)b;
-          *reinterpret_cast<unsigned short *>(to + (u + 1) * (DV * 2)) = (unsigned short)(b >> 16);
-        }
+        for (int u = 0; u < 8; ++u) b[u] = round2(mul2(pack2(x[2 * u], x[2 * u + 1]), both(p.scale)));
+        const int tok = 8 * (lane >> 4) + (lane & 7), chunk = 4 * quad + e / 8 + ((lane >> 3) & 1);
+        const uint32_t to = umma::smem_u32(stage) + tok * (DV * 2) + ((chunk ^ (tok & 7)) << 4);
+        umma::stmatrix4_trans(to, b[0], b[1], b[2], b[3]);
+        umma::stmatrix4_trans(to + 16 * (DV * 2), b[4], b[5], b[6], b[7]);
       }
     }
     asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
@@ -741,22 +751,21 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
       constexpr int kLanes = DV / 8, kStep = 128 / kLanes;  // threads of a row, rows at a time
       const int t = quad * 32 + lane, at = t % kLanes * 8;
       int i = t / kLanes;
-      const __nv_bfloat16 *from = reinterpret_cast<const __nv_bfloat16 *>(stage) + i * DV + at;
       __nv_bfloat16 *o =
           row_at(static_cast<__nv_bfloat16 *>(p.o), c.begin + 32 * half + i, p.os) + h * DV + at;
 #pragma unroll
       for (int e = 0; e < 32 / kStep; ++e) {
         if (32 * half + i < c.n) {
-          const uint4 b = *reinterpret_cast<const uint4 *>(from);
+          const __nv_bfloat16 *from =
+              reinterpret_cast<const __nv_bfloat16 *>(stage + i * (DV * 2) + ((t % kLanes ^ (i & 7)) << 4));
           if (p.o_vec) {
-            *reinterpret_cast<uint4 *>(o) = b;
+            *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(from);
           } else {
 #pragma unroll 1
             for (int u = 0; u < 8; ++u) o[u] = from[u];
           }
         }
         i += kStep;
-        from += kStep * DV;
         o = row_at(o, kStep, p.os);
       }
     }
