@@ -117,8 +117,8 @@ constexpr int kMaxSplitSeqs = 1024;
 // not a segment's last are gone over before, at kSum a chunk, and joined.  Whole,
 // the longest segment counts, which grows beside the mean with their number (the
 // lengths are on the device: of four whole prompts of 4096 tokens in all, 64 heads
-// of 128 x 64, the longest took 120 us where parts take 145; one that long alone,
-// 32 heads of 128 x 128, 262 and 70).  More than kMaxSplitSeqs segments fill the
+// of 128 x 64, whole ones took 112 us where parts take 106, and 60 if they are even;
+// one of 4096 alone, 32 heads of 128 x 128, 262 and 70).  More than kMaxSplitSeqs segments fill the
 // machine alone, and searching them costs more.
 int linear_part_chunks(int N, int B, const LinearCut &c) {
   constexpr double kPart = 1.5, kSum = 0.5, kLaunch = 1.0, kLarge = 12.0;

@@ -9,8 +9,8 @@
 // (linear_join_kernel), the outputs (out_kernel, which alone runs for whole segments).
 //
 // Precision.  Decays are summed in fixed point and kept as hi + lo, so that a token
-// that forgets everything costs the later ones nothing.  K~ is split into three
-// bf16, which hold 24 bits, and V is exact.  The tensor cores' sums lose up to a
+// that forgets everything costs the later ones nothing.  K~ (or V, where it is narrower) is split into three
+// bf16, which hold 24 bits, and the other is exact.  The tensor cores' sums lose up to a
 // unit in each of their steps, always downwards, so theirs are no longer than a
 // chunk (12 steps: states 3.5e-7 off in all, where a part in one accumulator was
 // 2.6e-6); chunks are added in registers.  The masked Q K^T is split into two
@@ -28,7 +28,6 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;  // chunks that L2 is ahead of the loads
 // TMEM columns: outputs [d_v][token], the state in bf16 [d_v][d_k / 2], and U
 // [d_v][d_k], before which Q K^T [token][token] has its place.
 constexpr uint32_t kAccO = 0, kState = 64, kAccU = 128;
@@ -76,12 +75,6 @@ struct Chunk {
     n = hi - lo;
   }
 };
-
-template <int D>
-__device__ __forceinline__ void prefetch_box(const CUtensorMap *map, int channel, int row) {
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) tma_prefetch2(map, channel + 64 * i, row);
-}
 
 // A thread's share of 64 rows of D channels in such blocks: 16 bytes of every
 // kStep-th row.
@@ -136,9 +129,10 @@ __device__ __forceinline__ uint32_t peel(f2 &x) {
   return __byte_perm(a, b, 0x7632);
 }
 
-// Eight keys times w, in three bf16 parts, which hold its 24 bits; hi in place.
-__device__ __forceinline__ void split3(unsigned char *hi, unsigned char *mid, unsigned char *lo, float w) {
-  const uint4 k = *reinterpret_cast<const uint4 *>(hi);
+// Eight keys or values times w, in three bf16 parts, which hold its 24 bits.
+__device__ __forceinline__ void split3(const unsigned char *from, unsigned char *hi, unsigned char *mid,
+                                       unsigned char *lo, float w) {
+  const uint4 k = *reinterpret_cast<const uint4 *>(from);
   const uint32_t in[4] = {k.x, k.y, k.z, k.w};
   uint32_t h[4], m[4], l[4];
 #pragma unroll
@@ -153,6 +147,11 @@ __device__ __forceinline__ void split3(unsigned char *hi, unsigned char *mid, un
   *reinterpret_cast<uint4 *>(mid) = make_uint4(m[0], m[1], m[2], m[3]);
   *reinterpret_cast<uint4 *>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
 }
+
+// Which takes the decays e^{G_C - G_j} and is split, keys or values: the narrower
+// (64 heads of 128 x 64, 4096 tokens: 117 us with the keys, 112 with the values).
+template <int DK, int DV>
+constexpr bool kOfValues = DV < DK;
 
 // What a thread holds of the state: a row (value channel: its lane of TMEM) and
 // half of the columns (key channels).  With d_v = 64 the warps of lanes 64 on hold
@@ -215,9 +214,9 @@ __device__ __forceinline__ float log_decay(const LinearParams &p, const Chunk &c
 // ------------------------------------------------------- what a part adds
 template <int DK, int DV>
 struct SumLay {
-  static constexpr uint32_t kK = DK * 128, kV = DV * 128;
-  static constexpr uint32_t K = 0, V = 2 * kK, MID = V + 2 * kV, LO = MID + kK, MISC = LO + kK;
-  static constexpr uint32_t W = MISC, MBAR = W + 512, TSLOT = MBAR + 24, END = TSLOT + 8;
+  static constexpr uint32_t kK = DK * 128, kV = DV * 128, kPart = kOfValues<DK, DV> ? kV : kK;
+  static constexpr uint32_t K = 0, V = 2 * kK, MID = V + 2 * kV, LO = MID + kPart, W = LO + kPart, MBAR = W + 512,
+                            TSLOT = MBAR + 24, END = TSLOT + 8;
 };
 
 // U = sum_j e^{G_end - G_j} k_j v_j^T over a part that is not its segment's last,
@@ -229,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
   using Lay = SumLay<DK, DV>;
   using F = Frag<DK, DV>;
   constexpr int NS = F::NS;
+  constexpr bool kOfV = kOfValues<DK, DV>;
   extern __shared__ __align__(1024) unsigned char sm[];
   begin_after_stream();
   const int h = blockIdx.x % p.H;
@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Lay::TSLOT);
   const Rows<DK, kThreads> kr(tid);
   const Rows<DV, kThreads> vr(tid);
+  const Rows<kOfV ? DV : DK, kThreads> xr(tid);
 
   constexpr int kLoadWarp = 7;
   int asked = -1;  // by the load warp
@@ -261,11 +262,6 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
         mbar_expect_tx(umma::smem_u32(full), Lay::kK + Lay::kV);
         load_box<DK>(sb + kt, 8192, &maps.k, h / p.rep * DK, c.begin, full);
         load_box<DV>(sb + vt, 8192, &maps.v, h * DV, c.begin, full);
-        if (it + kAhead < nq) {
-          const int row = Chunk(s, skew, q1 - it - kAhead).begin;
-          prefetch_box<DK>(&maps.k, h / p.rep * DK, row);
-          prefetch_box<DV>(&maps.v, h * DV, row);
-        }
       }
       asked = it;
     }
@@ -339,18 +335,20 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
         vr.clear(sm + vt, 8192, n);
       }
 #pragma unroll
-      for (int e = 0; e < kr.kLoads; ++e) {
-        const uint32_t off = kr.place(e, 8192);
-        split3(sm + kt + off, sm + Lay::MID + off, sm + Lay::LO + off, w[(it & 1) * 64 + kr.row_of(e)]);
+      for (int e = 0; e < xr.kLoads; ++e) {
+        const uint32_t off = xr.place(e, 8192);
+        unsigned char *x = sm + (kOfV ? vt : kt) + off;
+        split3(x, x, sm + Lay::MID + off, sm + Lay::LO + off, w[(it & 1) * 64 + xr.row_of(e)]);
       }
     }
     if (!(ok = tiles_ready(ok))) break;
     if (warp == 3 && umma::elect_one()) {
-      const uint64_t dv = umma::sdesc_sw128_mn(sb + vt, DV == 128 ? 8192 : 0);
       const uint32_t id = umma::idesc_bf16_abmn(128, DK);
 #pragma unroll
       for (int part = 0; part < 3; ++part) {
-        const uint64_t dk = umma::sdesc_sw128_mn(sb + (part == 0 ? kt : part == 1 ? Lay::MID : Lay::LO), 8192);
+        const uint32_t its = part == 1 ? Lay::MID : Lay::LO;
+        const uint64_t dk = umma::sdesc_sw128_mn(sb + (part == 0 || kOfV ? kt : its), 8192);
+        const uint64_t dv = umma::sdesc_sw128_mn(sb + (part == 0 || !kOfV ? vt : its), DV == 128 ? 8192 : 0);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma::mma_bf16(tmem + (it & 1) * 128, dadd(dv, kk * 2048), dadd(dk, kk * 2048), id, (uint32_t)(part | kk));
@@ -399,13 +397,16 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
 // ----------------------------------------------------------------- outputs
 template <int DK, int DV>
 struct OutLay {
-  static constexpr uint32_t kQK = DK * 256, kV = DV * 128, kKt = DK * 128;  // kKt: a part of K~
+  static constexpr bool kOfV = kOfValues<DK, DV>;
+  static constexpr uint32_t kQK = DK * 256, kV = DV * 128, kPart = kOfV ? kV : DK * 128;  // kPart: of K~ or V~
   // The masked Q K^T: hi in Q's first block, lo in its second or in a place of its
   // own; the outputs come after it, half of the tokens in each.
-  static constexpr uint32_t QK = 0, V = 2 * kQK, MID = V + kV, LO = MID + kKt, P2 = LO + kKt;
+  // K~ has its hi in the place of the keys; V, which P V needs too, stays beside V~.
+  static constexpr uint32_t QK = 0, V = 2 * kQK, HI = V + kV, MID = HI + (kOfV ? kPart : 0), LO = MID + kPart,
+                            P2 = LO + kPart;
   // States on their way between rows in registers and lines in memory: 4 KB a warp,
-  // in the place of K~ where that is large enough.
-  static constexpr uint32_t TURN = DK == 64 ? P2 + 8192 : MID, MISC = DK == 64 ? TURN + 32768 : P2;
+  // in the place of K~ or V~ where that is large enough.
+  static constexpr uint32_t TURN = DK == 64 ? P2 + 8192 : HI, MISC = DK == 64 ? TURN + 32768 : P2;
   static constexpr uint32_t G = MISC, EG = G + 512, A = EG + 256, MBAR = A + 8, ISSUED = MBAR + 56,
                             TSLOT = ISSUED + 16, END = TSLOT + 8;
 };
@@ -421,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
   using Lay = OutLay<DK, DV>;
   using F = Frag<DK, DV>;
   constexpr int NS = F::NS;
+  constexpr bool kOfV = Lay::kOfV;
   extern __shared__ __align__(1024) unsigned char sm[];
   begin_after_stream();
   const int h = blockIdx.x % p.H, target = blockIdx.x / p.H;
@@ -475,12 +477,6 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
         load_box<DK>(sb + to, 16384, &maps.q, h / p.rep * DK, c.begin, full + (at & 1));
         load_box<DK>(sb + to + 8192, 16384, &maps.k, h / p.rep * DK, c.begin, full + (at & 1));
         issued[2] = at;
-        if (q + kAhead < q1) {
-          const int row = Chunk(s, skew, q + kAhead).begin;
-          prefetch_box<DK>(&maps.q, h / p.rep * DK, row);
-          prefetch_box<DK>(&maps.k, h / p.rep * DK, row);
-          prefetch_box<DV>(&maps.v, h * DV, row);
-        }
       }
     }
   };
@@ -628,24 +624,34 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
     load_qk(q + 1);
     const float2 a = *whole;
     ok = warp_wait(bar, par, p.spin_limit);
-    // keys: hi in place, mid and lo beside; the last kLoads-th of them by kDecayWarp
-    auto split = [&](int j, uint32_t at, uint32_t block_at) {
-      unsigned char *m = sm + Lay::MID + at;
-      split3(sm + qk + 8192 + block_at, m, m + Lay::kKt, ex2f((G[j] - G[63]) + (G[64 + j] - G[127])));
+    if (p.vec && kOfV && (!tokens || warp == kDecayWarp)) ok = warp_wait(full + 2, par, p.spin_limit) && ok;
+    // The last kLoads-th of them by kDecayWarp.
+    using Split = Rows<kOfV ? DV : DK, 128>;
+    constexpr uint32_t kBlock = kOfV ? 8192 : 16384;
+    unsigned char *x = sm + (kOfV ? Lay::V : qk + 8192);
+    auto split = [&](const Split &r, int e) {
+      const int j = r.row_of(e);
+      const uint32_t at = r.place(e, 8192);
+      unsigned char *in = x + r.place(e, kBlock), *m = sm + Lay::MID + at;
+      split3(in, kOfV ? sm + Lay::HI + at : in, m, m + Lay::kPart,
+             ex2f((G[j] - G[63]) + (G[64 + j] - G[127])));
     };
     if (!tokens && ok) {
-      if (c.n < 64) kr.clear(sm + qk + 8192, 16384, c.n, kr.kLoads - 1);
+      const Split r(t2);
+      if (c.n < 64) {
+        r.clear(x, kBlock, c.n, r.kLoads - 1);
+        if (kOfV) kr.clear(sm + qk + 8192, 16384, c.n);
+      }
 #pragma unroll 2
-      for (int e = 0; e < kr.kLoads - 1; ++e) split(kr.row_of(e), kr.place(e, 8192), kr.place(e, 16384));
+      for (int e = 0; e < r.kLoads - 1; ++e) split(r, e);
     }
     if (warp == kDecayWarp && ok) {
 #pragma unroll 1
       for (int e = 0; e < 4; ++e) {
-        const Rows<DK, 128> r(32 * e + lane);
+        const Split r(32 * e + lane);
         const int last = r.kLoads - 1;
-        if (r.row_of(last) >= c.n)
-          *reinterpret_cast<uint4 *>(sm + qk + 8192 + r.place(last, 16384)) = make_uint4(0, 0, 0, 0);
-        split(r.row_of(last), r.place(last, 8192), r.place(last, 16384));
+        if (r.row_of(last) >= c.n) *reinterpret_cast<uint4 *>(x + r.place(last, kBlock)) = make_uint4(0, 0, 0, 0);
+        split(r, last);
       }
     }
     ok = warp_wait(bar + 1, par, p.spin_limit) && ok;
@@ -696,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
         umma::tmem_st(tl + kAccO + e, b);
       }
     }
-    if (!tokens) {  // v of this chunk
+    if (!kOfV && !tokens) {  // v of this chunk
       if (p.vec) ok = warp_wait(full + 2, par, p.spin_limit) && ok;
       if (ok && c.n < 64) vr.clear(sm + Lay::V, 8192, c.n);
     }
@@ -717,11 +723,13 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
       umma::commit(bar + 2);
 #pragma unroll
       for (int part = 0; part < 3; ++part) {
-        const uint64_t dk = part == 0 ? umma::sdesc_sw128_mn(sb + qk + 8192, 16384)
-                                      : umma::sdesc_sw128_mn(sb + (part == 1 ? Lay::MID : Lay::LO), 8192);
+        const uint32_t its = part == 0 ? Lay::HI : part == 1 ? Lay::MID : Lay::LO;
+        const uint64_t dk = kOfV || part == 0 ? umma::sdesc_sw128_mn(sb + qk + 8192, 16384)
+                                              : umma::sdesc_sw128_mn(sb + its, 8192);
+        const uint64_t dw = kOfV ? umma::sdesc_sw128_mn(sb + its, DV == 128 ? 8192 : 0) : dv;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma::mma_bf16(tmem + kAccU, dadd(dv, kk * 2048), dadd(dk, kk * 2048),
+          umma::mma_bf16(tmem + kAccU, dadd(dw, kk * 2048), dadd(dk, kk * 2048),
                          umma::idesc_bf16_abmn(128, DK), (uint32_t)(part | kk));
       }
       umma::commit(bar + 3);

@@ -58,12 +58,6 @@ __device__ __forceinline__ void tma_load2(uint32_t dst, const CUtensorMap *tm, i
       : "memory");
 }
 
-// Hint: bring the box into L2.
-__device__ __forceinline__ void tma_prefetch2(const CUtensorMap *tm, int x, int row) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];"
-               :: "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(row) : "memory");
-}
-
 __device__ __forceinline__ void mbar_expect_tx(uint32_t mbar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                :: "r"(mbar), "r"(bytes) : "memory");

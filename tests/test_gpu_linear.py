@@ -154,6 +154,15 @@ def test_prefill_checkpoints(dt, start, every, lens):
     linear_case(16, dt, lens, 2, 64, 64, every=every, max_ckpt=3, start=start)
 
 
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("view", [0, 3, 8])
+@pytest.mark.parametrize("lens,H,Hk,kind", [([1, 70, 0, 64, 300], 4, 1, "mild"), ([2, 1900], 6, 3, "forget"),
+                                            ([517], 2, 1, "strong"), ([1500, 300, 63, 129], 32, 2, "mild")])
+def test_prefill_shared_keys_and_narrow_values(dk, view, lens, H, Hk, kind):
+    linear_case(41, "bf16", lens, H, dk, 64, Hk=Hk, view=view, kind=kind, every=64, max_ckpt=3, start=[5] * len(lens))
+    linear_case(42, "bf16", lens, H, dk, 64, Hk=Hk, view=view, kind=kind, workspace=False, fixed=True)
+
+
 def test_prefill_many_segments():
     lens = np.random.default_rng(17).integers(0, 9, 1500)
     linear_case(17, "bf16", lens, 1, 64, 64)
