@@ -117,8 +117,9 @@ constexpr int kMaxSplitSeqs = 1024;
 // not a segment's last are gone over before, at kSum a chunk, and joined.  Whole,
 // the longest segment counts, which grows beside the mean with their number (the
 // lengths are on the device: of four whole prompts of 4096 tokens in all, 64 heads
-// of 128 x 64, whole ones took 112 us where parts take 106, and 60 if they are even;
-// one of 4096 alone, 32 heads of 128 x 128, 262 and 70).  More than kMaxSplitSeqs segments fill the
+// of 128 x 64, whole ones took 75 us if they were even, 116 with one of 2048 and 163
+// with one of 3000, where parts take 106; one of 4096 alone, 32 heads of 128 x 128,
+// 262 and 70).  More than kMaxSplitSeqs segments fill the
 // machine alone, and searching them costs more.
 int linear_part_chunks(int N, int B, const LinearCut &c) {
   constexpr double kPart = 1.5, kSum = 0.5, kLaunch = 1.0, kLarge = 12.0;
@@ -144,8 +145,9 @@ int linear_part_chunks(int N, int B, const LinearCut &c) {
     if (part == c.least) break;
   }
   // Better whole: but in a large batch a segment that is far longer than expected is
-  // cut, which costs two nearly empty launches where there is none (37 prompts of
-  // 16384 tokens in six draws: 214 to 403 us whole, 222 to 335 so).
+  // cut, which costs 6 to 10 us for two nearly empty launches where there is none (37
+  // prompts of 16384 tokens, the longest 985 to 1519: 201 to 233 us whole, 210 to 241
+  // so; with one of 5000: 326 and 283, of 8000: 493 and 284).
   if (!best && B > 1 && even >= kLarge) best = (int)(1.2 * std::fmax(longest, even)) + 4;
   return (long long)best * 64 < N ? best : 0;
 }

@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
   int q0 = 0, q1 = chunks;
   if (p.part_chunks) {
     q0 = loc.part * p.part_chunks;
-    q1 = min(chunks, q0 + p.part_chunks);
+    if (loc.parts > 1) q1 = min(chunks, q0 + p.part_chunks);
   }
   const uint32_t sb = umma::smem_u32(sm);
   float *G = reinterpret_cast<float *>(sm + Lay::G);  // -G_j: 64 hi, 64 lo
