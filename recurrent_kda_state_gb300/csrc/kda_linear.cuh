@@ -20,10 +20,10 @@ struct LinearParams {
   float *pool;
   int vec;  // q, k, v rows start on 16 bytes
   int o_vec;  // rows of o do
-  // Prompts that are split: chunks of 64 tokens of a part (0: segments are
-  // whole), parts that the grid and the workspace hold, each part's decay and
+  // Prompts that are split: tokens of a chunk (a power of two) and chunks of a part
+  // (0: segments are whole), parts that the grid and the workspace hold, each part's decay and
   // its state, first what it adds and then the one before it.
-  int part_chunks, max_parts;
+  int chunk, part_chunks, max_parts;
   int max_cut;         // the most parts that are not their segment's last
   float2 *part_decay;  // [max_parts][H]
   float *part_state;   // [max_parts][H][d_v * d_k]
@@ -63,7 +63,7 @@ constexpr long long kMostFixed = 1LL << 60;  // of a part's sum, which is held w
 __device__ __forceinline__ int segment_parts(const LinearParams &p, int i) {
   const int b = p.seg.cu[i], e = p.seg.cu[i + 1], p0 = p.seg.start_pos ? p.seg.start_pos[i] : 0;
   if (b < 0 || e <= b || e > p.seg.N || p0 < 0) return 0;
-  const int chunks = (int)(((p0 & 63) + (long long)(e - b) + 63) >> 6);
+  const int chunks = (int)(((p0 & (p.chunk - 1)) + (long long)(e - b) + p.chunk - 1) / p.chunk);
   return 2LL * chunks <= 3LL * p.part_chunks ? 1 : (chunks + p.part_chunks - 1) / p.part_chunks;
 }
 // Segments that no part stands for, reported by one block.
@@ -192,7 +192,7 @@ cudaError_t launch_linear_join(const LinearParams &p, cudaStream_t s) {
 // Where the chunks of a batch run, for the choice of its parts.
 struct LinearCut {
   int blocks, of_part;  // that the GPU holds; that a part takes, with all heads
-  int least;            // chunks of a part at least
+  int chunk, least;     // tokens of a chunk, chunks of a part at least
   int room() const { return of_part < blocks ? blocks / of_part : 1; }
 };
 LinearCut linear_cut(int dtype, int H, int d_k, int d_v);
@@ -206,8 +206,8 @@ inline bool linear_uses_tc(int dtype, int d_k, int d_v) {
 // Chunks of a part of a batch (0: it is not split) and the most parts it can
 // have; the most of any batch of at most N tokens and B segments (0: none is split).
 int linear_part_chunks(int N, int B, const LinearCut &c);
-int linear_max_parts(int N, int B, int part);
-int linear_max_cut(int N, int B, int part);
+int linear_max_parts(int N, int B, int part, const LinearCut &c);
+int linear_max_cut(int N, int B, int part, const LinearCut &c);
 size_t linear_workspace_parts(int N, int B, const LinearCut &c);
 // Bytes of the parts' decays at the start of the workspace.
 inline size_t linear_decay_bytes(size_t parts, int H) {

@@ -44,7 +44,7 @@ int linear_impl(const kda_linear_tokens *t, kda_state_pool *pool, const int32_t 
   const bool tc = !step && linear_uses_tc(t->dtype, t->d_k, t->d_v);
   const LinearCut cut = linear_cut(t->dtype, t->num_heads, t->d_k, t->d_v);
   const int part = !step && ws ? linear_part_chunks(t->num_tokens, t->num_seqs, cut) : 0;
-  const int parts = part ? linear_max_parts(t->num_tokens, t->num_seqs, part) : 0;
+  const int parts = part ? linear_max_parts(t->num_tokens, t->num_seqs, part, cut) : 0;
   if (ws_bytes < linear_workspace_bytes(parts, t->num_heads, t->d_k, t->d_v)) return KDA_ENOSPC;
   if ((long long)parts * t->num_heads > 0x7fffffffLL) return KDA_ESHAPE;
   if (device_refused()) return KDA_EDEVICE;
@@ -81,9 +81,10 @@ int linear_impl(const kda_linear_tokens *t, kda_state_pool *pool, const int32_t 
   p.vec = aligned(t->q, 16) && aligned(t->k, 16) && aligned(t->v, 16) && p.qs % 16 == 0 &&
           p.ks % 16 == 0 && p.vs % 16 == 0;
   p.o_vec = aligned(t->o, 16) && p.os % 16 == 0;
+  p.chunk = cut.chunk;
   p.part_chunks = part;
   p.max_parts = parts;
-  p.max_cut = part ? linear_max_cut(t->num_tokens, t->num_seqs, part) : 0;
+  p.max_cut = part ? linear_max_cut(t->num_tokens, t->num_seqs, part, cut) : 0;
   p.part_decay = part ? static_cast<float2 *>(ws) : nullptr;
   p.part_state = part ? reinterpret_cast<float *>(static_cast<unsigned char *>(ws) +
                                                   linear_decay_bytes(parts, p.H))
@@ -103,32 +104,35 @@ int check_out(const void *x, int64_t x_stride, const void *y, int64_t y_stride) 
 namespace kda {
 
 // Two blocks of the tensor cores' kernel on an SM; of the walking one's four to
-// eight, with half of 128 value channels each.
+// eight, with half of 128 value channels each, whose parts may be short: a token waits
+// for the one before (333 tokens x 6 heads of 64 x 32 in fp32: 28 us in parts of 64
+// tokens, 15 in parts of 16, 14 of 8; 1001 tokens x 2 x 16 x 16 20, 18 and 24).
 LinearCut linear_cut(int dtype, int H, int d_k, int d_v) {
-  if (linear_uses_tc(dtype, d_k, d_v)) return {2 * 152, H, 2};
-  return {152 * (d_k == 128 ? 4 : d_k == 64 ? 6 : 8), H * (d_v > 64 ? 2 : 1), 1};
+  if (linear_uses_tc(dtype, d_k, d_v)) return {2 * 152, H, 64, 2};
+  return {152 * (d_k == 128 ? 4 : d_k == 64 ? 6 : 8), H * (d_v > 64 ? 2 : 1), 16, 1};
 }
 
 constexpr int kMaxSplitSeqs = 1024;
 
-// Parts of a batch of B segments, by what it would take in units of a chunk's time.
+// Parts of a batch of B segments, by what it would take in units of a
+// chunk's time, `of_64` of the time of 64 tokens.
 // A segment's last part is half a part on average; a part costs kPart beside its
 // chunks; parts that do not fill the machine take as long as one; those that are
 // not a segment's last are gone over before, at kSum a chunk, and joined.  Whole,
 // the longest segment counts, which grows beside the mean with their number (the
-// lengths are on the device: of four whole prompts of 4096 tokens in all, 64 heads
-// of 128 x 64, whole ones took 75 us if they were even, 116 with one of 2048 and 163
+// lengths are on the device: four whole prompts of 4096 tokens in all, 64 heads of
+// 128 x 64, took 75 us if they were even, 116 with one of 2048 and 163
 // with one of 3000, where parts take 106; one of 4096 alone, 32 heads of 128 x 128,
 // 262 and 70).  More than kMaxSplitSeqs segments fill the
 // machine alone, and searching them costs more.
 int linear_part_chunks(int N, int B, const LinearCut &c) {
-  constexpr double kPart = 1.5, kSum = 0.5, kLaunch = 1.0, kLarge = 12.0;
-  if (B > kMaxSplitSeqs || B < 1 || N <= 64 * c.least) return 0;
-  const double chunks = N / 64.0 + 0.5 * B, share = (double)c.of_part / c.blocks;
+  if (B > kMaxSplitSeqs || B < 1 || N <= c.chunk * c.least) return 0;
+  const double of_64 = 64.0 / c.chunk, chunks = (double)N / c.chunk + 0.5 * B, share = (double)c.of_part / c.blocks;
   auto time = [&](double parts, double of_part) {
     const double waves = parts * share;
     return (waves <= 1.0 ? 1.0 : waves + 0.5) * of_part;
   };
+  const double kPart = 1.5 * of_64, kSum = 0.5, kLaunch = of_64, kLarge = 12.0 * of_64;
   const double longest = std::fmin(chunks, (1.0 + 0.45 * std::log2(B)) * chunks / B);
   const double even = B * share * (chunks / B + kPart);
   double least = longest + kPart > even ? longest + kPart : even;
@@ -139,7 +143,7 @@ int linear_part_chunks(int N, int B, const LinearCut &c) {
     if (part < c.least) part = c.least;
     const double cut = chunks / part - 0.5 * B;
     if (cut > 0.0) {
-      const double t = time(cut + B, part + kPart) + time(cut, kSum * part + 1.0) + kLaunch;
+      const double t = time(cut + B, part + kPart) + time(cut, kSum * part + of_64) + kLaunch;
       if (t < least) best = part, least = t;
     }
     if (part == c.least) break;
@@ -148,17 +152,17 @@ int linear_part_chunks(int N, int B, const LinearCut &c) {
   // cut, which costs 6 to 10 us for two nearly empty launches where there is none (37
   // prompts of 16384 tokens, the longest 985 to 1519: 201 to 233 us whole, 210 to 241
   // so; with one of 5000: 326 and 283, of 8000: 493 and 284).
-  if (!best && B > 1 && even >= kLarge) best = (int)(1.2 * std::fmax(longest, even)) + 4;
-  return (long long)best * 64 < N ? best : 0;
+  if (!best && B > 1 && even >= kLarge) best = (int)(1.2 * std::fmax(longest, even) + 4 * of_64);
+  return (long long)best * c.chunk < N ? best : 0;
 }
-// A segment of n tokens that begins inside a chunk touches at most n / 64 + 2 of
+// A segment of n tokens that begins inside a chunk touches at most n / chunk + 2 of
 // them, and one more than its first part's are needed for a cut.
-int linear_max_parts(int N, int B, int part) { return N / (64 * part) + 2 * B; }
-int linear_max_cut(int N, int B, int part) { return (N / 64 + B) / part + 1; }
+int linear_max_parts(int N, int B, int part, const LinearCut &c) { return N / (c.chunk * part) + 2 * B; }
+int linear_max_cut(int N, int B, int part, const LinearCut &c) { return (N / c.chunk + B) / part + 1; }
 // linear_part_chunks makes at most 2 room + B parts of a batch's chunks.
 size_t linear_workspace_parts(int N, int B, const LinearCut &c) {
-  if (N <= 64 * c.least) return 0;
-  const int b = B < kMaxSplitSeqs ? B : kMaxSplitSeqs, most = N / (64 * c.least);
+  if (N <= c.chunk * c.least) return 0;
+  const int b = B < kMaxSplitSeqs ? B : kMaxSplitSeqs, most = N / (c.chunk * c.least);
   const int fill = 2 * c.room() + b;
   return (most < fill ? most : fill) + 2 * b;
 }

@@ -106,7 +106,7 @@ def test_workspace_too_small(L):
     assert L.kda_linear_prefill(by(t), by(p), PTR, None, 0, 0, None, ctypes.c_void_p(0x70000), need - 1,
                                 None) == K.KDA_ENOSPC
     for bad in ((-1, 1, 4, 64, 64, 1), (8192, 0, 4, 64, 64, 1), (8192, 65536, 4, 64, 64, 1), (8192, 1, 0, 64, 64, 1),
-                (8192, 1, 4, 48, 64, 1), (8192, 1, 4, 64, 256, 1), (8192, 1, 4, 64, 64, 2), (64, 1, 4, 64, 64, 0)):
+                (8192, 1, 4, 48, 64, 1), (8192, 1, 4, 64, 256, 1), (8192, 1, 4, 64, 64, 2), (16, 1, 4, 64, 64, 0)):
         assert K.kda_linear_workspace_size(*bad) == 0
 
 
