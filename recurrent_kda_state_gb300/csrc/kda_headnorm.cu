@@ -11,7 +11,7 @@
 // kernels were bound by issue slots (70 % busy) and starts, not by memory.  8192
 // tokens of 64 heads of 128 in bf16, rotated: 78 us so, 56 with four heads a group
 // and pairs, 45.4 walking, 90 % of the copy bandwidth.  Gated, 8192 x 32 heads of
-// 128 from fp32 to bf16: 71, 54, 46, with pairs 43.0 (93 %).
+// 128 from fp32 to bf16: 71, 54, 46, with pairs 42.6 (94 %).
 #include "kda_linear.cuh"
 
 namespace kda {

@@ -9,8 +9,12 @@
 // kept one.  Steps are bound by those bytes (8 d_k d_v a row and head); tokens
 // go through shared memory, converted to fp32 once a block.  Blocks of four
 // warps, states marked to leave L2 first: 256 rows of 32 heads of 128 x 128 in
-// 166 us, 97 % of the copy bandwidth (without the marks 186; eight warps 178,
-// two 199).
+// 161 us, the copy bandwidth (without the marks 186; eight warps 178, two 199).
+//
+// Prompts are bound by the chain from token to token (0.1 to 0.2 us each), so long
+// ones are cut into parts of 16 tokens and more: 8192 tokens of 32 heads of 128 x 128
+// in fp32 1280 us, whole 2280; then by fp32 arithmetic, three packed operations a pair
+// of states and token, two without q.
 //
 // e^g is kept as hi + lo.  A state lives through thousands of tokens when g is
 // small, and the 2^-25 by which one fp32 e^g is off is the same every time:
@@ -60,8 +64,7 @@ __device__ __forceinline__ void four(const __nv_bfloat16 *p, f2 &a, f2 &b) {
   b = pack2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
 }
 
-// `count` values (a multiple of 16 bytes) of a token's row into shared memory, the
-// block's e-th 16 bytes of them.
+// 16 bytes of a token's row into shared memory.
 template <typename T>
 __device__ __forceinline__ void stage16(const T *src, T *dst, bool vec) {
   if (vec) {

@@ -114,17 +114,16 @@ LinearCut linear_cut(int dtype, int H, int d_k, int d_v) {
 
 constexpr int kMaxSplitSeqs = 1024;
 
-// Parts of a batch of B segments, by what it would take in units of a
-// chunk's time, `of_64` of the time of 64 tokens.
-// A segment's last part is half a part on average; a part costs kPart beside its
-// chunks; parts that do not fill the machine take as long as one; those that are
-// not a segment's last are gone over before, at kSum a chunk, and joined.  Whole,
-// the longest segment counts, which grows beside the mean with their number (the
-// lengths are on the device: four whole prompts of 4096 tokens in all, 64 heads of
-// 128 x 64, took 75 us if they were even, 116 with one of 2048 and 163
-// with one of 3000, where parts take 106; one of 4096 alone, 32 heads of 128 x 128,
-// 262 and 70).  More than kMaxSplitSeqs segments fill the
-// machine alone, and searching them costs more.
+// Parts of a batch of B segments, by what it would take in units of a chunk's time,
+// `of_64` of the time of 64 tokens.  A segment's last part is half a part on average;
+// a part costs kPart beside its chunks; parts that do not fill the machine take as long
+// as one; those that are not a segment's last are gone over before, at kSum a chunk, and
+// joined.  Whole, the longest segment counts, whose length is on the device alone: for
+// lengths cut at random it is 1 + 1/2 + .. + 1/B times the mean (four prompts of 4096
+// tokens in all, 64 heads of 128 x 64, the longest 1469, 1505, 2172, 3031: whole 88, 93,
+// 126, 167 us, in parts 138, 127, 122, 109; one of 4096 alone, 32 heads of 128 x 128, 262
+// and 70).  More than kMaxSplitSeqs segments fill the machine alone, and searching them
+// costs more.
 int linear_part_chunks(int N, int B, const LinearCut &c) {
   if (B > kMaxSplitSeqs || B < 1 || N <= c.chunk * c.least) return 0;
   const double of_64 = 64.0 / c.chunk, chunks = (double)N / c.chunk + 0.5 * B, share = (double)c.of_part / c.blocks;
@@ -133,7 +132,7 @@ int linear_part_chunks(int N, int B, const LinearCut &c) {
     return (waves <= 1.0 ? 1.0 : waves + 0.5) * of_part;
   };
   const double kPart = 1.5 * of_64, kSum = 0.5, kLaunch = of_64, kLarge = 12.0 * of_64;
-  const double longest = std::fmin(chunks, (1.0 + 0.45 * std::log2(B)) * chunks / B);
+  const double longest = std::fmin(chunks, (1.0 + 0.55 * std::log2(B)) * chunks / B);
   const double even = B * share * (chunks / B + kPart);
   double least = longest + kPart > even ? longest + kPart : even;
   int best = 0;

@@ -22,7 +22,7 @@ def part_chunks(N, B, dt, H, dk, dv):
     def time(parts, of_part):
         waves = parts * share
         return (1.0 if waves <= 1 else waves + 0.5) * of_part
-    longest = min(chunks, (1 + 0.45 * math.log2(B)) * chunks / B)
+    longest = min(chunks, (1 + 0.55 * math.log2(B)) * chunks / B)
     even = B * share * (chunks / B + 1.5 * of_64)
     least, best, k = max(longest + 1.5 * of_64, even), 0, 2
     while k <= 2 * room + B:

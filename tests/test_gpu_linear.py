@@ -365,6 +365,80 @@ def test_other_sequences_values_stay_out():
         assert got[0][0].isfinite().all()
 
 
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("dt,dk,dv", [("bf16", 128, 64), ("bf16", 64, 128), ("bf16", 128, 32), ("f32", 64, 64)])
+def test_tokens_behind_the_last_sequence(dt, dk, dv, workspace):
+    """A padded batch: what lies behind the last segment is not read into anything, and
+    its outputs stay as they were; with room for more segments, empty ones at the end."""
+    rng = np.random.default_rng(38)
+    H, n, last = 4, 1100, 1000
+    q, v = rows(rng, n, (H, dk), dt), rows(rng, n, (H, dv), dt)
+    k = rows(rng, n, (H, dk), dt, std=dk ** -0.5)
+    g = torch.from_numpy(decays(rng, n, H, "mild")).float().cuda()
+    first = torch.from_numpy(rng.standard_normal((5, H, dv, dk))).float().cuda()
+
+    def call(cu, slots, step):
+        b = K.LinearBatch(q, k, v, g, i32(cu), o=torch.full((n, H, dv), MARK, dtype=DT[dt], device="cuda"))
+        pool = K.StatePool(first.clone())
+        if step:
+            K.kda_linear_step(b, pool, i32(slots))
+        else:
+            K.kda_linear_prefill(b, pool, i32(slots), workspace=K.linear_workspace(b) if workspace else None)
+        return b.o, pool.data
+    for step in (False, True):
+        tensor = dt == "bf16" and dv >= 64 and not step
+        ref = linear_ref.linear(f64(q[:last]), f64(k[:last]), f64(v[:last]), f64(g[:last]), [0, 930, last],
+                                f64(first), [3, 1], 1.0, dt, tensor)
+        want, states = call([0, 930, last], [3, 1], step)
+        for t in (q, k, v, g):
+            t[last:] = float("nan")
+        got, states_2 = call([0, 930, last], [3, 1], step)
+        assert torch.equal(got, want) and torch.equal(states, states_2) and got[:last].isfinite().all()
+        assert (got[last:] == got.new_tensor(MARK)).all() and torch.equal(states[[0, 2, 4]], first[[0, 2, 4]])
+        got, states_2 = call([0, 930, last, last, last], [3, 1, 0, 4], step)
+        assert (got[last:] == got.new_tensor(MARK)).all() and torch.equal(states_2[[0, 2, 4]], first[[0, 2, 4]])
+        within(got[:last], ref[0][:last], ref[1][:last], "o")
+        within(states_2, ref[2], ref[3], "states")
+        for t in (q, k, v, g):
+            t[last:] = 0.0
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured calls of different batches, one workspace, replayed in turn and beside
+    an eager call of a third."""
+    rng = np.random.default_rng(39)
+    H, d = 8, 64
+    batches = []
+    for lens in ([1500], [700, 60, 900], [2500, 3]):
+        n = sum(lens)
+        q, k, v = (rows(rng, n, (H, d), "bf16") for _ in range(3))
+        g = torch.from_numpy(decays(rng, n, H, "mild")).float().cuda()
+        b = K.LinearBatch(q, k, v, g, i32(cumulate(lens)))
+        batches.append((b, K.StatePool.zeros(len(lens), H, d), i32(np.arange(len(lens)))))
+    size = max(K.linear_workspace(b).numel() for b, _, _ in batches)
+    work, want = torch.empty(size, dtype=torch.uint8, device="cuda"), []
+
+    def call(i):
+        b, pool, slots = batches[i]
+        pool.data.zero_()
+        K.kda_linear_prefill(b, pool, slots, workspace=work)
+    for i, (b, pool, _) in enumerate(batches):
+        call(i)
+        want.append((b.o.clone(), pool.data.clone()))
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            call(i)
+    for order in ((0, 2, 1), (1, 0, 2), (1, 2, 0)):
+        for b, pool, _ in batches:
+            b.o.zero_()
+            pool.data.fill_(7.0)
+        for i in order:
+            graphs[i].replay() if i < 2 else call(2)
+        for (b, pool, _), (o, states) in zip(batches, want):
+            assert torch.equal(b.o, o) and torch.equal(pool.data, states)
+
+
 def test_a_nan_reaches_what_follows_it():
     """A decay that is NaN: the tokens from it on, and the state."""
     rng = np.random.default_rng(37)
