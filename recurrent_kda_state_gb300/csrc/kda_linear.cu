@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(128) linear_walk_kernel(const LinearParams p) 
   }
   int first = 0, end = s.len;  // the block's tokens
   if (KIND != kStep && loc.parts > 1) {
-    const long long part = (long long)p.chunk * p.part_chunks, skew = p0 & (p.chunk - 1);
+    const long long part = (long long)p.part_chunks << p.chunk_log2, skew = p0 & ((1 << p.chunk_log2) - 1);
     first = (int)max(0LL, loc.part * part - skew);
     end = (int)min((long long)s.len, (loc.part + 1) * part - skew);
   }

@@ -20,10 +20,10 @@ struct LinearParams {
   float *pool;
   int vec;  // q, k, v rows start on 16 bytes
   int o_vec;  // rows of o do
-  // Prompts that are split: tokens of a chunk (a power of two) and chunks of a part
+  // Prompts that are split: tokens of a chunk (their log2) and chunks of a part
   // (0: segments are whole), parts that the grid and the workspace hold, each part's decay and
   // its state, first what it adds and then the one before it.
-  int chunk, part_chunks, max_parts;
+  int chunk_log2, part_chunks, max_parts;
   int max_cut;         // the most parts that are not their segment's last
   float2 *part_decay;  // [max_parts][H]
   float *part_state;   // [max_parts][H][d_v * d_k]
@@ -63,7 +63,8 @@ constexpr long long kMostFixed = 1LL << 60;  // of a part's sum, which is held w
 __device__ __forceinline__ int segment_parts(const LinearParams &p, int i) {
   const int b = p.seg.cu[i], e = p.seg.cu[i + 1], p0 = p.seg.start_pos ? p.seg.start_pos[i] : 0;
   if (b < 0 || e <= b || e > p.seg.N || p0 < 0) return 0;
-  const int chunks = (int)(((p0 & (p.chunk - 1)) + (long long)(e - b) + p.chunk - 1) / p.chunk);
+  const int size = 1 << p.chunk_log2;
+  const int chunks = (int)(((p0 & (size - 1)) + (long long)(e - b) + size - 1) >> p.chunk_log2);
   return 2LL * chunks <= 3LL * p.part_chunks ? 1 : (chunks + p.part_chunks - 1) / p.part_chunks;
 }
 // Segments that no part stands for, reported by one block.
@@ -131,10 +132,13 @@ struct GateParams {
 
 // The states before the parts of every cut segment, in the place of what the parts
 // add: a thread follows four states of one head, F::plain of them in the pool, for
-// every gridDim.y-th of the cut segments.
+// every gridDim.y-th of the cut segments.  Bound by the latency of kAhead parts' loads
+// in turn; four of them and 64 registers, so that 152 SMs hold the machine's blocks at
+// once (eight and 102 registers: four prompts of 4096 tokens, 64 heads of 128 x 64, 136
+// us in all, 128 so; one of 8192, 32 heads of 128 x 128, 127 and 125).
 template <typename F>
-__global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p) {
-  constexpr int kAhead = 8;
+__global__ void __launch_bounds__(256, 4) linear_join_kernel(const LinearParams p) {
+  constexpr int kAhead = 4;
   begin_after_stream();
   const int state4 = p.DK * p.DV / 4, idx = blockIdx.x * 256 + threadIdx.x, h = idx / state4, e = idx % state4;
   const int lane = threadIdx.x & 31;
@@ -162,18 +166,16 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p) 
         float4 add[kAhead];
         float2 a[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-          if (q + u + 1 < parts) {
-            add[u] = at[(q + u) * step];
-            a[u] = decay[(long long)(q + u) * p.H];
-          }
+        for (int u = 0; u < kAhead; ++u) {
+          const int r = min(q + u, parts - 2);
+          add[u] = at[r * step];
+          a[u] = decay[(long long)r * p.H];
+        }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          if (q + u >= parts) break;
-          at[(q + u) * step] = S;
-          if (q + u + 1 < parts)
-            S = make_float4(decayed(S.x, a[u], add[u].x), decayed(S.y, a[u], add[u].y),
-                            decayed(S.z, a[u], add[u].z), decayed(S.w, a[u], add[u].w));
+          if (q + u < parts) at[(q + u) * step] = S;
+          S = make_float4(decayed(S.x, a[u], add[u].x), decayed(S.y, a[u], add[u].y), decayed(S.z, a[u], add[u].z),
+                          decayed(S.w, a[u], add[u].w));
         }
       }
       __syncwarp();

@@ -81,7 +81,7 @@ int linear_impl(const kda_linear_tokens *t, kda_state_pool *pool, const int32_t 
   p.vec = aligned(t->q, 16) && aligned(t->k, 16) && aligned(t->v, 16) && p.qs % 16 == 0 &&
           p.ks % 16 == 0 && p.vs % 16 == 0;
   p.o_vec = aligned(t->o, 16) && p.os % 16 == 0;
-  p.chunk = cut.chunk;
+  p.chunk_log2 = cut.chunk == 64 ? 6 : 4;
   p.part_chunks = part;
   p.max_parts = parts;
   p.max_cut = part ? linear_max_cut(t->num_tokens, t->num_seqs, part, cut) : 0;
@@ -121,7 +121,7 @@ constexpr int kMaxSplitSeqs = 1024;
 // joined.  Whole, the longest segment counts, whose length is on the device alone: for
 // lengths cut at random it is 1 + 1/2 + .. + 1/B times the mean (four prompts of 4096
 // tokens in all, 64 heads of 128 x 64, the longest 1469, 1505, 2172, 3031: whole 88, 93,
-// 126, 167 us, in parts 138, 127, 122, 109; one of 4096 alone, 32 heads of 128 x 128, 262
+// 126, 167 us, in parts 129, 113, 112, 104; one of 4096 alone, 32 heads of 128 x 128, 262
 // and 70).  More than kMaxSplitSeqs segments fill the machine alone, and searching them
 // costs more.
 int linear_part_chunks(int N, int B, const LinearCut &c) {

@@ -22,8 +22,8 @@
 // takes 64 cycles, and as long with 64 rows; reading both operands from shared
 // memory is the limit for 128 x 64 x 16 (48 cycles, 32 with one of them in TMEM).
 //
-// 8192 tokens, 32 heads of 128 x 128, in 9 parts: 42 us for what they add, 11 to join,
-// 82 for the outputs, where the bytes of both passes take 63 at the copy bandwidth.  No
+// 8192 tokens, 32 heads of 128 x 128, in 9 parts, 125 us: 42 for what they add, the rest
+// to join them and 81 for the outputs, where the bytes of both passes take 63 at the copy bandwidth.  No
 // unit is busy (tensor pipe 28 %, DRAM 40 %): a chunk is a chain of products, conversions
 // and barriers, and two blocks do not fill its gaps.
 #include "kda_linear.cuh"
@@ -250,7 +250,6 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Lay::TSLOT);
   const Rows<DK, kThreads> kr(tid);
   const Rows<DV, kThreads> vr(tid);
-  const Rows<kOfV ? DV : DK, kThreads> xr(tid);
 
   constexpr int kLoadWarp = 7;
   int asked = -1;  // by the load warp
@@ -339,12 +338,16 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
         kr.clear(sm + kt, 8192, n);
         vr.clear(sm + vt, 8192, n);
       }
+      auto split = [&](const auto &r, uint32_t tile) {
 #pragma unroll
-      for (int e = 0; e < xr.kLoads; ++e) {
-        const uint32_t off = xr.place(e, 8192);
-        unsigned char *x = sm + (kOfV ? vt : kt) + off;
-        split3(x, x, sm + Lay::MID + off, sm + Lay::LO + off, w[(it & 1) * 64 + xr.row_of(e)]);
-      }
+        for (int e = 0; e < r.kLoads; ++e) {
+          const uint32_t off = r.place(e, 8192);
+          unsigned char *x = sm + tile + off;
+          split3(x, x, sm + Lay::MID + off, sm + Lay::LO + off, w[(it & 1) * 64 + r.row_of(e)]);
+        }
+      };
+      if constexpr (kOfV) split(vr, vt);
+      else split(kr, kt);
     }
     if (!(ok = tiles_ready(ok))) break;
     if (warp == 3 && umma::elect_one()) {
@@ -381,11 +384,11 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
       for (int f = 0; f < NS / 4; ++f)
         dst[F::at(warp, lane, f)] = make_float4(U[4 * f], U[4 * f + 1], U[4 * f + 2], U[4 * f + 3]);
     }
-    if (tid == 0) {
+    if (warp == 0 && lane == 0) {
       const float2 a = decay_pair(unfixed(later) * kLn2);
       p.part_decay[at] = make_float2(a.x + nan, a.y);
     }
-  } else if (tid == 0) {
+  } else if (warp == 0 && lane == 0) {
     set_error(p.seg.err, KDA_DERR_TIMEOUT);
     // one more bounded chance for the tensor cores before TMEM is freed
     const int last = min(it, nq) - 1;
@@ -447,11 +450,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int quad = warp & 3, half = warp >> 2, skew = p0 & 63;
   const int chunks = (int)((skew + (long long)s.len + 63) >> 6);
-  int q0 = 0, q1 = chunks;
-  if (p.part_chunks) {
-    q0 = loc.part * p.part_chunks;
-    if (loc.parts > 1) q1 = min(chunks, q0 + p.part_chunks);
-  }
+  const int q0 = loc.part * p.part_chunks, q1 = loc.part + 1 == loc.parts ? chunks : q0 + p.part_chunks;
   const uint32_t sb = umma::smem_u32(sm);
   float *G = reinterpret_cast<float *>(sm + Lay::G);  // -G_j: 64 hi, 64 lo
   float *eg = reinterpret_cast<float *>(sm + Lay::EG);
@@ -535,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
   load_qk(q0);
   load_v(q0);
   if (warp == 1) umma::tmem_alloc(tslot, 256);
-  const int row = F::row(warp, lane), col = F::col(warp);
+  const int col = F::col(warp);
   f2 S[NS / 2];
   // A state's rows of 32 floats between memory (lines of 128 bytes, four an
   // instruction) and registers (a row a lane).
@@ -824,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
       if (issued[3] >= 0 && !umma::mbar_wait(full + 2, issued[3] & 1, kDrainWaitPolls))
         set_error(p.seg.err, KDA_DERR_UNSAFE);
     }
-  } else if (loc.part + 1 == loc.parts) {
+  } else if (q1 == chunks) {
     store(s.slot);
   }
   umma::fence_before_sync();
@@ -854,8 +853,9 @@ cudaError_t linear_tc(const LinearParams &p, cudaStream_t s) {
   if (!p.part_chunks)
     return launch_after(out_kernel<DK, DV>, dim3(p.seg.B * p.H), dim3(kThreads), out_bytes, s, p, maps);
   if ((e = allow(sum_kernel<DK, DV>, sum_bytes)) != cudaSuccess) return e;
-  if ((e = launch_after(sum_kernel<DK, DV>, dim3(p.max_cut * p.H), dim3(kThreads), sum_bytes, s, p, maps)) != cudaSuccess) return e;
-  if ((e = launch_linear_join<Frag<DK, DV>>(p, s)) != cudaSuccess) return e;
+  e = launch_after(sum_kernel<DK, DV>, dim3(p.max_cut * p.H), dim3(kThreads), sum_bytes, s, p, maps);
+  if (e == cudaSuccess) e = launch_linear_join<Frag<DK, DV>>(p, s);
+  if (e != cudaSuccess) return e;
   return launch_after(out_kernel<DK, DV>, dim3(p.max_parts * p.H), dim3(kThreads), out_bytes, s, p, maps);
 }
 
