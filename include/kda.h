@@ -624,8 +624,11 @@ typedef struct {
  * slot as it is.  Checkpoints as in kda_prefill_chunked, with ckpt_every a
  * multiple of 64.
  * In bf16 with d_k and d_v of at least 64 the prompt runs in chunks of 64
- * tokens on the tensor cores; there a NaN or an infinity in k or v reaches
- * the outputs of its whole chunk, those of earlier tokens included.
+ * tokens on the tensor cores; there a NaN or an infinity in a value of v
+ * reaches its channel's outputs of the whole chunk, those of earlier tokens
+ * included, and one in k leaves NaN in the state where the definition may
+ * leave an infinity.  Other heads, channels of v and earlier chunks have no
+ * part in it.
  * workspace: kda_linear_workspace_size(...) bytes, 256-byte aligned, owned by
  * the caller and not used by another call until this one completes; with it
  * long segments are split into parts that run at the same time.  NULL: every

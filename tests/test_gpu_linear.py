@@ -455,6 +455,47 @@ def test_a_nan_reaches_what_follows_it():
             assert pool.data[0, 0].isfinite().all() and pool.data[0, 1].isnan().all()
 
 
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("dt,dk,dv", [("bf16", 64, 64), ("bf16", 128, 64), ("bf16", 64, 128), ("f32", 64, 64)])
+def test_where_a_nan_of_q_k_or_v_goes(dt, dk, dv, workspace):
+    """q: its token; k: its head's later tokens; v: its channel's later tokens, and on
+    the tensor cores those of its chunk of 64."""
+    rng = np.random.default_rng(40)
+    H, n, at = 3, 500, 300
+    tc = dt == "bf16"
+    base = [rows(rng, n, (H, dk), dt), rows(rng, n, (H, dk), dt, std=dk ** -0.5), rows(rng, n, (H, dv), dt)]
+    g = torch.full((n, H), -0.1, device="cuda")
+
+    def call(which, bad):
+        x = [t.clone() for t in base]
+        if which is not None:
+            x[which][at, 1, 5] = bad
+        b = K.LinearBatch(*x, g, i32([0, n]))
+        pool = K.StatePool.zeros(1, H, dk, d_v=dv)
+        K.kda_linear_prefill(b, pool, i32([0]), workspace=K.linear_workspace(b) if workspace else None)
+        return b.o, pool.data[0]
+    clean, state = call(None, 0.0)
+    for bad in (float("nan"), float("inf")):
+        for which in range(3):
+            o, s = call(which, bad)
+            touched = torch.zeros(n, H, dv, dtype=torch.bool, device="cuda")
+            states = torch.zeros(H, dv, dk, dtype=torch.bool, device="cuda")
+            if which == 0:
+                touched[at, 1] = True
+            elif which == 1:
+                touched[at:, 1] = True
+                states[1, :, 5] = True
+            else:
+                touched[at // 64 * 64 if tc else at:, 1, 5] = True
+                states[1, 5] = True
+            assert torch.equal(o[~touched], clean[~touched]) and torch.equal(s[~states], state[~states])
+            assert not s[states].isfinite().any()
+            if which == 2 or bad != bad:
+                hit = touched.clone()
+                hit[:at] = False
+                assert not o[hit].isfinite().any()
+
+
 # ------------------------------------------------------------- head norms
 def qk_case(seed, dt, n, hq, hk, d, norm="rms", rot=0, interleaved=False, view=0, weights=True,
             scale=0.3, in_place=False, span=50):
