@@ -624,7 +624,9 @@ typedef struct {
  * slot as it is.  Checkpoints as in kda_prefill_chunked, with ckpt_every a
  * multiple of 64.
  * In bf16 with d_k and d_v of at least 64 the prompt runs in chunks of 64
- * tokens on the tensor cores; there a NaN or an infinity in a value of v
+ * tokens on the tensor cores.  There the outputs take the state, and the decayed
+ * products of q and k, as two bf16 each: off by 2^-16 of a term at most, beside
+ * the outputs' own rounding; the stored states are fp32 throughout.  There a NaN or an infinity in a value of v
  * reaches its channel's outputs of the whole chunk, those of earlier tokens
  * included, and one in k leaves NaN in the state where the definition may
  * leave an infinity.  Other heads, channels of v and earlier chunks have no

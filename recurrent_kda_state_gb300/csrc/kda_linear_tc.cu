@@ -14,16 +14,17 @@
 // the other is exact.  The tensor cores' sums lose up to a unit in each of their steps,
 // always downwards, so theirs are no longer than a chunk (12 steps: states 3.5e-7 off
 // in all, where a part in one accumulator was 2.6e-6); chunks are added in registers.
-// The masked Q K^T is split into two (2^-17).  The state enters Q S as bf16: an error
-// of 2^-8 of its products, as the rounding of the outputs has.
+// The masked Q K^T and the state of Q S are split into two each: 8 bits of 24 cut off,
+// the next 16 rounded to 8, so that their products are off by 2^-16 at most.
 //
 // One block of 256 threads walks the chunks of a part, two blocks an SM, so that
 // one's products run beside the other's conversions.  An MMA of 128 x 128 x 16
 // takes 64 cycles, and as long with 64 rows; reading both operands from shared
 // memory is the limit for 128 x 64 x 16 (48 cycles, 32 with one of them in TMEM).
 //
-// 8192 tokens, 32 heads of 128 x 128, in 9 parts, 125 us: 42 for what they add, the rest
-// to join them and 81 for the outputs, where the bytes of both passes take 63 at the copy bandwidth.  No
+// 8192 tokens, 32 heads of 128 x 128, in 9 parts, 134 us (125 with the state of Q S as
+// one bf16, 2^-8 of its products off): 42 for what they add, the rest to join them and 90
+// for the outputs, where the bytes of both passes take 63 at the copy bandwidth.  No
 // unit is busy (tensor pipe 28 %, DRAM 40 %): a chunk is a chain of products, conversions
 // and barriers, and two blocks do not fill its gaps.
 #include "kda_linear.cuh"
@@ -33,9 +34,12 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-// TMEM columns: outputs [d_v][token], the state in bf16 [d_v][d_k / 2], and U
-// [d_v][d_k], before which Q K^T [token][token] has its place.
+// TMEM columns: outputs [d_v][token], the state in bf16 [d_v][d_k / 2], its first 8
+// bits and then its next 8, and U [d_v][d_k], before which Q K^T [token][token] has its
+// place, and with d_k = 128 the state's second bits.
 constexpr uint32_t kAccO = 0, kState = 64, kAccU = 128;
+template <int DK>
+constexpr uint32_t kState2 = DK == 64 ? kState + 32 : kAccU + 64;
 
 __device__ __forceinline__ uint64_t dadd(uint64_t d, uint32_t off) { return d + (off >> 4); }
 
@@ -592,12 +596,26 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = *tslot, tl = tmem + ((uint32_t)(quad * 32) << 16);
-  auto tile = [&]() {  // the state in bf16
+  auto tile = [&]() {  // the state in bf16, in two
     if (!F::any(warp)) return;
-    uint32_t b[NS / 2];
 #pragma unroll
-    for (int e = 0; e < NS / 2; ++e) b[e] = round2(S[e]);
-    umma::tmem_st(tl + kState + col / 2, b);
+    for (int e = 0; e < NS / 2; e += 16) {
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        f2 x = S[e + i];
+        hi[i] = peel(x);
+        lo[i] = round2(x);
+      }
+      umma::tmem_st(tl + kState + col / 2 + e, hi);
+      umma::tmem_st(tl + kState2<DK> + col / 2 + e, lo);
+    }
+  };
+  // The two warps of a quarter of the lanes meet.
+  auto meet = [&]() {
+    umma::fence_before_sync();
+    asm volatile("bar.sync %0, 64;" ::"r"(3 + quad) : "memory");
+    umma::fence_after_sync();
   };
   tile();
   bool ok = true;
@@ -619,9 +637,13 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
       }
       umma::commit(bar);
 #pragma unroll
-      for (int kk = 0; kk < DK / 16; ++kk)
-        umma::mma_bf16_ts(tmem + kAccO, tmem + kState + kk * 8, dadd(dq, (kk >> 2) * 16384 + (kk & 3) * 32),
-                          umma::idesc_bf16(128, 64), (uint32_t)kk);
+      for (int part = 0; part < 2; ++part) {
+#pragma unroll
+        for (int kk = 0; kk < DK / 16; ++kk)
+          umma::mma_bf16_ts(tmem + kAccO, tmem + (part ? kState2<DK> : kState) + kk * 8,
+                            dadd(dq, (kk >> 2) * 16384 + (kk & 3) * 32), umma::idesc_bf16(128, 64),
+                            (uint32_t)(part | kk));
+      }
       umma::commit(bar + 1);
       issued[0] = q - q0;
     }
@@ -795,6 +817,10 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
             S[(e + x) / 2] = fma2(S[(e + x) / 2], ah, fma2(S[(e + x) / 2], al, pack2(u[x], u[x + 1])));
         }
       }
+    }
+    // the state's second bits go where the other warp of these lanes reads U
+    if (DK == 128) meet();
+    if (ok) {
       tile();
       if (p.seg.ckpt_slots) {  // positions fit 32 bits without a sign
         const unsigned every = p.seg.ckpt_every, pos = p0 + (c.begin - s.begin) + c.n;
