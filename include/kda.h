@@ -626,11 +626,10 @@ typedef struct {
  * In bf16 with d_k and d_v of at least 64 the prompt runs in chunks of 64
  * tokens on the tensor cores.  There the outputs take the state, and the decayed
  * products of q and k, as two bf16 each: off by 2^-16 of a term at most, beside
- * the outputs' own rounding; the stored states are fp32 throughout.  There a NaN or an infinity in a value of v
- * reaches its channel's outputs of the whole chunk, those of earlier tokens
- * included, and one in k leaves NaN in the state where the definition may
- * leave an infinity.  Other heads, channels of v and earlier chunks have no
- * part in it.
+ * the outputs' own rounding; the stored states are fp32 throughout.  An infinity
+ * may count as a NaN there: a value of v that is either leaves NaN in its
+ * channel's outputs from its token on and in its channel of the state, one in q
+ * or k reaches the outputs and the state that it enters, and nothing before.
  * workspace: kda_linear_workspace_size(...) bytes, 256-byte aligned, owned by
  * the caller and not used by another call until this one completes; with it
  * long segments are split into parts that run at the same time.  NULL: every

@@ -22,8 +22,12 @@
 // takes 64 cycles, and as long with 64 rows; reading both operands from shared
 // memory is the limit for 128 x 64 x 16 (48 cycles, 32 with one of them in TMEM).
 //
-// 8192 tokens, 32 heads of 128 x 128, in 9 parts, 134 us (125 with the state of Q S as
-// one bf16, 2^-8 of its products off): 42 for what they add, the rest to join them and 90
+// A value of v that is not finite would make NaN of the earlier tokens' outputs too, by
+// the zeros of the mask: it is dropped from the tile (each value is looked at once, which
+// takes 3 us of 8192 tokens) and its channel's outputs and state are made NaN afterwards.
+//
+// 8192 tokens, 32 heads of 128 x 128, in 9 parts, 137 us (125 with the state of Q S as
+// one bf16, 2^-8 of its products off, and v unchecked): 42 for what they add, the rest to join them and 90
 // for the outputs, where the bytes of both passes take 63 at the copy bandwidth.  No
 // unit is busy (tensor pipe 28 %, DRAM 40 %): a chunk is a chain of products, conversions
 // and barriers, and two blocks do not fill its gaps.
@@ -139,9 +143,8 @@ __device__ __forceinline__ uint32_t peel(f2 &x) {
 }
 
 // Eight keys or values times w, in three bf16 parts, which hold its 24 bits.
-__device__ __forceinline__ void split3(const unsigned char *from, unsigned char *hi, unsigned char *mid,
-                                       unsigned char *lo, float w) {
-  const uint4 k = *reinterpret_cast<const uint4 *>(from);
+__device__ __forceinline__ void split3(const uint4 &k, unsigned char *hi, unsigned char *mid, unsigned char *lo,
+                                       float w) {
   const uint32_t in[4] = {k.x, k.y, k.z, k.w};
   uint32_t h[4], m[4], l[4];
 #pragma unroll
@@ -156,6 +159,22 @@ __device__ __forceinline__ void split3(const unsigned char *from, unsigned char 
   *reinterpret_cast<uint4 *>(mid) = make_uint4(m[0], m[1], m[2], m[3]);
   *reinterpret_cast<uint4 *>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
 }
+
+// Whether any of the bf16 values taken in is a NaN or an infinity, whose product with 0
+// is a NaN: one instruction for two of them.
+struct AllFinite {
+  __nv_bfloat162 sum = __bfloat162bfloat162(__ushort_as_bfloat16(0));
+  __device__ __forceinline__ void take(const uint4 &x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const __nv_bfloat162 zero = __bfloat162bfloat162(__ushort_as_bfloat16(0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), zero, sum);
+  }
+  __device__ __forceinline__ bool failed() const {
+    return (*reinterpret_cast<const uint32_t *>(&sum) & 0x7fff7fffu) != 0;
+  }
+};
+__device__ __forceinline__ bool finite(unsigned short bf16) { return (bf16 & 0x7f80) != 0x7f80; }
 
 // Which takes the decays e^{G_C - G_j} and is split, keys or values: the narrower
 // (64 heads of 128 x 64, 4096 tokens: 117 us with the keys, 112 with the values).
@@ -347,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
         for (int e = 0; e < r.kLoads; ++e) {
           const uint32_t off = r.place(e, 8192);
           unsigned char *x = sm + tile + off;
-          split3(x, x, sm + Lay::MID + off, sm + Lay::LO + off, w[(it & 1) * 64 + r.row_of(e)]);
+          split3(*reinterpret_cast<const uint4 *>(x), x, sm + Lay::MID + off, sm + Lay::LO + off,
+                 w[(it & 1) * 64 + r.row_of(e)]);
         }
       };
       if constexpr (kOfV) split(vr, vt);
@@ -462,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
   uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Lay::MBAR);  // Q K^T, Q S, P V, U
   uint64_t *full = bar + 4;                                      // q and k (two stages), v
   uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Lay::TSLOT);
+  int *bad_v = reinterpret_cast<int *>(sm + Lay::TSLOT + 4);  // the last chunk with such a value in v
   const bool tokens = quad < 2;                        // the warps of the tokens' rows
   const int t2 = ((quad & 1) + 2 * half) * 32 + lane;  // thread among the others
   const Rows<DK, 128> kr(t2);
@@ -531,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
     if (umma::elect_one()) {
       for (int i = 0; i < 7; ++i) umma::mbar_init(bar + i, 1);
       for (int i = 0; i < 4; ++i) issued[i] = -1;
+      *bad_v = -1;
       umma::fence_smem_to_async();
     }
     __syncwarp();
@@ -617,6 +639,9 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
     asm volatile("bar.sync %0, 64;" ::"r"(3 + quad) : "memory");
     umma::fence_after_sync();
   };
+  auto bad_at = [&](int token, int channel) {
+    return !finite(row_at(static_cast<const unsigned short *>(p.v), token, p.vs)[h * DV + channel]);
+  };
   tile();
   bool ok = true;
   for (int q = q0; q < q1; ++q) {
@@ -655,12 +680,26 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
     using Split = Rows<kOfV ? DV : DK, 128>;
     constexpr uint32_t kBlock = kOfV ? 8192 : 16384;
     unsigned char *x = sm + (kOfV ? Lay::V : qk + 8192);
-    auto split = [&](const Split &r, int e) {
+    auto split = [&](const Split &r, int e, AllFinite &check) {
       const int j = r.row_of(e);
       const uint32_t at = r.place(e, 8192);
       unsigned char *in = x + r.place(e, kBlock), *m = sm + Lay::MID + at;
-      split3(in, kOfV ? sm + Lay::HI + at : in, m, m + Lay::kPart,
+      const uint4 v = *reinterpret_cast<const uint4 *>(in);
+      if (kOfV) check.take(v);
+      split3(v, kOfV ? sm + Lay::HI + at : in, m, m + Lay::kPart,
              ex2f((G[j] - G[63]) + (G[64 + j] - G[127])));
+    };
+    // P V would multiply a NaN or an infinity of v with the zeros of earlier tokens too:
+    // such a value leaves the tile, and NaN is put where it belongs afterwards.
+    auto drop = [&](const Rows<DV, 128> &r, int from, int to) {
+#pragma unroll 1
+      for (int e = from; e < to; ++e) {
+        unsigned short *v = reinterpret_cast<unsigned short *>(sm + Lay::V + r.place(e, 8192));
+#pragma unroll 1
+        for (int u = 0; u < 8; ++u)
+          if (!finite(v[u])) v[u] = 0;
+      }
+      *bad_v = q - q0;
     };
     if (!tokens && ok) {
       const Split r(t2);
@@ -668,8 +707,10 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
         r.clear(x, kBlock, c.n, r.kLoads - 1);
         if (kOfV) kr.clear(sm + qk + 8192, 16384, c.n);
       }
+      AllFinite check;
 #pragma unroll 2
-      for (int e = 0; e < r.kLoads - 1; ++e) split(r, e);
+      for (int e = 0; e < r.kLoads - 1; ++e) split(r, e, check);
+      if (kOfV && check.failed()) drop(vr, 0, vr.kLoads - 1);
     }
     if (warp == kDecayWarp && ok) {
 #pragma unroll 1
@@ -677,7 +718,9 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
         const Split r(32 * e + lane);
         const int last = r.kLoads - 1;
         if (r.row_of(last) >= c.n) *reinterpret_cast<uint4 *>(x + r.place(last, kBlock)) = make_uint4(0, 0, 0, 0);
-        split(r, last);
+        AllFinite check;
+        split(r, last, check);
+        if (kOfV && check.failed()) drop(Rows<DV, 128>(32 * e + lane), last, last + 1);
       }
     }
     ok = warp_wait(bar + 1, par, p.spin_limit) && ok;
@@ -730,7 +773,14 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
     }
     if (!kOfV && !tokens) {  // v of this chunk
       if (p.vec) ok = warp_wait(full + 2, par, p.spin_limit) && ok;
-      if (ok && c.n < 64) vr.clear(sm + Lay::V, 8192, c.n);
+      if (ok) {
+        if (c.n < 64) vr.clear(sm + Lay::V, 8192, c.n);
+        AllFinite check;
+#pragma unroll
+        for (int e = 0; e < vr.kLoads; ++e)
+          check.take(*reinterpret_cast<const uint4 *>(sm + Lay::V + vr.place(e, 8192)));
+        if (check.failed()) drop(vr, 0, vr.kLoads);
+      }
     }
     if (!(ok = tiles_ready(ok))) break;
     if (warp == 3 && umma::elect_one()) {
@@ -785,22 +835,41 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
       constexpr int kLanes = DV / 8, kStep = 128 / kLanes;  // threads of a row, rows at a time
       const int t = quad * 32 + lane, at = t % kLanes * 8;
       int i = t / kLanes;
-      __nv_bfloat16 *o =
-          row_at(static_cast<__nv_bfloat16 *>(p.o), c.begin + 32 * half + i, p.os) + h * DV + at;
-#pragma unroll
-      for (int e = 0; e < 32 / kStep; ++e) {
-        if (32 * half + i < c.n) {
-          const __nv_bfloat16 *from =
-              reinterpret_cast<const __nv_bfloat16 *>(stage + i * (DV * 2) + ((t % kLanes ^ (i & 7)) << 4));
-          if (p.o_vec) {
-            *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(from);
-          } else {
+      auto row = [&](int r) {
+        return row_at(static_cast<__nv_bfloat16 *>(p.o), c.begin + 32 * half + r, p.os) + h * DV + at;
+      };
+      auto staged = [&](int r) {
+        return reinterpret_cast<const __nv_bfloat16 *>(stage + r * (DV * 2) + ((t % kLanes ^ (r & 7)) << 4));
+      };
+      if (*bad_v == q - q0) {  // NaN from the first such value of a channel on
+        unsigned hit = 0;
+        int j = 0;
 #pragma unroll 1
-            for (int u = 0; u < 8; ++u) o[u] = from[u];
-          }
+        for (; i < 32 && 32 * half + i < c.n; i += kStep) {
+#pragma unroll 1
+          for (; j <= 32 * half + i; ++j)
+#pragma unroll 1
+            for (int u = 0; u < 8; ++u)
+              if (bad_at(c.begin + j, at + u)) hit |= 1u << u;
+#pragma unroll 1
+          for (int u = 0; u < 8; ++u) row(i)[u] = hit >> u & 1 ? __ushort_as_bfloat16(0x7fff) : staged(i)[u];
         }
-        i += kStep;
-        o = row_at(o, kStep, p.os);
+      } else {
+        __nv_bfloat16 *o = row(i);
+#pragma unroll
+        for (int e = 0; e < 32 / kStep; ++e) {
+          if (32 * half + i < c.n) {
+            const __nv_bfloat16 *from = staged(i);
+            if (p.o_vec) {
+              *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(from);
+            } else {
+#pragma unroll 1
+              for (int u = 0; u < 8; ++u) o[u] = from[u];
+            }
+          }
+          i += kStep;
+          o = row_at(o, kStep, p.os);
+        }
       }
     }
     ok = warp_wait(bar + 3, par, p.spin_limit) && ok;
@@ -815,6 +884,15 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
 #pragma unroll
           for (int x = 0; x < 16; x += 2)
             S[(e + x) / 2] = fma2(S[(e + x) / 2], ah, fma2(S[(e + x) / 2], al, pack2(u[x], u[x + 1])));
+        }
+        if (!kOfV && *bad_v == q - q0) {  // V~ keeps such values, V has lost them
+          bool hit = false;
+#pragma unroll 1
+          for (int j = 0; j < c.n; ++j) hit = hit || bad_at(c.begin + j, F::row(warp, lane));
+          if (hit) {
+#pragma unroll
+            for (int e = 0; e < NS / 2; ++e) S[e] = both(__int_as_float(0x7fffffff));
+          }
         }
       }
     }
