@@ -621,8 +621,8 @@ typedef struct {
  *     o = scale * S^T q                               (post-update state)
  * States, sums and decays are fp32.  g <= 0 as a rule; g = -inf forgets the
  * state.  The slot receives the last state; a segment of no tokens leaves its
- * slot as it is.  Checkpoints as in kda_prefill_chunked, with ckpt_every a
- * multiple of 64.
+ * slot as it is, which has to be one of the pool all the same.  Checkpoints as
+ * in kda_prefill_chunked, with ckpt_every a multiple of 64.
  * In bf16 with d_k and d_v of at least 64 the prompt runs in chunks of 64
  * tokens on the tensor cores.  There the outputs take the state, and the decayed
  * products of q and k, as two bf16 each: off by 2^-16 of a term at most, beside

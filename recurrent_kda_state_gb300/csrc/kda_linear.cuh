@@ -67,11 +67,12 @@ __device__ __forceinline__ int segment_parts(const LinearParams &p, int i) {
   const int chunks = (int)(((p0 & (size - 1)) + (long long)(e - b) + size - 1) >> p.chunk_log2);
   return 2LL * chunks <= 3LL * p.part_chunks ? 1 : (chunks + p.part_chunks - 1) / p.part_chunks;
 }
-// Segments that no part stands for, reported by one block.
+// Table entries of segments that no part stands for, reported by one block: as a
+// block of its own would, where segments are whole.
 __device__ __forceinline__ void report_segments(const LinearParams &p) {
   for (int i = threadIdx.x; i < p.seg.B; i += blockDim.x) {
-    const int b = p.seg.cu[i], e = p.seg.cu[i + 1];
-    if (b < 0 || e < b || e > p.seg.N || (p.seg.start_pos && p.seg.start_pos[i] < 0))
+    SegLoc s;
+    if (locate_segment(p.seg, i, &s) && s.len > 0 && p.seg.start_pos && p.seg.start_pos[i] < 0)
       set_error(p.seg.err, KDA_DERR_SEGMENT);
   }
 }
