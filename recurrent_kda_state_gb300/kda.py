@@ -194,9 +194,21 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_ready = False  # the first call goes through torch, which sets CUDA up
 
 
-def _stream(stream):
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _stream(stream, dev=-1):
+    """The stream's handle (None: the current one's) for a call on tensors of GPU dev:
+    its kernels run on the current device, which has to be that one, as has the
+    stream's.  dev -1: a call without tensors on a GPU."""
     global _raw_ready
+    if dev >= 0 and _current_device() != dev:
+        raise ValueError("the tensors are on GPU %d, the current device is GPU %d"
+                         % (dev, _current_device()))
     if stream is not None:
+        if dev >= 0 and stream.device_index != dev:
+            raise ValueError("the tensors are on GPU %d, the stream is of GPU %d"
+                             % (dev, stream.device_index))
         return stream.cuda_stream
     if _raw_ready:
         return _raw_stream(torch._C._cuda_getDevice())
@@ -293,7 +305,7 @@ def kda_prefill_chunked(tok, pool, state_slots, chunk, ckpt_every=0,
         ctypes.byref(tok.c), ctypes.byref(pool.c), _ptr(state_slots),
         _ptr(ckpt_slots), max_ckpt, ckpt_every, chunk, _ptr(start_pos),
         _ptr(workspace), 0 if workspace is None else workspace.numel(),
-        _stream(stream)), name)
+        _stream(stream, pool.dev)), name)
     return workspace
 
 
@@ -308,7 +320,7 @@ def kda_prefill_chunked_noalloc(tok, pool, state_slots, chunk, ckpt_every=0,
     _check(lib().kda_prefill_chunked_noalloc(
         ctypes.byref(tok.c), ctypes.byref(pool.c), _ptr(state_slots),
         _ptr(ckpt_slots), max_ckpt, ckpt_every, chunk, _ptr(start_pos),
-        _stream(stream)), "kda_prefill_chunked_noalloc")
+        _stream(stream, pool.dev)), "kda_prefill_chunked_noalloc")
 
 
 def kda_verify(tok, max_T, pool, state_slots, ring, is_spec=None, stream=None,
@@ -318,7 +330,7 @@ def kda_verify(tok, max_T, pool, state_slots, ring, is_spec=None, stream=None,
     fn, name = ((lib().kda_verify_raw, "kda_verify_raw") if raw
                 else (lib().kda_verify, "kda_verify"))
     _check(fn(ctypes.byref(tok.c), max_T, ctypes.byref(pool.c), _ptr(state_slots),
-              ctypes.byref(ring.c), _ptr(is_spec), _stream(stream)), name)
+              ctypes.byref(ring.c), _ptr(is_spec), _stream(stream, pool.dev)), name)
 
 
 def kda_forward_mixed(tok, num_prefill, prefill_tokens, pool, state_slots, chunk,
@@ -337,13 +349,13 @@ def kda_forward_mixed(tok, num_prefill, prefill_tokens, pool, state_slots, chunk
                                             chunk, tok.c.dtype)
         if nbytes > 0:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=tok.k.device)
-    side = None if side_stream is None else ctypes.c_void_p(side_stream.cuda_stream)
+    side = None if side_stream is None else ctypes.c_void_p(_stream(side_stream, pool.dev))
     _check(lib().kda_forward_mixed(
         ctypes.byref(tok.c), num_prefill, prefill_tokens, ctypes.byref(pool.c),
         _ptr(state_slots), _ptr(ckpt_slots), max_ckpt, ckpt_every, chunk,
         _ptr(start_pos), _ptr(workspace),
         0 if workspace is None else workspace.numel(), max_T,
-        ctypes.byref(ring.c), _ptr(is_spec), _stream(stream), side),
+        ctypes.byref(ring.c), _ptr(is_spec), _stream(stream, pool.dev), side),
         "kda_forward_mixed")
     return workspace
 
@@ -351,7 +363,7 @@ def kda_forward_mixed(tok, num_prefill, prefill_tokens, pool, state_slots, chunk
 def kda_commit(accepted_len, state_slots, pool, ring, stream=None):
     _check(lib().kda_commit(_ptr(accepted_len), _ptr(state_slots),
                             state_slots.numel(), ctypes.byref(pool.c),
-                            ctypes.byref(ring.c), _stream(stream)), "kda_commit")
+                            ctypes.byref(ring.c), _stream(stream, pool.dev)), "kda_commit")
 
 
 def kda_commit_layers(accepted_len, state_slots, pool, rings, stream=None):
@@ -359,19 +371,19 @@ def kda_commit_layers(accepted_len, state_slots, pool, rings, stream=None):
     arr = (kda_replay_ring * len(rings))(*[r.c for r in rings])
     _check(lib().kda_commit_layers(_ptr(accepted_len), _ptr(state_slots),
                                    state_slots.numel(), ctypes.byref(pool.c),
-                                   arr, len(rings), _stream(stream)),
+                                   arr, len(rings), _stream(stream, pool.dev)),
            "kda_commit_layers")
 
 
 def kda_materialize(state_slots, pool, ring, stream=None):
     _check(lib().kda_materialize(_ptr(state_slots), state_slots.numel(),
                                  ctypes.byref(pool.c), ctypes.byref(ring.c),
-                                 _stream(stream)), "kda_materialize")
+                                 _stream(stream, pool.dev)), "kda_materialize")
 
 
 def kda_ring_reset(slots, pool, ring, stream=None):
     _check(lib().kda_ring_reset(_ptr(slots), slots.numel(), ctypes.byref(pool.c),
-                                ctypes.byref(ring.c), _stream(stream)),
+                                ctypes.byref(ring.c), _stream(stream, pool.dev)),
            "kda_ring_reset")
 
 
@@ -381,14 +393,14 @@ def kda_gather_states(pool, slots, out=None, stream=None):
         out = torch.empty(slots.numel(), H, dv, dk, dtype=torch.float32,
                           device=pool.data.device)
     _check(lib().kda_gather_states(ctypes.byref(pool.c), _ptr(slots),
-                                   slots.numel(), _ptr(out), _stream(stream)),
+                                   slots.numel(), _ptr(out), _stream(stream, pool.dev)),
            "kda_gather_states")
     return out
 
 
 def kda_copy_slots(pool, src, dst, stream=None):
     _check(lib().kda_copy_slots(ctypes.byref(pool.c), _ptr(src), _ptr(dst),
-                                src.numel(), _stream(stream)), "kda_copy_slots")
+                                src.numel(), _stream(stream, pool.dev)), "kda_copy_slots")
 
 
 def snapshot_buffer(num_seqs, max_T, pool):
@@ -402,7 +414,7 @@ def snapshot_buffer(num_seqs, max_T, pool):
 def kda_verify_snapshot(tok, max_T, pool, state_slots, snapshots, stream=None):
     _check(lib().kda_verify_snapshot(ctypes.byref(tok.c), max_T,
                                      ctypes.byref(pool.c), _ptr(state_slots),
-                                     _ptr(snapshots), _stream(stream)),
+                                     _ptr(snapshots), _stream(stream, pool.dev)),
            "kda_verify_snapshot")
 
 
@@ -410,7 +422,7 @@ def kda_commit_snapshot(accepted_len, state_slots, pool, snapshots, stream=None)
     _check(lib().kda_commit_snapshot(_ptr(accepted_len), _ptr(state_slots),
                                      state_slots.numel(), ctypes.byref(pool.c),
                                      _ptr(snapshots), int(snapshots.shape[1]),
-                                     _stream(stream)), "kda_commit_snapshot")
+                                     _stream(stream, pool.dev)), "kda_commit_snapshot")
 
 
 def _row_view(t, dt, what):
@@ -586,7 +598,7 @@ def kda_conv_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, star
     ckpt, max_ckpt = _ckpt(ckpt_slots, B, dev)
     _check(lib().kda_conv_prefill(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev), ckpt, max_ckpt, ckpt_every,
-        _table(start_pos, B, "start_pos", dev), _stream(stream)), "kda_conv_prefill")
+        _table(start_pos, B, "start_pos", dev), _stream(stream, dev)), "kda_conv_prefill")
 
 
 def kda_conv_step(tok, pool, state_slots, commit_len=None, stream=None):
@@ -595,7 +607,8 @@ def kda_conv_step(tok, pool, state_slots, commit_len=None, stream=None):
     B, dev = tok.num_seqs, _call_device(tok, pool)
     st = (_lib or lib()).kda_conv_step(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev),
-        None if commit_len is None else _table(commit_len, B, "commit_len", dev), _stream(stream))
+        None if commit_len is None else _table(commit_len, B, "commit_len", dev),
+        _stream(stream, dev))
     if st:
         _check(st, "kda_conv_step")
 
@@ -623,7 +636,7 @@ def kda_scan_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, star
     ws, size = _workspace(workspace, dev)
     _check(lib().kda_scan_prefill(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev), ckpt, max_ckpt, ckpt_every,
-        _table(start_pos, B, "start_pos", dev), ws, size, _stream(stream)), "kda_scan_prefill")
+        _table(start_pos, B, "start_pos", dev), ws, size, _stream(stream, dev)), "kda_scan_prefill")
 
 
 def kda_scan_step(tok, pool, state_slots, commit_len=None, stream=None):
@@ -631,7 +644,8 @@ def kda_scan_step(tok, pool, state_slots, commit_len=None, stream=None):
     B, dev = tok.num_seqs, _call_device(tok, pool)
     st = (_lib or lib()).kda_scan_step(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev),
-        None if commit_len is None else _table(commit_len, B, "commit_len", dev), _stream(stream))
+        None if commit_len is None else _table(commit_len, B, "commit_len", dev),
+        _stream(stream, dev))
     if st:
         _check(st, "kda_scan_step")
 
@@ -694,7 +708,8 @@ def kda_linear_prefill(tok, pool, state_slots, ckpt_every=0, ckpt_slots=None, st
     ws, size = _workspace(workspace, dev)
     _check(lib().kda_linear_prefill(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev), ckpt, max_ckpt, ckpt_every,
-        _table(start_pos, B, "start_pos", dev), ws, size, _stream(stream)), "kda_linear_prefill")
+        _table(start_pos, B, "start_pos", dev), ws, size, _stream(stream, dev)),
+        "kda_linear_prefill")
 
 
 def kda_linear_step(tok, pool, state_slots, commit_len=None, stream=None):
@@ -702,7 +717,8 @@ def kda_linear_step(tok, pool, state_slots, commit_len=None, stream=None):
     B, dev = tok.num_seqs, _call_device(tok, pool)
     st = (_lib or lib()).kda_linear_step(
         tok.ref, pool.ref, _table(state_slots, B, "state_slots", dev),
-        None if commit_len is None else _table(commit_len, B, "commit_len", dev), _stream(stream))
+        None if commit_len is None else _table(commit_len, B, "commit_len", dev),
+        _stream(stream, dev))
     if st:
         _check(st, "kda_linear_step")
 
@@ -766,7 +782,7 @@ def _on_gpu(tok):
 def kda_qk_norm(tok, stream=None):
     """Norm, rotation and scale of queries and keys: into tok.q_out, tok.k_out."""
     _on_gpu(tok)
-    st = (_lib or lib()).kda_qk_norm(tok.ref, _stream(stream))
+    st = (_lib or lib()).kda_qk_norm(tok.ref, _stream(stream, tok.dev))
     if st:
         _check(st, "kda_qk_norm")
 
@@ -801,7 +817,7 @@ class GateBatch:
 def kda_gated_norm(tok, stream=None):
     """Norm of each head's outputs times the gate's activation: into tok.y."""
     _on_gpu(tok)
-    st = (_lib or lib()).kda_gated_norm(tok.ref, _stream(stream))
+    st = (_lib or lib()).kda_gated_norm(tok.ref, _stream(stream, tok.dev))
     if st:
         _check(st, "kda_gated_norm")
 
@@ -842,7 +858,7 @@ def kda_move_slots(arrays, src, dst, workspace=None, stream=None):
     ws, size = _workspace(workspace, dev)
     st = (_lib or lib()).kda_move_slots(
         arrays.c, len(arrays.tensors), arrays.num_slots, _table(src, n, "src", dev),
-        _table(dst, n, "dst", dev), n, ws, size, _stream(stream))
+        _table(dst, n, "dst", dev), n, ws, size, _stream(stream, dev))
     if st:
         _check(st, "kda_move_slots")
 
