@@ -11,9 +11,11 @@
 // Precision.  Decays are summed in fixed point and kept as hi + lo, so that a token
 // that forgets everything costs the later ones nothing.  K~ (or V, where it is
 // narrower, with the same weights) is split into three bf16, which hold 24 bits, and
-// the other is exact.  The tensor cores' sums lose up to a unit in each of their steps,
-// always downwards, so theirs are no longer than a chunk (12 steps: states 3.5e-7 off
-// in all, where a part in one accumulator was 2.6e-6); chunks are added in registers.
+// the other is exact.  The tensor cores cut what they add in a step of 16 products, always
+// downwards, a little behind the last bit of the largest, so the small parts come first,
+// and sums are no longer than a chunk (12 steps; a part in one accumulator left states
+// 2.6e-6 off); chunks are added in registers.  Keys and values of one sign, 2000 tokens:
+// states 1.6e-6 off with the large parts first.
 // The masked Q K^T and the state of Q S are split into two each: 8 bits of 24 cut off,
 // the next 16 rounded to 8, so that their products are off by 2^-16 at most.
 //
@@ -377,13 +379,14 @@ __global__ void __launch_bounds__(kThreads, 2) sum_kernel(const LinearParams p, 
     if (warp == 3 && umma::elect_one()) {
       const uint32_t id = umma::idesc_bf16_abmn(128, DK);
 #pragma unroll
-      for (int part = 0; part < 3; ++part) {
+      for (int part = 2; part >= 0; --part) {
         const uint32_t its = part == 1 ? Lay::MID : Lay::LO;
         const uint64_t dk = umma::sdesc_sw128_mn(sb + (part == 0 || kOfV ? kt : its), 8192);
         const uint64_t dv = umma::sdesc_sw128_mn(sb + (part == 0 || !kOfV ? vt : its), DV == 128 ? 8192 : 0);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma::mma_bf16(tmem + (it & 1) * 128, dadd(dv, kk * 2048), dadd(dk, kk * 2048), id, (uint32_t)(part | kk));
+          umma::mma_bf16(tmem + (it & 1) * 128, dadd(dv, kk * 2048), dadd(dk, kk * 2048), id,
+                         (uint32_t)(part < 2 || kk > 0));
       }
       umma::commit(mbar);
     }
@@ -662,12 +665,12 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
       }
       umma::commit(bar);
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
+      for (int part = 1; part >= 0; --part) {
 #pragma unroll
         for (int kk = 0; kk < DK / 16; ++kk)
           umma::mma_bf16_ts(tmem + kAccO, tmem + (part ? kState2<DK> : kState) + kk * 8,
                             dadd(dq, (kk >> 2) * 16384 + (kk & 3) * 32), umma::idesc_bf16(128, 64),
-                            (uint32_t)(part | kk));
+                            (uint32_t)(part < 1 || kk > 0));
       }
       umma::commit(bar + 1);
       issued[0] = q - q0;
@@ -786,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
     if (warp == 3 && umma::elect_one()) {
       const uint64_t dv = umma::sdesc_sw128_mn(sb + Lay::V, DV == 128 ? 8192 : 0);
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
+      for (int part = 1; part >= 0; --part) {
         const uint64_t dp = umma::sdesc_sw128(sb + (part ? pl : qk));
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
@@ -798,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
       }
       umma::commit(bar + 2);
 #pragma unroll
-      for (int part = 0; part < 3; ++part) {
+      for (int part = 2; part >= 0; --part) {
         const uint32_t its = part == 0 ? Lay::HI : part == 1 ? Lay::MID : Lay::LO;
         const uint64_t dk = kOfV || part == 0 ? umma::sdesc_sw128_mn(sb + qk + 8192, 16384)
                                               : umma::sdesc_sw128_mn(sb + its, 8192);
@@ -806,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 2) out_kernel(const LinearParams p, 
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma::mma_bf16(tmem + kAccU, dadd(dw, kk * 2048), dadd(dk, kk * 2048),
-                         umma::idesc_bf16_abmn(128, DK), (uint32_t)(part | kk));
+                         umma::idesc_bf16_abmn(128, DK), (uint32_t)(part < 2 || kk > 0));
       }
       umma::commit(bar + 3);
       issued[1] = q - q0;
