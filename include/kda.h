@@ -626,14 +626,17 @@ typedef struct {
  * In bf16 with d_k and d_v of at least 64 the prompt runs in chunks of 64
  * tokens on the tensor cores.  There the outputs take the state, and the decayed
  * products of q and k, as two bf16 each: off by 2^-16 of a term at most, beside
- * the outputs' own rounding; the stored states are fp32 throughout.  An infinity
- * may count as a NaN there: a value of v that is either leaves NaN in its
- * channel's outputs from its token on and in its channel of the state, one in q
- * or k reaches the outputs and the state that it enters, and nothing before.
+ * the outputs' own rounding; the stored states are fp32 throughout.
+ * A NaN, or an infinity but g = -inf, reaches its own token and later ones, never
+ * earlier ones: one of v its channel's outputs and state, one of q its token's
+ * outputs, one of k or g its head's (of k: that key of the state).  An infinity may
+ * count as a NaN on the way.
  * workspace: kda_linear_workspace_size(...) bytes, 256-byte aligned, owned by
  * the caller and not used by another call until this one completes; with it
  * long segments are split into parts that run at the same time.  NULL: every
- * segment is walked by itself.  Both meet the same tolerances; they are not
+ * segment is walked by itself, the faster way for a few prompts of like lengths
+ * whose heads give every SM a block or more (the lengths are on the device, so
+ * the call does not know).  Both meet the same tolerances; they are not
  * bit-identical to each other.
  */
 int kda_linear_prefill(const kda_linear_tokens *tok, kda_state_pool *pool,
@@ -718,7 +721,8 @@ typedef struct {
 /*
  * kda_gated_norm -- y = x / sqrt(mean(x^2) + eps) * weight * act(gate), the
  * mean over the channels of a head: the way from a KDA or linear attention
- * layer to the output projection.  Sums and products in fp32, rounded once.
+ * layer to the output projection.  Sums and products in fp32, rounded once; the
+ * sigmoid of a gate u is off by up to 0.62 |u| + 4 units of fp32's last place.
  * y may be the gate itself, or x where it has y's dtype (the same pointer and
  * stride); otherwise it overlaps no input.
  */

@@ -220,7 +220,7 @@ __device__ __forceinline__ const float *table_row(const QkParams &p, int pos, bo
   return nullptr;
 }
 
-// 1 / (1 + e^-v).  log2(e) v is rounded before ex2: up to |v| / 2 ulp.
+// 1 / (1 + e^-v).  log2(e) and its product with v are rounded before ex2: up to 0.62 |v| ulp.
 __device__ __forceinline__ float sigmoid(float v) { return rcpf(1.0f + ex2f(-kLog2e * v)); }
 __device__ __forceinline__ f2 sigmoid(f2 v) {
   const float2 d = unpack2(add2(exp2_2(mul2(v, both(-kLog2e))), both(1.0f)));

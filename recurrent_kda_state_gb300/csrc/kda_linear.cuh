@@ -59,7 +59,7 @@ constexpr long long kMostFixed = 1LL << 60;  // of a part's sum, which is held w
 // Parts of segment i, 0 for one without tokens or with a bad table entry.  What a cut
 // saves has to pay for going over its first part twice: a segment of up to 3/2 of a
 // part stays whole (lengths 3000, 500, 300 and 296, 64 heads of 128 x 64, parts of 41
-// chunks: 209 us when it was cut, 168 so).
+// chunks, the state of Q S as one bf16: 209 us when it was cut, 168 so).
 __device__ __forceinline__ int segment_parts(const LinearParams &p, int i) {
   const int b = p.seg.cu[i], e = p.seg.cu[i + 1], p0 = p.seg.start_pos ? p.seg.start_pos[i] : 0;
   if (b < 0 || e <= b || e > p.seg.N || p0 < 0) return 0;
@@ -134,9 +134,10 @@ struct GateParams {
 // The states before the parts of every cut segment, in the place of what the parts
 // add: a thread follows four states of one head, F::plain of them in the pool, for
 // every gridDim.y-th of the cut segments.  Bound by the latency of kAhead parts' loads
-// in turn; four of them and 64 registers, so that 152 SMs hold the machine's blocks at
-// once (eight and 102 registers: four prompts of 4096 tokens, 64 heads of 128 x 64, 136
-// us in all, 128 so; one of 8192, 32 heads of 128 x 128, 127 and 125).
+// in turn; four of them and 64 registers, so that an SM holds four blocks and the 512 of
+// one cut segment run at once, three rows of them in two to three turns (eight and 102
+// registers: four prompts of 4096 tokens, 64 heads of 128 x 64, 136 us in all, 128 so; one
+// of 8192, 32 heads of 128 x 128, 127 and 125, with the state of Q S as one bf16).
 template <typename F>
 __global__ void __launch_bounds__(256, 4) linear_join_kernel(const LinearParams p) {
   constexpr int kAhead = 4;
@@ -187,7 +188,8 @@ __global__ void __launch_bounds__(256, 4) linear_join_kernel(const LinearParams 
 template <typename F>
 cudaError_t launch_linear_join(const LinearParams &p, cudaStream_t s) {
   const long long blocks = ((long long)p.H * p.DK * p.DV / 4 + 255) / 256;
-  const long long rows = 152 * 8 / blocks + 1;  // the machine once, if segments are cut
+  // more rows than are resident at once: several cut segments' loads beside one another
+  const long long rows = 152 * 8 / blocks + 1;
   return launch_after(linear_join_kernel<F>, dim3((unsigned)blocks, p.seg.B < rows ? p.seg.B : (int)rows), dim3(256),
                       0, s, p);
 }

@@ -120,9 +120,9 @@ constexpr int kMaxSplitSeqs = 1024;
 // as one; those that are not a segment's last are gone over before, at kSum a chunk, and
 // joined.  Whole, the longest segment counts, whose length is on the device alone: for
 // lengths cut at random it is 1 + 1/2 + .. + 1/B times the mean (four prompts of 4096
-// tokens in all, 64 heads of 128 x 64, the longest 1469, 1505, 2172, 3031: whole 88, 93,
-// 126, 167 us, in parts 129, 113, 112, 104; one of 4096 alone, 32 heads of 128 x 128, 262
-// and 70).  More than kMaxSplitSeqs segments fill the machine alone, and searching them
+// tokens in all, 64 heads of 128 x 64, the longest 1469, 1505, 2172, 3031: whole 100, 106,
+// 143, 190 us, in parts 143, 126, 127, 115; one of 4096 alone, 32 heads of 128 x 128, 273
+// and 86).  More than kMaxSplitSeqs segments fill the machine alone, and searching them
 // costs more.
 int linear_part_chunks(int N, int B, const LinearCut &c) {
   if (B > kMaxSplitSeqs || B < 1 || N <= c.chunk * c.least) return 0;
@@ -149,8 +149,8 @@ int linear_part_chunks(int N, int B, const LinearCut &c) {
   }
   // Better whole: but in a large batch a segment that is far longer than expected is
   // cut, which costs 6 to 10 us for two nearly empty launches where there is none (37
-  // prompts of 16384 tokens, the longest 985 to 1519: 201 to 233 us whole, 210 to 241
-  // so; with one of 5000: 326 and 283, of 8000: 493 and 284).
+  // prompts of 16384 tokens, the longest 985 to 1519: 229 to 260 us whole, 238 to 270
+  // so; with one of 5000: 364 and 303, of 8000: 551 and 302).
   if (!best && B > 1 && even >= kLarge) best = (int)(1.2 * std::fmax(longest, even) + 4 * of_64);
   return (long long)best * c.chunk < N ? best : 0;
 }

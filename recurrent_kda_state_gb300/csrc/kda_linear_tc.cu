@@ -28,11 +28,11 @@
 // the zeros of the mask: it is dropped from the tile (each value is looked at once, which
 // takes 3 us of 8192 tokens) and its channel's outputs and state are made NaN afterwards.
 //
-// 8192 tokens, 32 heads of 128 x 128, in 9 parts, 137 us (125 with the state of Q S as
-// one bf16, 2^-8 of its products off, and v unchecked): 42 for what they add, the rest to join them and 90
-// for the outputs, where the bytes of both passes take 63 at the copy bandwidth.  No
-// unit is busy (tensor pipe 28 %, DRAM 40 %): a chunk is a chain of products, conversions
-// and barriers, and two blocks do not fill its gaps.
+// 8192 tokens, 32 heads of 128 x 128, in 9 parts, 138 us (125 with the state of Q S as
+// one bf16, 2^-8 of its products off, and v unchecked): 42 for what they add, 95 for the
+// outputs and the rest to join them, where the bytes of both passes take 63 at the copy
+// bandwidth.  No unit is busy (tensor pipe 28 %, DRAM 35 %): a chunk is a chain of
+// products, conversions and barriers, and two blocks do not fill its gaps.
 #include "kda_linear.cuh"
 #include "kda_tma.cuh"
 
@@ -179,7 +179,8 @@ struct AllFinite {
 __device__ __forceinline__ bool finite(unsigned short bf16) { return (bf16 & 0x7f80) != 0x7f80; }
 
 // Which takes the decays e^{G_C - G_j} and is split, keys or values: the narrower
-// (64 heads of 128 x 64, 4096 tokens: 117 us with the keys, 112 with the values).
+// (64 heads of 128 x 64, 4096 tokens, the state of Q S as one bf16: 117 us with the keys,
+// 112 with the values).
 template <int DK, int DV>
 constexpr bool kOfValues = DV < DK;
 

@@ -693,7 +693,8 @@ def kda_linear_workspace_size(num_tokens, num_seqs, H, d_k, d_v, dtype):
 
 def linear_workspace(tok):
     """A workspace tensor for kda_linear_prefill of this batch and of smaller ones
-    (None: not needed)."""
+    (None: not needed).  A few prompts of like lengths whose heads fill the GPU are
+    faster without one."""
     c = tok.c
     n = kda_linear_workspace_size(c.num_tokens, c.num_seqs, c.num_heads, c.d_k, c.d_v, c.dtype)
     return torch.empty(n, dtype=torch.uint8, device=tok.q.device) if n else None
